@@ -22,6 +22,9 @@ __all__ = [
     "w4_fp8_quantize_rows", "w4_fp8_gemm", "w4_int8_quantize_rows", "w4_int8_gemm",
     "W4Format", "w4_zeros_bytes", "w4_quantize_fmt", "w4_prepared_bytes_fmt", "w4_prepare_fmt",
     "w4_unprepare_fmt", "w4_gemv_fmt",
+    "w4_rmsnorm", "w4_rmsnorm_fp8", "w4_rmsnorm_int8", "w4_silu_mul", "w4_silu_mul_fp8", "w4_silu_mul_int8",
+    "W4KVCache", "W4Rope", "w4_rope_frequencies", "w4_rope_cache", "w4_block_tables",
+    "w4_paged_attention", "w4_paged_attention_workspace_bytes",
     "W4_OK", "W4_F32", "W4_BF16", "GROUP",
 ]
 
@@ -37,6 +40,9 @@ GEMM_NOALLOC_MAX_WORKSPACE = 16 << 20
 STATUS_NONFINITE = 1
 STATUS_SCALE_OVERFLOW = 2
 STATUS_SCALE_ZERO = 4
+STATUS_PAGE = 8
+STATUS_LENGTH = 16
+STATUS_PAGES_SHORT = 32
 
 _lib = None
 
@@ -50,6 +56,29 @@ class W4Format(ctypes.Structure):
     @classmethod
     def make(cls, group=128, scale_bf16=False, zero_bits=8, symmetric=False):
         return cls(int(group), int(bool(scale_bf16)), int(zero_bits), int(bool(symmetric)))
+
+
+class _KVCacheStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("type", ctypes.c_int32)]
+
+
+class W4Rope(ctypes.Structure):
+    """w4_rope: how positions turn the pairs of a head (see w4_rope_frequencies)."""
+
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double), ("original_positions", ctypes.c_int64)]
+    SCALINGS = ("none", "linear", "bands", "ramp")
+
+    @classmethod
+    def make(cls, rotary_dim, base=10000.0, interleaved=False, scaling="none", factor=1.0, low=1.0, high=4.0,
+             original_positions=1):
+        if scaling not in cls.SCALINGS:
+            raise ValueError(f"scaling must be one of {cls.SCALINGS}")
+        return cls(int(rotary_dim), int(bool(interleaved)), cls.SCALINGS.index(scaling), 0, float(base),
+                   float(factor), float(low), float(high), int(original_positions))
 
 
 class W4Error(RuntimeError):
@@ -121,6 +150,21 @@ def lib() -> ctypes.CDLL:
     L.w4_unprepare_fmt.restype = i32
     L.w4_gemv_fmt.argtypes = [vp, i64, i64, fp, vp, i32, i64, vp, i32, vp]
     L.w4_gemv_fmt.restype = i32
+    f32 = ctypes.c_float
+    cp, rp = ctypes.POINTER(_KVCacheStruct), ctypes.POINTER(W4Rope)
+    norm = [vp, i32, vp, vp, i32, vp, i32, f32, i64, i64]
+    gate = [vp, i32, i64, i64]
+    L.w4_rmsnorm.argtypes = norm + [vp, i32, vp]
+    L.w4_silu_mul.argtypes = gate + [vp, i32, vp]
+    for kind in ("fp8", "int8"):
+        getattr(L, f"w4_rmsnorm_{kind}").argtypes = norm + [vp, vp, vp, vp]
+        getattr(L, f"w4_silu_mul_{kind}").argtypes = gate + [vp, vp, vp, vp]
+    L.w4_rope_frequencies.argtypes = [rp, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_double)]
+    L.w4_rope_cache.argtypes = [vp, i32, i64, i64, cp, vp, vp, rp, vp, vp, vp, vp]
+    L.w4_block_tables.argtypes = [vp, vp, i64, vp, i64, vp, vp, vp, vp, i64, i32, vp, vp, vp, i64, vp, vp]
+    L.w4_paged_attention_workspace_bytes.argtypes = [i64, i64, cp, i64, i64]
+    L.w4_paged_attention_workspace_bytes.restype = sz
+    L.w4_paged_attention.argtypes = [vp, i64, i64, cp, vp, i64, vp, vp, i64, f32, i64, vp, vp, sz, vp, vp]
     del u32
     _lib = L
     return L
@@ -537,3 +581,307 @@ def w4_int8_gemm(xq, sx, wq, sw, Y=None, out_dtype=None):
                               W4_F32 if Y.dtype == torch.float32 else W4_BF16, _stream(xq)),
            "w4_int8_gemm")
     return Y
+
+
+# --------------------------------------------------------------------------
+# Operators between the products of a decoder layer
+# --------------------------------------------------------------------------
+
+def _want(t, dtypes, shape, name, device):
+    """_require, and that the tensor lies on the device of the call."""
+    _require(t, dtypes, shape, name)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _float_code(t):
+    import torch
+    return W4_F32 if t.dtype == torch.float32 else W4_BF16
+
+
+def _opt(t):
+    return None if t is None else t.data_ptr()
+
+
+def _status_ptr(status, device):
+    import torch
+    if status is None:
+        return None
+    _want(status, torch.int32, None, "status", device)
+    if status.numel() < 1:
+        raise ValueError("status must hold one element")
+    return status.data_ptr()
+
+
+def _call(name, device, *args):
+    """Run an entry point on the device of its tensors and that device's current stream."""
+    import torch
+    fn = getattr(lib(), name)
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    _check(status, name)
+
+
+def _rows_of(x, name):
+    import torch
+    _require(x, (torch.float32, torch.bfloat16), None, name)
+    if x.dim() == 1:
+        x = x.unsqueeze(0)
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be [rows, values]")
+    return x
+
+
+def _value_rows(y, out_dtype, shape, device):
+    import torch
+    if y is None:
+        y = torch.empty(shape, dtype=out_dtype or torch.bfloat16, device=device)
+    _want(y, (torch.float32, torch.bfloat16), shape, "y", device)
+    return y
+
+
+def _code_rows(codes, scales, dtype, shape, device):
+    import torch
+    if codes is None:
+        codes = torch.empty(shape, dtype=dtype, device=device)
+    if scales is None:
+        scales = torch.empty(shape[0], dtype=torch.float32, device=device)
+    _want(codes, dtype, shape, "codes", device)
+    _want(scales, torch.float32, shape[:1], "scales", device)
+    return codes, scales
+
+
+def _norm_args(x, weight, eps, residual, residual_out):
+    import torch
+    x = _rows_of(x, "x")
+    rows, k = x.shape
+    _want(weight, (torch.float32, torch.bfloat16), (k,), "weight", x.device)
+    rt = W4_F32
+    if residual is not None:
+        if residual.dim() == 1:
+            residual = residual.unsqueeze(0)
+        _want(residual, (torch.float32, torch.bfloat16), (rows, k), "residual", x.device)
+        if residual_out is None:
+            residual_out = residual
+        if residual_out.dim() == 1:
+            residual_out = residual_out.unsqueeze(0)
+        _want(residual_out, residual.dtype, (rows, k), "residual_out", x.device)
+        rt = _float_code(residual)
+    elif residual_out is not None:
+        raise ValueError("residual_out without residual")
+    return x, (x.data_ptr(), _float_code(x), _opt(residual), _opt(residual_out), rt, weight.data_ptr(),
+               _float_code(weight), eps, rows, k)
+
+
+def w4_rmsnorm(x, weight, eps, residual=None, residual_out=None, y=None, out_dtype=None):
+    """Root-mean-square norm of x [rows, K] (after adding ``residual``, which is updated in place
+    unless ``residual_out`` is given); y [rows, K] bfloat16 by default."""
+    x, args = _norm_args(x, weight, eps, residual, residual_out)
+    y = _value_rows(y, out_dtype, x.shape, x.device)
+    _call("w4_rmsnorm", x.device, *args, y.data_ptr(), _float_code(y))
+    return y
+
+
+def _rmsnorm_codes(name, dtype, x, weight, eps, residual, residual_out, codes, scales, status):
+    x, args = _norm_args(x, weight, eps, residual, residual_out)
+    codes, scales = _code_rows(codes, scales, dtype, x.shape, x.device)
+    _call(name, x.device, *args, codes.data_ptr(), scales.data_ptr(), _status_ptr(status, x.device))
+    return codes, scales
+
+
+def w4_rmsnorm_fp8(x, weight, eps, residual=None, residual_out=None, codes=None, scales=None, status=None):
+    """w4_rmsnorm quantized per row: E4M3 codes [rows, K] uint8 and scales [rows]."""
+    import torch
+    return _rmsnorm_codes("w4_rmsnorm_fp8", torch.uint8, x, weight, eps, residual, residual_out, codes, scales, status)
+
+
+def w4_rmsnorm_int8(x, weight, eps, residual=None, residual_out=None, codes=None, scales=None, status=None):
+    """w4_rmsnorm quantized per row: symmetric INT8 codes [rows, K] and steps [rows]."""
+    import torch
+    return _rmsnorm_codes("w4_rmsnorm_int8", torch.int8, x, weight, eps, residual, residual_out, codes, scales, status)
+
+
+def _gate_args(gate_up):
+    x = _rows_of(gate_up, "gate_up")
+    rows, width = x.shape
+    if width % 2:
+        raise ValueError("gate_up must be [rows, 2F]")
+    return x, (rows, width // 2), (x.data_ptr(), _float_code(x), rows, width // 2)
+
+
+def w4_silu_mul(gate_up, y=None, out_dtype=None):
+    """silu(gate) * up of gate_up [rows, 2F] (gate first); y [rows, F] bfloat16 by default."""
+    x, shape, args = _gate_args(gate_up)
+    y = _value_rows(y, out_dtype, shape, x.device)
+    _call("w4_silu_mul", x.device, *args, y.data_ptr(), _float_code(y))
+    return y
+
+
+def _silu_mul_codes(name, dtype, gate_up, codes, scales, status):
+    x, shape, args = _gate_args(gate_up)
+    codes, scales = _code_rows(codes, scales, dtype, shape, x.device)
+    _call(name, x.device, *args, codes.data_ptr(), scales.data_ptr(), _status_ptr(status, x.device))
+    return codes, scales
+
+
+def w4_silu_mul_fp8(gate_up, codes=None, scales=None, status=None):
+    """w4_silu_mul quantized per row: E4M3 codes [rows, F] uint8 and scales [rows]."""
+    import torch
+    return _silu_mul_codes("w4_silu_mul_fp8", torch.uint8, gate_up, codes, scales, status)
+
+
+def w4_silu_mul_int8(gate_up, codes=None, scales=None, status=None):
+    """w4_silu_mul quantized per row: symmetric INT8 codes [rows, F] and steps [rows]."""
+    import torch
+    return _silu_mul_codes("w4_silu_mul_int8", torch.int8, gate_up, codes, scales, status)
+
+
+class W4KVCache:
+    """A paged cache: k and v [pages, kv_heads, page_size, head_dim], bfloat16, or uint8 (E4M3
+    codes) with float32 scales [pages, kv_heads, page_size].  Keeps its tensors alive."""
+
+    def __init__(self, k, v, k_scales=None, v_scales=None):
+        import torch
+        _require(k, (torch.bfloat16, torch.uint8), None, "k")
+        if k.dim() != 4:
+            raise ValueError("k must be [pages, kv_heads, page_size, head_dim]")
+        _want(v, k.dtype, k.shape, "v", k.device)
+        fp8 = k.dtype == torch.uint8
+        if fp8:
+            _want(k_scales, torch.float32, k.shape[:3], "k_scales", k.device)
+            _want(v_scales, torch.float32, k.shape[:3], "v_scales", k.device)
+        elif k_scales is not None or v_scales is not None:
+            raise ValueError("a bfloat16 cache has no scales")
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        self.pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        self.device = k.device
+        self._c = _KVCacheStruct(k.data_ptr(), v.data_ptr(), _opt(k_scales), _opt(v_scales), self.pages,
+                                 self.page_size, self.kv_heads, self.head_dim, int(fp8))
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, pages, page_size, kv_heads, head_dim, fp8=False, device="cuda"):
+        """A cache of that shape (zeros)."""
+        import torch
+        shape = (pages, kv_heads, page_size, head_dim)
+        kv = [torch.zeros(shape, dtype=torch.uint8 if fp8 else torch.bfloat16, device=device) for _ in range(2)]
+        scales = [torch.ones(shape[:3], dtype=torch.float32, device=device) if fp8 else None for _ in range(2)]
+        return cls(*kv, *scales)
+
+
+def w4_rope_frequencies(rope: W4Rope, device=None):
+    """Angle per position of each pair, and the amplitude: (list of floats, float) on the host, or
+    with a device (float64 tensor [rotary_dim / 2], float)."""
+    n = max(1, int(rope.rotary_dim) // 2)
+    freqs, amplitude = (ctypes.c_double * n)(), ctypes.c_double()
+    _check(lib().w4_rope_frequencies(ctypes.byref(rope), freqs, ctypes.byref(amplitude)), "w4_rope_frequencies")
+    if device is None:
+        return list(freqs), amplitude.value
+    import torch
+    return torch.tensor(list(freqs), dtype=torch.float64, device=device), amplitude.value
+
+
+def w4_rope_cache(qkv, cache: W4KVCache, positions, slots, rope: W4Rope, freqs, q=None, status=None):
+    """Rotate the rows of the fused q|k|v product qkv [T, (heads + 2 kv_heads) * head_dim] and store
+    K and V at ``slots``; returns q [T, heads, head_dim] bfloat16.  ``freqs``: float64 device tensor
+    of w4_rope_frequencies.  Rows with a negative slot are left out (of q too)."""
+    import torch
+    x = _rows_of(qkv, "qkv")
+    dev = x.device
+    T, width = x.shape
+    d = cache.head_dim
+    heads = width // d - 2 * cache.kv_heads
+    if width % d or heads < 1:
+        raise ValueError("qkv must be [T, (heads + 2 kv_heads) * head_dim]")
+    if cache.device != dev:
+        raise ValueError(f"cache is on {cache.device}, expected {dev}")
+    _want(positions, torch.int32, (T,), "positions", dev)
+    _want(slots, torch.int64, (T,), "slots", dev)
+    _want(freqs, torch.float64, (rope.rotary_dim // 2,), "freqs", dev)
+    if q is None:
+        q = torch.empty(T, heads, d, dtype=torch.bfloat16, device=dev)
+    _want(q, torch.bfloat16, (T, heads, d), "q", dev)
+    _call("w4_rope_cache", dev, x.data_ptr(), _float_code(x), T, heads, cache._ref, positions.data_ptr(),
+          slots.data_ptr(), ctypes.byref(rope), freqs.data_ptr(), q.data_ptr(), _status_ptr(status, dev))
+    return q
+
+
+def w4_block_tables(new_lens, lens, free_pages, free_count, block_table, page_size, tokens=None, lens_out=None,
+                    free_count_out=None, cu_q=None, positions=None, slots=None, status=None):
+    """Place the new tokens of a batch in pages; returns (cu_q, positions, slots).
+
+    ``lens`` and ``free_count`` are updated in place unless ``lens_out`` / ``free_count_out`` are
+    given; ``block_table`` is.  ``tokens``: places of positions and slots where those are not given."""
+    import torch
+    i32 = torch.int32
+    _require(new_lens, i32, None, "new_lens")
+    dev = new_lens.device
+    if new_lens.dim() != 1:
+        raise ValueError("new_lens must be [B]")
+    B = new_lens.shape[0]
+    lens_out = lens if lens_out is None else lens_out
+    free_count_out = free_count if free_count_out is None else free_count_out
+    if positions is None or slots is None:
+        if tokens is None:
+            raise ValueError("tokens is needed where positions or slots are not given")
+        positions = torch.empty(tokens, dtype=i32, device=dev) if positions is None else positions
+        slots = torch.empty(tokens, dtype=torch.int64, device=dev) if slots is None else slots
+    if cu_q is None:
+        cu_q = torch.empty(B + 1, dtype=i32, device=dev)
+    _want(lens, i32, (B,), "lens", dev)
+    _want(lens_out, i32, (B,), "lens_out", dev)
+    _want(free_pages, i32, None, "free_pages", dev)
+    _want(free_count, i32, (1,), "free_count", dev)
+    _want(free_count_out, i32, (1,), "free_count_out", dev)
+    _want(block_table, i32, None, "block_table", dev)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, max_pages]")
+    _want(cu_q, i32, (B + 1,), "cu_q", dev)
+    _want(positions, i32, None, "positions", dev)
+    _want(slots, torch.int64, positions.shape, "slots", dev)
+    _call("w4_block_tables", dev, new_lens.data_ptr(), lens.data_ptr(), B, free_pages.data_ptr(),
+          free_pages.numel(), free_count.data_ptr(), lens_out.data_ptr(), free_count_out.data_ptr(),
+          block_table.data_ptr(), block_table.shape[1], page_size, cu_q.data_ptr(), positions.data_ptr(),
+          slots.data_ptr(), positions.numel(), _status_ptr(status, dev))
+    return cu_q, positions, slots
+
+
+def w4_paged_attention_workspace_bytes(T: int, heads: int, cache: W4KVCache, B: int, max_pages: int) -> int:
+    return int(lib().w4_paged_attention_workspace_bytes(T, heads, cache._ref, B, max_pages))
+
+
+def w4_paged_attention(q, cache: W4KVCache, block_table, cu_q, lens, scale, window=0, o=None, workspace=None,
+                       status=None):
+    """Attention of q [T, heads, head_dim] (bfloat16) over the paged cache; returns o like q.
+
+    ``cu_q`` [B + 1] and ``lens`` [B] as w4_block_tables gives them (lens counts the new tokens);
+    rows of q behind cu_q[B] are left out of o.  The workspace is allocated where it is not given."""
+    import torch
+    _require(q, torch.bfloat16, None, "q")
+    dev = q.device
+    if q.dim() != 3 or q.shape[2] != cache.head_dim:
+        raise ValueError("q must be [T, heads, head_dim]")
+    if cache.device != dev:
+        raise ValueError(f"cache is on {cache.device}, expected {dev}")
+    T, heads, _ = q.shape
+    _want(block_table, torch.int32, None, "block_table", dev)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    B, max_pages = block_table.shape
+    _want(cu_q, torch.int32, (B + 1,), "cu_q", dev)
+    _want(lens, torch.int32, (B,), "lens", dev)
+    if o is None:
+        o = torch.empty_like(q)
+    _want(o, torch.bfloat16, q.shape, "o", dev)
+    if workspace is None:
+        need = lib().w4_paged_attention_workspace_bytes(T, heads, cache._ref, B, max_pages)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    else:
+        _want(workspace, torch.uint8, None, "workspace", dev)
+    _call("w4_paged_attention", dev, q.data_ptr(), T, heads, cache._ref, block_table.data_ptr(), max_pages,
+          cu_q.data_ptr(), lens.data_ptr(), B, scale, window, o.data_ptr(), _opt(workspace),
+          0 if workspace is None else workspace.numel(), _status_ptr(status, dev))
+    return o

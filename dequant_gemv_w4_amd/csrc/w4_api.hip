@@ -1,7 +1,8 @@
 // C-ABI entry points of libw4a16: argument validation, device check, launch.
-// The kernels live in w4_quantize.hip, w4_gemv.hip, w4_gemv_mfma.hip, w4_gemm.hip and
-// w4_w8a8.hip.
+// The kernels live in w4_quantize.hip, w4_gemv.hip, w4_gemv_mfma.hip, w4_gemm.hip, w4_w8a8.hip,
+// w4_rows.hip, w4_cache.hip and w4_attention.hip.
 #include <atomic>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 #include <string>
@@ -59,6 +60,77 @@ w4_status to_fmt(const w4_format* in, w4::Fmt* out) {
     return W4_OK;
 }
 
+bool is_dtype(w4_dtype t) { return t == W4_F32 || t == W4_BF16; }
+
+w4_status check_rows(int64_t rows, int64_t k) {
+    if (rows < 1 || rows > (int64_t)INT32_MAX || k < W4_GROUP || k % W4_GROUP != 0 ||
+        k > W4_ROWS_MAX_K)
+        return W4_ERR_SHAPE;
+    return W4_OK;
+}
+
+// Geometry of a paged cache (the pointers apart); *shift is log2(page_size).
+w4_status check_page_size(int32_t page_size, int* shift) {
+    if (page_size < 16 || page_size > 4096 || (page_size & (page_size - 1)) != 0)
+        return W4_ERR_UNSUPPORTED;
+    *shift = __builtin_ctz((unsigned)page_size);
+    return W4_OK;
+}
+
+w4_status check_cache(const w4_kv_cache* c, int* shift) {
+    if (!c) return W4_ERR_NULL;
+    if (c->type != W4_CACHE_BF16 && c->type != W4_CACHE_FP8) return W4_ERR_UNSUPPORTED;
+    if (c->head_dim != 64 && c->head_dim != 128) return W4_ERR_UNSUPPORTED;
+    const w4_status st = check_page_size(c->page_size, shift);
+    if (st != W4_OK) return st;
+    if (c->kv_heads < 1 || c->kv_heads > 1024 || c->pages < 1 || c->pages > (int64_t)INT32_MAX ||
+        c->pages * c->page_size >= ((int64_t)1 << 40) / c->kv_heads)
+        return W4_ERR_SHAPE;
+    return W4_OK;
+}
+
+w4_status check_cache_pointers(const w4_kv_cache* c) {
+    if (!c->k || !c->v) return W4_ERR_NULL;
+    if (c->type == W4_CACHE_FP8 && (!c->k_scales || !c->v_scales)) return W4_ERR_NULL;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scales, 4) ||
+        !aligned(c->v_scales, 4))
+        return W4_ERR_ALIGN;
+    return W4_OK;
+}
+
+w4_status check_heads(int64_t T, int64_t heads, const w4_kv_cache* c) {
+    if (T < 1 || T > W4_MAX_TOKENS || heads < c->kv_heads || heads % c->kv_heads != 0 ||
+        heads >= ((int64_t)1 << 26) / T)
+        return W4_ERR_SHAPE;
+    return W4_OK;
+}
+
+w4_status check_batch(int64_t B, int64_t max_pages, int64_t page_size) {
+    if (B < 1 || B > W4_MAX_SEQUENCES || max_pages < 1 || max_pages > W4_MAX_CONTEXT / page_size)
+        return W4_ERR_SHAPE;
+    return W4_OK;
+}
+
+w4_status check_rope(const w4_rope* r) {
+    if (!r) return W4_ERR_NULL;
+    if (r->scaling < W4_ROPE_NONE || r->scaling > W4_ROPE_RAMP || r->reserved != 0 ||
+        (r->interleaved != 0 && r->interleaved != 1) || r->rotary_dim < 16 ||
+        r->rotary_dim % 16 != 0 || r->rotary_dim > 128)
+        return W4_ERR_UNSUPPORTED;
+    if (!(r->base > 1.0) || !std::isfinite(r->base)) return W4_ERR_VALUE;
+    if (r->scaling == W4_ROPE_NONE) return W4_OK;
+    if (!(r->factor >= 1.0) || !std::isfinite(r->factor)) return W4_ERR_VALUE;
+    if (r->scaling == W4_ROPE_LINEAR) return W4_OK;
+    if (!(r->low > 0.0) || !(r->high > r->low) || !std::isfinite(r->high) ||
+        r->original_positions < 1)
+        return W4_ERR_VALUE;
+    return W4_OK;
+}
+
+double rope_amplitude(const w4_rope* r) {
+    return r->scaling == W4_ROPE_RAMP ? 1.0 + 0.1 * std::log(r->factor) : 1.0;
+}
+
 }  // namespace
 
 // Workspace of w4_gemm_noalloc.  In host code this name is only a stand-in for the
@@ -108,6 +180,7 @@ const char* w4_status_string(w4_status s) {
         case W4_ERR_WORKSPACE: return "workspace missing or too small";
         case W4_ERR_HIP: return "HIP runtime error";
         case W4_ERR_BUFFER: return "destination buffer too small";
+        case W4_ERR_VALUE: return "argument value out of range";
     }
     return "unknown status";
 }
@@ -410,6 +483,281 @@ w4_status w4_int8_gemm(const int8_t* xq, const float* sx, int64_t M, const int8_
     hipError_t e = w4::launch_int8_gemm(reinterpret_cast<const uint8_t*>(xq), sx, M,
                                         reinterpret_cast<const uint8_t*>(wq), sw, N, K, Y,
                                         yt == W4_BF16, stream);
+    return e == hipSuccess ? W4_OK : hip_fail(e);
+}
+
+static w4_status rmsnorm_common(const void* x, w4_dtype xt, const void* residual,
+                                void* residual_out, w4_dtype rt, const void* weight, w4_dtype wt,
+                                float eps, int64_t rows, int64_t K, const w4::RowOut& out,
+                                hipStream_t stream) {
+    const bool codes = out.kind == w4::RowOut::kFp8 || out.kind == w4::RowOut::kInt8;
+    if (!x || !weight || !out.y || (codes && !out.scales) || !residual != !residual_out)
+        return W4_ERR_NULL;
+    if (!is_dtype(xt) || !is_dtype(wt) || (residual && !is_dtype(rt))) return W4_ERR_DTYPE;
+    w4_status st = check_rows(rows, K);
+    if (st != W4_OK) return st;
+    if (!(eps > 0.0f) || !std::isfinite(eps)) return W4_ERR_VALUE;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(residual_out, 16) ||
+        !aligned(weight, 16) || !aligned(out.y, 16) || !aligned(out.scales, 4) ||
+        !aligned(out.status, 4))
+        return W4_ERR_ALIGN;
+    st = check_arch();
+    if (st != W4_OK) return st;
+    w4::RmsnormArgs a;
+    a.x = x;
+    a.r = residual;
+    a.r_out = residual_out;
+    a.w = weight;
+    a.x_f32 = xt == W4_F32;
+    a.r_f32 = rt == W4_F32;
+    a.w_f32 = wt == W4_F32;
+    a.eps = eps;
+    a.rows = rows;
+    a.K = K;
+    const hipError_t e = w4::launch_rmsnorm(a, out, stream);
+    return e == hipSuccess ? W4_OK : hip_fail(e);
+}
+
+w4_status w4_rmsnorm(const void* x, w4_dtype xt, const void* residual, void* residual_out,
+                     w4_dtype rt, const void* weight, w4_dtype wt, float eps, int64_t rows,
+                     int64_t K, void* y, w4_dtype yt, hipStream_t stream) {
+    if (!is_dtype(yt)) return W4_ERR_DTYPE;
+    const w4::RowOut out = {yt == W4_F32 ? w4::RowOut::kF32 : w4::RowOut::kBf16, y, nullptr, nullptr};
+    return rmsnorm_common(x, xt, residual, residual_out, rt, weight, wt, eps, rows, K, out, stream);
+}
+
+w4_status w4_rmsnorm_fp8(const void* x, w4_dtype xt, const void* residual, void* residual_out,
+                         w4_dtype rt, const void* weight, w4_dtype wt, float eps, int64_t rows,
+                         int64_t K, uint8_t* codes, float* scales, uint32_t* d_status,
+                         hipStream_t stream) {
+    const w4::RowOut out = {w4::RowOut::kFp8, codes, scales, d_status};
+    return rmsnorm_common(x, xt, residual, residual_out, rt, weight, wt, eps, rows, K, out, stream);
+}
+
+w4_status w4_rmsnorm_int8(const void* x, w4_dtype xt, const void* residual, void* residual_out,
+                          w4_dtype rt, const void* weight, w4_dtype wt, float eps, int64_t rows,
+                          int64_t K, int8_t* codes, float* scales, uint32_t* d_status,
+                          hipStream_t stream) {
+    const w4::RowOut out = {w4::RowOut::kInt8, codes, scales, d_status};
+    return rmsnorm_common(x, xt, residual, residual_out, rt, weight, wt, eps, rows, K, out, stream);
+}
+
+static w4_status silu_mul_common(const void* gate_up, w4_dtype gt, int64_t rows, int64_t F,
+                                 const w4::RowOut& out, hipStream_t stream) {
+    const bool codes = out.kind == w4::RowOut::kFp8 || out.kind == w4::RowOut::kInt8;
+    if (!gate_up || !out.y || (codes && !out.scales)) return W4_ERR_NULL;
+    if (!is_dtype(gt)) return W4_ERR_DTYPE;
+    w4_status st = check_rows(rows, F);
+    if (st != W4_OK) return st;
+    if (!aligned(gate_up, 16) || !aligned(out.y, 16) || !aligned(out.scales, 4) ||
+        !aligned(out.status, 4))
+        return W4_ERR_ALIGN;
+    st = check_arch();
+    if (st != W4_OK) return st;
+    const hipError_t e = w4::launch_silu_mul(gate_up, gt == W4_F32, rows, F, out, stream);
+    return e == hipSuccess ? W4_OK : hip_fail(e);
+}
+
+w4_status w4_silu_mul(const void* gate_up, w4_dtype gt, int64_t rows, int64_t F, void* y,
+                      w4_dtype yt, hipStream_t stream) {
+    if (!is_dtype(yt)) return W4_ERR_DTYPE;
+    const w4::RowOut out = {yt == W4_F32 ? w4::RowOut::kF32 : w4::RowOut::kBf16, y, nullptr, nullptr};
+    return silu_mul_common(gate_up, gt, rows, F, out, stream);
+}
+
+w4_status w4_silu_mul_fp8(const void* gate_up, w4_dtype gt, int64_t rows, int64_t F,
+                          uint8_t* codes, float* scales, uint32_t* d_status, hipStream_t stream) {
+    const w4::RowOut out = {w4::RowOut::kFp8, codes, scales, d_status};
+    return silu_mul_common(gate_up, gt, rows, F, out, stream);
+}
+
+w4_status w4_silu_mul_int8(const void* gate_up, w4_dtype gt, int64_t rows, int64_t F,
+                           int8_t* codes, float* scales, uint32_t* d_status, hipStream_t stream) {
+    const w4::RowOut out = {w4::RowOut::kInt8, codes, scales, d_status};
+    return silu_mul_common(gate_up, gt, rows, F, out, stream);
+}
+
+w4_status w4_rope_frequencies(const w4_rope* rope, double* freqs, double* amplitude) {
+    if (!freqs) return W4_ERR_NULL;
+    const w4_status st = check_rope(rope);
+    if (st != W4_OK) return st;
+    const int half = rope->rotary_dim / 2;
+    const double two_pi = 6.283185307179586476925;
+    double first = 0.0, last = 0.0;                          // pairs between which the ramp rises
+    if (rope->scaling == W4_ROPE_RAMP) {
+        const auto pair_of = [&](double turns) {
+            return half * std::log((double)rope->original_positions / (two_pi * turns)) /
+                   std::log(rope->base);
+        };
+        first = std::fmax(0.0, std::floor(pair_of(rope->high)));
+        last = std::fmin(2.0 * half - 1.0, std::ceil(pair_of(rope->low)));
+        if (first == last) last += 0.001;
+    }
+    for (int i = 0; i < half; ++i) {
+        double f = std::pow(rope->base, -(double)i / half);
+        switch (rope->scaling) {
+            case W4_ROPE_LINEAR: f /= rope->factor; break;
+            case W4_ROPE_BANDS: {
+                const double turns = (double)rope->original_positions * f / two_pi;
+                const double k = std::fmin(1.0, std::fmax(0.0, (turns - rope->low) / (rope->high - rope->low)));
+                f *= k + (1.0 - k) / rope->factor;
+                break;
+            }
+            case W4_ROPE_RAMP: {
+                const double r = std::fmin(1.0, std::fmax(0.0, (i - first) / (last - first)));
+                f *= 1.0 - r + r / rope->factor;
+                break;
+            }
+            default: break;
+        }
+        freqs[i] = f;
+    }
+    if (amplitude) *amplitude = rope_amplitude(rope);
+    return W4_OK;
+}
+
+w4_status w4_rope_cache(const void* qkv, w4_dtype xt, int64_t T, int64_t heads,
+                        const w4_kv_cache* cache, const int32_t* positions, const int64_t* slots,
+                        const w4_rope* rope, const double* d_freqs, void* q, uint32_t* d_status,
+                        hipStream_t stream) {
+    if (!qkv || !cache || !positions || !slots || !rope || !d_freqs || !q) return W4_ERR_NULL;
+    if (!is_dtype(xt)) return W4_ERR_DTYPE;
+    int shift = 0;
+    w4_status st = check_cache(cache, &shift);
+    if (st == W4_OK) st = check_cache_pointers(cache);
+    if (st == W4_OK) st = check_heads(T, heads, cache);
+    if (st == W4_OK) st = check_rope(rope);
+    if (st != W4_OK) return st;
+    if (rope->rotary_dim > cache->head_dim) return W4_ERR_SHAPE;
+    if (!aligned(qkv, 16) || !aligned(q, 16) || !aligned(positions, 4) || !aligned(slots, 8) ||
+        !aligned(d_freqs, 8) || !aligned(d_status, 4))
+        return W4_ERR_ALIGN;
+    st = check_arch();
+    if (st != W4_OK) return st;
+    w4::RopeArgs a;
+    a.qkv = qkv;
+    a.positions = positions;
+    a.slots = slots;
+    a.freqs = d_freqs;
+    a.q = static_cast<uint16_t*>(q);
+    a.k = cache->k;
+    a.v = cache->v;
+    a.k_scales = cache->k_scales;
+    a.v_scales = cache->v_scales;
+    a.status = d_status;
+    a.T = T;
+    a.pages = cache->pages;
+    a.heads = (int)heads;
+    a.kv_heads = cache->kv_heads;
+    a.head_dim = cache->head_dim;
+    a.page_shift = shift;
+    a.rotary = rope->rotary_dim;
+    a.interleaved = rope->interleaved;
+    a.amplitude = (float)rope_amplitude(rope);
+    const hipError_t e = w4::launch_rope_cache(a, xt == W4_F32, cache->type == W4_CACHE_FP8, stream);
+    return e == hipSuccess ? W4_OK : hip_fail(e);
+}
+
+w4_status w4_block_tables(const int32_t* new_lens, const int32_t* lens_in, int64_t B,
+                          const int32_t* free_pages, int64_t free_capacity,
+                          const int32_t* free_count_in, int32_t* lens_out,
+                          int32_t* free_count_out, int32_t* block_table, int64_t max_pages,
+                          int32_t page_size, int32_t* cu_q, int32_t* positions, int64_t* slots,
+                          int64_t T, uint32_t* d_status, hipStream_t stream) {
+    if (!new_lens || !lens_in || (!free_pages && free_capacity != 0) || !free_count_in ||
+        !lens_out || !free_count_out || !block_table || !cu_q || !positions || !slots)
+        return W4_ERR_NULL;
+    int shift = 0;
+    w4_status st = check_page_size(page_size, &shift);
+    if (st != W4_OK) return st;
+    st = check_batch(B, max_pages, page_size);
+    if (st != W4_OK) return st;
+    if (T < 1 || T > W4_MAX_TOKENS || free_capacity < 0 || free_capacity > (int64_t)INT32_MAX)
+        return W4_ERR_SHAPE;
+    if (!aligned(new_lens, 4) || !aligned(lens_in, 4) || !aligned(free_pages, 4) ||
+        !aligned(free_count_in, 4) || !aligned(lens_out, 4) || !aligned(free_count_out, 4) ||
+        !aligned(block_table, 4) || !aligned(cu_q, 4) || !aligned(positions, 4) ||
+        !aligned(slots, 8) || !aligned(d_status, 4))
+        return W4_ERR_ALIGN;
+    st = check_arch();
+    if (st != W4_OK) return st;
+    w4::TableArgs a;
+    a.new_lens = new_lens;
+    a.lens_in = lens_in;
+    a.free_pages = free_pages;
+    a.count_in = free_count_in;
+    a.lens_out = lens_out;
+    a.count_out = free_count_out;
+    a.table = block_table;
+    a.cu = cu_q;
+    a.positions = positions;
+    a.slots = slots;
+    a.status = d_status;
+    a.free_capacity = free_capacity;
+    a.max_pages = max_pages;
+    a.T = T;
+    a.B = (int)B;
+    a.page_shift = shift;
+    const hipError_t e = w4::launch_block_tables(a, stream);
+    return e == hipSuccess ? W4_OK : hip_fail(e);
+}
+
+size_t w4_paged_attention_workspace_bytes(int64_t T, int64_t heads, const w4_kv_cache* cache,
+                                          int64_t B, int64_t max_pages) {
+    int shift = 0;
+    if (check_cache(cache, &shift) != W4_OK || check_heads(T, heads, cache) != W4_OK ||
+        check_batch(B, max_pages, cache->page_size) != W4_OK)
+        return 0;
+    w4::AttendPlan plan;
+    w4::plan_attend(T, B, heads, cache->kv_heads, max_pages << shift, &plan);
+    return w4::attend_workspace(cache->head_dim, plan);
+}
+
+w4_status w4_paged_attention(const void* q, int64_t T, int64_t heads, const w4_kv_cache* cache,
+                             const int32_t* block_table, int64_t max_pages, const int32_t* cu_q,
+                             const int32_t* lens, int64_t B, float scale, int64_t window, void* o,
+                             void* workspace, size_t workspace_bytes, uint32_t* d_status,
+                             hipStream_t stream) {
+    if (!q || !cache || !block_table || !cu_q || !lens || !o) return W4_ERR_NULL;
+    int shift = 0;
+    w4_status st = check_cache(cache, &shift);
+    if (st == W4_OK) st = check_cache_pointers(cache);
+    if (st == W4_OK) st = check_heads(T, heads, cache);
+    if (st == W4_OK) st = check_batch(B, max_pages, cache->page_size);
+    if (st != W4_OK) return st;
+    if (!(scale > 0.0f) || !std::isfinite(scale) || window < 0) return W4_ERR_VALUE;
+    w4::AttendPlan plan;
+    w4::plan_attend(T, B, heads, cache->kv_heads, max_pages << shift, &plan);
+    const size_t need = w4::attend_workspace(cache->head_dim, plan);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return W4_ERR_WORKSPACE;
+    if (!aligned(q, 16) || !aligned(o, 16) || !aligned(block_table, 4) || !aligned(cu_q, 4) ||
+        !aligned(lens, 4) || !aligned(workspace, 16) || !aligned(d_status, 4))
+        return W4_ERR_ALIGN;
+    st = check_arch();
+    if (st != W4_OK) return st;
+    w4::AttendArgs a = {};
+    a.q = static_cast<const uint16_t*>(q);
+    a.o = static_cast<uint16_t*>(o);
+    a.k = cache->k;
+    a.v = cache->v;
+    a.k_scales = cache->k_scales;
+    a.v_scales = cache->v_scales;
+    a.table = block_table;
+    a.cu = cu_q;
+    a.lens = lens;
+    a.status = d_status;
+    a.T = T;
+    a.pages = cache->pages;
+    a.max_pages = max_pages;
+    a.B = (int)B;
+    a.heads = (int)heads;
+    a.kv_heads = cache->kv_heads;
+    a.group = (int)(heads / cache->kv_heads);
+    a.page_shift = shift;
+    a.window = (int)(window < W4_MAX_CONTEXT ? window : 0);   // wider than any context: none
+    a.scale_log2 = (float)((double)scale * 1.4426950408889634074);
+    const hipError_t e = w4::launch_attend(a, cache->head_dim, cache->type == W4_CACHE_FP8, plan,
+                                           workspace, stream);
     return e == hipSuccess ? W4_OK : hip_fail(e);
 }
 

@@ -1,0 +1,809 @@
+// Attention of new tokens over the paged cache:
+//     o = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale * q.k_j - max),
+// over the keys that a query sees, in one pass with the running maximum and sum of the softmax.
+// The index arithmetic (tiles, parts, pages) is in w4_paging.h.
+//
+// Both kernels multiply on v_mfma_f32_32x32x16_bf16 with the keys as rows and the query rows as
+// columns: S^T = K Q^T leaves each lane one query row (lane % 32) and half of the keys, so the
+// running maximum is one exchange between lane halves, and the same registers, rounded to
+// bfloat16, are the right operand of O^T += V^T P^T without any movement: which key stands at
+// which place of that product's inner dimension is free, and the left operand follows (half h of
+// the lanes holds the keys 4h..4h+3 and 8+4h..8+4h+3 of each 16).  V stays in its row order and
+// is turned by ds_read_b64_tr_b16, which gives a lane four keys of one column.
+//
+// Rounding: scores, maximum, sum and O are binary32.  P is rounded to bfloat16 for the matrix
+// unit (each weight within 2^-8 relative; the same size as the rounding of the bfloat16 output,
+// and averaged over the keys), the sum takes the unrounded P.  E4M3 codes enter as exact bfloat16
+// values; the scale of a key's row multiplies its scores, that of a value's row its P, both in
+// binary32.
+//
+// attend_wide: 256 rows a workgroup, 8 waves of 32 rows; tiles of 64 keys pass through LDS for
+// all of them, double-buffered, the next tile's loads in flight during the products.
+// attend_narrow: up to 32 rows, for single tokens: the waves take 32-key tiles in turn, each with
+// its own piece of LDS, and join their sums at the end.
+// Either may split the keys of a tile over several workgroups, which then leave (m, l, O / l) in
+// the workspace for combine_kernel.
+//
+// Masked keys: scores are set to -inf by selection, so NaN there is harmless.  A masked value row
+// meets a weight of zero in the matrix unit, where an infinity or NaN would survive as NaN: rows
+// past the context are replaced by zeros when they are staged, and a query row whose result is not
+// finite is computed again by attend_row, which skips masked keys.
+#include "w4_codes.h"
+#include "w4_internal.h"
+#include "w4_paging.h"
+
+namespace w4 {
+namespace {
+
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+constexpr float kNegInf = -__builtin_huge_valf();
+// O is rescaled when a row's maximum grows by more than this (in powers of two); until then the
+// weights are up to 2^8 and the sums stay far inside binary32
+constexpr float kSlack = 8.0f;
+
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+    const f32x2_t f = {a, b};
+    const bf16x2_t h = __builtin_convertvector(f, bf16x2_t);
+    return __builtin_bit_cast(uint32_t, h);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// 16 bytes of E4M3 codes -> 16 bfloat16 values (exact)
+__device__ __forceinline__ void fp8_to_bf16(const u32x4_t c, u32x4_t& lo, u32x4_t& hi) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], 1.0f, false);
+        const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], 1.0f, true);
+        const uint32_t ua = __builtin_bit_cast(uint32_t, a), ub = __builtin_bit_cast(uint32_t, b);
+        if (i < 2) {
+            lo[2 * i] = ua;
+            lo[2 * i + 1] = ub;
+        } else {
+            hi[2 * (i - 2)] = ua;
+            hi[2 * (i - 2) + 1] = ub;
+        }
+    }
+}
+
+// Places of 16-byte chunk c of key row r in LDS.  K is read 16 rows at a time at one chunk: the
+// rows' chunks go to different bank groups.  V is read as 4 rows of 64 bytes: the rows go to
+// different quarters of the banks.
+template <int D>
+__device__ __forceinline__ int k_place(int r, int c) {
+    return r * (2 * D) + 16 * (D == 128 ? c ^ (r & 15) : c ^ ((r >> 1) & 7));
+}
+template <int D>
+__device__ __forceinline__ int v_place(int r, int c) {
+    return r * (2 * D) + 16 * (D == 128 ? c ^ ((r & 3) << 2) : c ^ (((r >> 1) & 1) << 2));
+}
+
+__device__ __forceinline__ uint64_t read_tr(const uint8_t* p) {
+    typedef __attribute__((address_space(3))) s16x4_t* lds_t;
+    const s16x4_t r = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t)(p));
+    return __builtin_bit_cast(uint64_t, r);
+}
+
+// Stages the 16 bytes that a lane loaded of key row r (chunk c of the stored row).
+template <int D, bool FP8, bool IS_V>
+__device__ __forceinline__ void stage(uint8_t* tile, int r, int c, u32x4_t w, bool keep) {
+    if (!keep) w = u32x4_t{0u, 0u, 0u, 0u};
+    if constexpr (FP8) {
+        u32x4_t lo, hi;
+        fp8_to_bf16(w, lo, hi);
+        *reinterpret_cast<u32x4_t*>(tile + (IS_V ? v_place<D>(r, 2 * c) : k_place<D>(r, 2 * c))) = lo;
+        *reinterpret_cast<u32x4_t*>(tile + (IS_V ? v_place<D>(r, 2 * c + 1) : k_place<D>(r, 2 * c + 1))) = hi;
+    } else {
+        *reinterpret_cast<u32x4_t*>(tile + (IS_V ? v_place<D>(r, c) : k_place<D>(r, c))) = w;
+    }
+}
+
+// The running state of 32 query rows: lane % 32 is the row, lane / 32 picks half of the keys in
+// the scores and half of the columns in O (register r of block i: column 32 i + 8 (r / 4) +
+// 4 (lane / 32) + r % 4).  l is the lane's own part of the sum.
+template <int D>
+struct Rows {
+    u32x4_t q[D / 16];
+    f32x16_t o[D / 32];
+    float m, l;
+};
+
+template <int D>
+__device__ __forceinline__ void clear_rows(Rows<D>& s) {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s.o[i][r] = 0.0f;
+    s.m = kNegInf;
+    s.l = 0.0f;
+}
+
+// One step over NB blocks of 32 keys.  kt, vt: staged tiles; ks, vs: their row scales (FP8).
+// first: position of the first key; lo, hi: the row sees lo <= key <= hi; mask: whether the step
+// reaches outside some row's keys.
+template <int D, bool FP8, int NB>
+__device__ __forceinline__ void attend_step(Rows<D>& s, const uint8_t* kt, const uint8_t* vt,
+                                            const float* ks, const float* vs, float scale,
+                                            int first, int lo, int hi, bool mask) {
+    const int lane = threadIdx.x & 63, half = lane >> 5, l32 = lane & 31;
+    f32x16_t z[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) z[b][r] = 0.0f;
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+            const u32x4_t a = *reinterpret_cast<const u32x4_t*>(kt + k_place<D>(32 * b + l32, 2 * d + half));
+            z[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                           __builtin_bit_cast(bf16x8_t, s.q[d]), z[b], 0, 0, 0);
+        }
+    }
+    if constexpr (FP8) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const f32x4_t f = *reinterpret_cast<const f32x4_t*>(ks + 32 * b + 8 * i + 4 * half);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) z[b][4 * i + j] *= f[j];
+            }
+    }
+    if (mask) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int key = first + 32 * b + 8 * (r >> 2) + 4 * half + (r & 3);
+                if (key < lo || key > hi) z[b][r] = kNegInf;
+            }
+    }
+    float mx = z[0][0];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) mx = fmaxf(mx, z[b][r]);
+    mx = fmaxf(mx, __shfl_xor(mx, 32)) * scale;              // scale > 0
+    if (__any(mx > s.m + kSlack)) {
+        const float m = fmaxf(s.m, mx);
+        const float f = m == s.m ? 1.0f : exp2_fast(s.m - m);
+        s.m = m;
+        s.l *= f;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s.o[i][r] *= f;
+    }
+    const float sub = s.m == kNegInf ? 0.0f : s.m;           // nothing seen yet: every weight is 0
+    uint32_t p[NB][8];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        f32x4_t f = {1.0f, 1.0f, 1.0f, 1.0f};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float e0 = exp2_fast(fmaf(z[b][2 * i], scale, -sub));
+            const float e1 = exp2_fast(fmaf(z[b][2 * i + 1], scale, -sub));
+            s.l += e0 + e1;
+            if constexpr (FP8) {
+                if ((i & 1) == 0) f = *reinterpret_cast<const f32x4_t*>(vs + 32 * b + 4 * i + 4 * half);
+                p[b][i] = bf16_pair(e0 * f[2 * (i & 1)], e1 * f[2 * (i & 1) + 1]);
+            } else {
+                p[b][i] = bf16_pair(e0, e1);
+            }
+        }
+    }
+    const int i16 = lane & 15, g16 = (lane >> 4) & 1;
+#pragma unroll
+    for (int c = 0; c < 2 * NB; ++c) {                       // 16 keys each
+        const u32x4_t pb = {p[c >> 1][4 * (c & 1)], p[c >> 1][4 * (c & 1) + 1], p[c >> 1][4 * (c & 1) + 2],
+                            p[c >> 1][4 * (c & 1) + 3]};
+        const int r0 = 16 * c + 4 * half + (i16 >> 2);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            const int chunk = 4 * i + 2 * g16 + ((i16 & 3) >> 1), off = 8 * (i16 & 1);
+            const uint64_t a0 = read_tr(vt + v_place<D>(r0, chunk) + off);
+            const uint64_t a1 = read_tr(vt + v_place<D>(r0 + 8, chunk) + off);
+            const u32x4_t a = {(uint32_t)a0, (uint32_t)(a0 >> 32), (uint32_t)a1, (uint32_t)(a1 >> 32)};
+            s.o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                             __builtin_bit_cast(bf16x8_t, pb), s.o[i], 0, 0, 0);
+        }
+    }
+}
+
+// Which sequence a number belongs to: the last b with key(b) <= x, by all lanes of a wave (the
+// keys of 64 sequences at a time, so two rounds of loads for up to 4096 sequences).
+template <typename Key>
+__device__ __forceinline__ int find_seq(int B, Key key, int64_t x) {
+    const int lane = threadIdx.x & 63;
+    int base = 0;
+    for (int step = B > 64 ? 64 : 1;; step = 1) {
+        const int b = base + lane * step;
+        const bool below = b < B && key(b) <= x;
+        const int n = __popcll(__ballot(below));
+        if (n == 0) return base;                             // only at the start: key(0) > x
+        base += (n - 1) * step;
+        if (step == 1) return base;
+    }
+}
+
+__device__ __forceinline__ Seq load_seq(const AttendArgs& a, int b) {
+    return clamp_seq(a.cu[b], a.cu[b + 1], a.lens[b], a.T, a.max_pages << a.page_shift);
+}
+
+// Row of the cache that holds a key (times D elements), or -1 where the table names no page.
+__device__ __forceinline__ int64_t key_row(const AttendArgs& a, int b, int kv, int64_t key) {
+    const int64_t page = checked_page(a.table[(int64_t)b * a.max_pages + (key >> a.page_shift)], a.pages);
+    if (page < 0) return -1;
+    return ((page * a.kv_heads + kv) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+}
+
+// One query row over keys [k0, k1) by one wave, D / 64 columns a lane, skipping masked keys; O is
+// kept divided by the sum, so values near the end of the range do not overflow.
+template <int D, bool FP8>
+__device__ void attend_row(const AttendArgs& a, int b, int kv, int64_t row, int64_t k0, int64_t k1,
+                           int lo, int hi, float* o, float& m_out, float& l_out) {
+    constexpr int E = D / 64;
+    const int lane = threadIdx.x & 63;
+    float q[E], m = kNegInf, l = 0.0f;
+    for (int e = 0; e < E; ++e) {
+        q[e] = __uint_as_float((uint32_t)a.q[row * D + lane * E + e] << 16);
+        o[e] = 0.0f;
+    }
+    for (int64_t j = k0 > lo ? k0 : lo; j < k1 && j <= hi; ++j) {
+        const int64_t at = key_row(a, b, kv, j);
+        float k[E], v[E];
+        for (int e = 0; e < E; ++e) {
+            k[e] = v[e] = 0.0f;
+            if (at >= 0) {
+                const int64_t i = at * D + lane * E + e;
+                if constexpr (FP8) {
+                    k[e] = __builtin_amdgcn_cvt_f32_fp8(static_cast<const uint8_t*>(a.k)[i], 0) * a.k_scales[at];
+                    v[e] = __builtin_amdgcn_cvt_f32_fp8(static_cast<const uint8_t*>(a.v)[i], 0) * a.v_scales[at];
+                } else {
+                    k[e] = __uint_as_float((uint32_t) static_cast<const uint16_t*>(a.k)[i] << 16);
+                    v[e] = __uint_as_float((uint32_t) static_cast<const uint16_t*>(a.v)[i] << 16);
+                }
+            }
+        }
+        float z = 0.0f;
+        for (int e = 0; e < E; ++e) z = fmaf(q[e], k[e], z);
+        for (int off = 32; off > 0; off >>= 1) z += __shfl_xor(z, off);
+        z *= a.scale_log2;
+        const float mn = z != z ? z : fmaxf(m, z);
+        const float keep = mn == m ? 1.0f : exp2_fast(m - mn);
+        const float p = mn == kNegInf ? 0.0f : exp2_fast(z - mn);
+        const float ln = l * keep + p;
+        if (!(ln == 0.0f)) {
+            const float fo = l * keep / ln, fv = p / ln;
+            for (int e = 0; e < E; ++e) o[e] = (fo == 0.0f ? 0.0f : o[e] * fo) + v[e] * fv;
+        }
+        l = ln;
+        m = mn;
+    }
+    m_out = m;
+    l_out = l;
+}
+
+// What a row's sum of weights divides by: a row that sees no key gives zeros, one that sees keys
+// of weight zero only (every score -inf) 0/0 like the formula.
+__device__ __forceinline__ float inverse(float l, bool sees) {
+    return l == 0.0f ? (sees ? __builtin_nanf("") : 0.0f) : 1.0f / l;
+}
+
+struct Tile {
+    Seq seq;
+    Span span;
+    int b;
+    int64_t part_row;  // the tile's first row in the workspace
+    int64_t row0;      // first row of the tile in its sequence
+    int64_t rows;      // rows of the sequence
+    int64_t k0, k1;    // keys of this workgroup's part
+    bool run;
+};
+
+// Tile number `index` of attend_wide's or attend_narrow's launch.  Where both are launched, a
+// sequence of at most kNarrowRows rows is the narrow kernel's, as its only tile, and the narrow
+// launch has one tile a sequence.
+template <bool WIDE>
+__device__ __forceinline__ Tile find_tile(const AttendArgs& a, int64_t index, int part, int& kv) {
+    constexpr int R = WIDE ? kWideRows : kNarrowRows;
+    Tile t;
+    const int G = a.group;
+    kv = (int)(index % a.kv_heads);
+    const int64_t tile = index / a.kv_heads;
+    t.part_row = index * R;
+    if (!WIDE && a.both) {
+        t.b = (int)tile;
+        t.row0 = 0;
+    } else {
+        t.b = find_seq(a.B, [&](int b) { return first_tile(a.cu[b], b, G, R); }, tile);
+        t.row0 = (tile - first_tile(a.cu[t.b], t.b, G, R)) * R;
+    }
+    t.seq = load_seq(a, t.b);
+    t.rows = t.seq.n * G;
+    const bool few = t.rows <= kNarrowRows;
+    t.run = t.row0 >= 0 && t.row0 < t.rows && (WIDE ? !few : few || !a.both);
+    if (!t.run) return t;
+    t.span = key_span(t.seq, t.row0, imin(R, t.rows - t.row0), G, a.window,
+                      WIDE ? a.wide_parts : a.narrow_parts, WIDE ? kWideLeast : kNarrowLeast);
+    t.run = part < t.span.parts;
+    t.k0 = t.span.begin + part * t.span.chunk;
+    t.k1 = imin(t.span.end, t.k0 + t.span.chunk);
+    return t;
+}
+
+// The place of a row of the tile: its row in q and o, and the keys it sees.
+struct Place {
+    int64_t row;       // token * heads + head
+    int lo, hi;
+    bool real;
+};
+__device__ __forceinline__ Place row_place(const AttendArgs& a, const Tile& t, int kv, int64_t r) {
+    Place p;
+    p.real = r < t.rows;
+    const int64_t token = p.real ? r / a.group : 0;
+    p.row = (t.seq.start + token) * a.heads + (int64_t)kv * a.group + (p.real ? r - token * a.group : 0);
+    p.hi = p.real ? (int)(t.seq.ctx - t.seq.n + token) : -1;
+    p.lo = a.window > 0 ? (int)imax(0, p.hi - (int64_t)a.window + 1) : 0;
+    return p;
+}
+
+template <int D>
+__device__ __forceinline__ void load_q(const AttendArgs& a, const Place& p, Rows<D>& s) {
+    const int half = (threadIdx.x & 63) >> 5;
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) {
+        s.q[d] = u32x4_t{0u, 0u, 0u, 0u};
+        if (p.real) s.q[d] = *reinterpret_cast<const u32x4_t*>(a.q + p.row * D + 16 * d + 8 * half);
+    }
+}
+
+// Stores 4 neighbouring columns of a row that are already divided by its sum.
+template <bool WIDE>
+struct Parts {
+    float* o;          // [parts][rows of all tiles][D]
+    float* ml;         // [parts][rows of all tiles][2]
+    int64_t rows;
+    __device__ explicit Parts(const AttendArgs& a)
+        : o(WIDE ? a.wide_o : a.narrow_o), ml(WIDE ? a.wide_ml : a.narrow_ml),
+          rows(WIDE ? a.wide_rows : a.narrow_rows) {}
+    __device__ int64_t at(const Tile& t, int part, int r) const { return part * rows + t.part_row + r; }
+};
+
+template <bool WIDE>
+__device__ __forceinline__ void store4(const AttendArgs& a, const Tile& t, int part, int r, int64_t row,
+                                       int D, int col, f32x4_t v) {
+    if (t.span.parts == 1) {
+        const uint2 w = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+        *reinterpret_cast<uint2*>(a.o + row * D + col) = w;
+    } else {
+        const Parts<WIDE> w(a);
+        *reinterpret_cast<f32x4_t*>(w.o + w.at(t, part, r) * D + col) = v;
+    }
+}
+
+template <bool WIDE>
+__device__ __forceinline__ void store_ml(const AttendArgs& a, const Tile& t, int part, int r, float m, float l) {
+    const Parts<WIDE> w(a);
+    float* p = w.ml + 2 * w.at(t, part, r);
+    p[0] = m;
+    p[1] = l;
+}
+
+// Computes the rows of `bad` (one bit per row from row r0 of the tile) again.
+template <int D, bool FP8, bool WIDE>
+__device__ void redo_rows(const AttendArgs& a, const Tile& t, int part, int kv, int r0, uint32_t bad) {
+    constexpr int E = D / 64;
+    const int lane = threadIdx.x & 63;
+    while (bad) {
+        const int r = r0 + __ffs(bad) - 1;
+        bad &= bad - 1;
+        const Place p = row_place(a, t, kv, t.row0 + r);
+        float o[E], m, l;
+        attend_row<D, FP8>(a, t.b, kv, p.row, t.k0, t.k1, p.lo, p.hi, o, m, l);
+        if (t.span.parts == 1) {
+            const bool sees = p.hi >= 0;
+            for (int e = 0; e < E; ++e) {
+                const float v = l == 0.0f && sees ? __builtin_nanf("") : o[e];
+                a.o[p.row * D + lane * E + e] = (uint16_t)bf16_pair(v, v);
+            }
+        } else {
+            const Parts<WIDE> w(a);
+            for (int e = 0; e < E; ++e) w.o[w.at(t, part, r) * D + lane * E + e] = o[e];
+            if (lane == 0) store_ml<WIDE>(a, t, part, r, m, l);
+        }
+    }
+}
+
+constexpr int kWideWaves = 8;
+constexpr int kWideThreads = 64 * kWideWaves;
+
+template <int D, bool FP8>
+__global__ __launch_bounds__(kWideThreads, 2) void attend_wide_kernel(AttendArgs a) {
+    constexpr int kRowBytes = FP8 ? D : 2 * D;               // of a cached row
+    constexpr int kChunks = kRowBytes / 16;
+    constexpr int kStepRows = kWideThreads / kChunks;        // rows that one load of all threads covers
+    constexpr int kLoads = kStepRows >= kKeyTile ? 1 : kKeyTile / kStepRows;
+    constexpr int kTileBytes = kKeyTile * 2 * D;
+    __shared__ __attribute__((aligned(16))) uint8_t kt[2][kTileBytes], vt[2][kTileBytes];
+    __shared__ __attribute__((aligned(16))) float ksc[2][kKeyTile], vsc[2][kKeyTile];
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const int part = blockIdx.y;
+    int kv;
+    // the last tiles of a sequence see the most keys: they start first
+    const Tile t = find_tile<true>(a, (int64_t)gridDim.x - 1 - blockIdx.x, part, kv);
+    if (!t.run) return;
+    const int r = 32 * wave + (lane & 31);
+    const Place p = row_place(a, t, kv, t.row0 + r);
+    Rows<D> s;
+    load_q<D>(a, p, s);
+    clear_rows<D>(s);
+    // keys that any row of this wave sees, and those that all of them see
+    int any_lo = p.real ? p.lo : INT32_MAX, any_hi = p.hi, all_lo = p.lo, all_hi = p.real ? p.hi : INT32_MAX;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        any_lo = min(any_lo, __shfl_xor(any_lo, off));
+        any_hi = max(any_hi, __shfl_xor(any_hi, off));
+        all_lo = max(all_lo, __shfl_xor(all_lo, off));
+        all_hi = min(all_hi, __shfl_xor(all_hi, off));
+    }
+    any_lo = __builtin_amdgcn_readfirstlane(any_lo);
+    any_hi = __builtin_amdgcn_readfirstlane(any_hi);
+    all_lo = __builtin_amdgcn_readfirstlane(all_lo);
+    all_hi = __builtin_amdgcn_readfirstlane(all_hi);
+
+    const int k0 = (int)t.k0, k1 = (int)t.k1;
+    const int tiles = (k1 - k0 + kKeyTile - 1) / kKeyTile;
+    const int crow = tid / kChunks, chunk = tid % kChunks;
+    const bool loads = crow < kKeyTile;                      // more threads than chunks of a tile
+    int64_t at[kLoads];                                      // cache rows of the tile after next
+    u32x4_t kw[kLoads], vw[kLoads];
+    float sc = 1.0f;
+    bool keep[kLoads], bad_page = false;
+    auto look_up = [&](int i) {
+#pragma unroll
+        for (int c = 0; c < kLoads; ++c) {
+            const int key = k0 + i * kKeyTile + crow + c * kStepRows;
+            at[c] = -2;
+            if (loads && key < k1) {
+                at[c] = key_row(a, t.b, kv, key);
+                bad_page |= at[c] == -1;
+            }
+        }
+    };
+    auto fetch = [&]() {                                     // rows found by look_up
+#pragma unroll
+        for (int c = 0; c < kLoads; ++c) {
+            keep[c] = at[c] >= 0;
+            const int64_t row = keep[c] ? at[c] : 0;         // the cache has at least one row
+            kw[c] = *reinterpret_cast<const u32x4_t*>(static_cast<const uint8_t*>(a.k) + row * kRowBytes + 16 * chunk);
+            vw[c] = *reinterpret_cast<const u32x4_t*>(static_cast<const uint8_t*>(a.v) + row * kRowBytes + 16 * chunk);
+            if constexpr (FP8) {
+                static_assert(kLoads == 1, "one row a thread");
+                if (chunk < 2) sc = keep[c] ? (chunk == 0 ? a.k_scales : a.v_scales)[row] : 1.0f;
+            }
+        }
+    };
+    auto put = [&](int buf) {
+        if (!loads) return;
+#pragma unroll
+        for (int c = 0; c < kLoads; ++c) {
+            stage<D, FP8, false>(kt[buf], crow + c * kStepRows, chunk, kw[c], keep[c]);
+            stage<D, FP8, true>(vt[buf], crow + c * kStepRows, chunk, vw[c], keep[c]);
+        }
+        if constexpr (FP8) {
+            if (chunk < 2) (chunk == 0 ? ksc[buf] : vsc[buf])[crow] = sc;
+        }
+    };
+    if (tiles > 0) {
+        look_up(0);
+        fetch();
+        look_up(1);
+        put(0);
+    }
+    __syncthreads();
+    for (int i = 0; i < tiles; ++i) {
+        const int buf = i & 1;
+        if (i + 1 < tiles) {
+            fetch();
+            look_up(i + 2);
+        }
+        const int first = k0 + i * kKeyTile, last = first + kKeyTile - 1;
+        if (first <= any_hi && last >= any_lo)
+            attend_step<D, FP8, 2>(s, kt[buf], vt[buf], ksc[buf], vsc[buf], a.scale_log2, first, p.lo, p.hi,
+                                   first < all_lo || last > all_hi);
+        if (i + 1 < tiles) put(buf ^ 1);
+        __syncthreads();
+    }
+    if (bad_page && a.status) atomicOr(a.status, kStatusPage);
+
+    const float l = s.l + __shfl_xor(s.l, 32);
+    const bool whole = t.span.parts == 1;
+    const float inv = inverse(l, whole && p.hi >= 0);
+    const int half = lane >> 5;
+    bool bad = !isfinite(l);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            f32x4_t v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                bad |= !isfinite(s.o[i][4 * g + j]);
+                v[j] = s.o[i][4 * g + j] * inv;
+            }
+            if (p.real) store4<true>(a, t, part, r, p.row, D, 32 * i + 8 * g + 4 * half, v);
+        }
+    if (p.real && !whole && half == 0) store_ml<true>(a, t, part, r, s.m, l);
+    const uint64_t mask = __ballot(bad && p.real);
+    const uint32_t rows = (uint32_t)mask | (uint32_t)(mask >> 32);
+    if (rows) {
+        __threadfence();                                     // the rows' first results have landed
+        redo_rows<D, FP8, true>(a, t, part, kv, 32 * wave, rows);
+    }
+}
+
+constexpr int kNarrowWaves = 8;
+constexpr int kNarrowThreads = 64 * kNarrowWaves;
+
+template <int D, bool FP8>
+__global__ __launch_bounds__(kNarrowThreads, 2) void attend_narrow_kernel(AttendArgs a) {
+    constexpr int kKeys = 32;                                // of a wave's tile
+    constexpr int kRowBytes = FP8 ? D : 2 * D;
+    constexpr int kChunks = kRowBytes / 16;
+    constexpr int kStepRows = 64 / kChunks;                  // rows that one load of the wave covers
+    constexpr int kLoads = kKeys / kStepRows;
+    constexpr int kTileBytes = kKeys * 2 * D;
+    // a wave's tiles; at the end its O (32 rows of D binary32) takes the same place
+    __shared__ __attribute__((aligned(16))) uint8_t tiles_lds[kNarrowWaves][2 * kTileBytes];
+    __shared__ __attribute__((aligned(16))) float scales[kNarrowWaves][2 * kKeys];
+    __shared__ float sm[kNarrowWaves][32], sl[kNarrowWaves][32];
+    static_assert(2 * kTileBytes == 32 * D * 4, "O fits the tiles' place");
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const int part = blockIdx.y;
+    int kv;
+    const Tile t = find_tile<false>(a, blockIdx.x, part, kv);
+    if (!t.run) return;
+    const Place p = row_place(a, t, kv, t.row0 + (lane & 31));
+    Rows<D> s;
+    load_q<D>(a, p, s);
+    clear_rows<D>(s);
+    int all_lo = p.lo, all_hi = p.real ? p.hi : INT32_MAX;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        all_lo = max(all_lo, __shfl_xor(all_lo, off));
+        all_hi = min(all_hi, __shfl_xor(all_hi, off));
+    }
+    all_lo = __builtin_amdgcn_readfirstlane(all_lo);
+    all_hi = __builtin_amdgcn_readfirstlane(all_hi);
+
+    const int k0 = (int)t.k0, k1 = (int)t.k1;
+    uint8_t* kt = tiles_lds[wave];
+    uint8_t* vt = kt + kTileBytes;
+    const int crow = lane / kChunks, chunk = lane % kChunks;
+    // A page holds 16 keys at least and tiles begin at multiples of 32, so either half of a tile
+    // lies in one page: two lookups a tile, the same for all lanes.
+    int64_t base[2];                                         // cache row of each half's first key
+    u32x4_t kw[kLoads], vw[kLoads];
+    float sc = 1.0f;
+    bool bad_page = false, ok[2] = {false, false};
+    auto look_up = [&](int i) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int key = k0 + i * kKeys + 16 * h;
+            base[h] = -2;
+            if (key < k1) {
+                base[h] = key_row(a, t.b, kv, key);
+                bad_page |= base[h] == -1;
+            }
+        }
+    };
+    auto fetch = [&]() {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) ok[h] = base[h] >= 0;
+#pragma unroll
+        for (int c = 0; c < kLoads; ++c) {
+            const int row = c * kStepRows + crow, h = (c * kStepRows) >> 4;
+            const int64_t at = (ok[h] ? base[h] : 0) + (row & 15);   // a page has 16 rows at least
+            kw[c] = *reinterpret_cast<const u32x4_t*>(static_cast<const uint8_t*>(a.k) + at * kRowBytes + 16 * chunk);
+            vw[c] = *reinterpret_cast<const u32x4_t*>(static_cast<const uint8_t*>(a.v) + at * kRowBytes + 16 * chunk);
+        }
+        if constexpr (FP8) {
+            const int key = lane & 31, h = key >> 4;
+            const int64_t at = (ok[h] ? base[h] : 0) + (key & 15);
+            sc = (lane < 32 ? a.k_scales : a.v_scales)[at];
+        }
+    };
+    const int tiles = (k1 - k0 + kKeys - 1) / kKeys;
+    if (wave < tiles) {
+        look_up(wave);
+        fetch();
+        look_up(wave + kNarrowWaves);
+    }
+    for (int i = wave; i < tiles; i += kNarrowWaves) {
+        const int first = k0 + i * kKeys;
+#pragma unroll
+        for (int c = 0; c < kLoads; ++c) {
+            const int row = c * kStepRows + crow;
+            const bool keep = ok[(c * kStepRows) >> 4] && first + row < k1;
+            stage<D, FP8, false>(kt, row, chunk, kw[c], keep);
+            stage<D, FP8, true>(vt, row, chunk, vw[c], keep);
+        }
+        if constexpr (FP8) scales[wave][lane] = ok[(lane & 31) >> 4] && first + (lane & 31) < k1 ? sc : 1.0f;
+        if (i + kNarrowWaves < tiles) {
+            fetch();
+            look_up(i + 2 * kNarrowWaves);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // rows staged by other lanes
+        attend_step<D, FP8, 1>(s, kt, vt, scales[wave], scales[wave] + kKeys, a.scale_log2, first, p.lo, p.hi,
+                               first < all_lo || first + kKeys - 1 > all_hi);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // read before the next rows land
+    }
+    if (bad_page && lane == 0 && a.status) atomicOr(a.status, kStatusPage);
+
+    // Join the waves: O of wave w counts 2^(m_w - m).
+    const int half = lane >> 5;
+    const float l = s.l + __shfl_xor(s.l, 32);
+    if (lane < 32) {
+        sm[wave][lane] = s.m;
+        sl[wave][lane] = l;
+    }
+    float* own = reinterpret_cast<float*>(tiles_lds[wave]);
+    // row r's groups of 4 columns are rotated by r, so that 8 rows do not share banks
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const f32x4_t v = {s.o[i][4 * g], s.o[i][4 * g + 1], s.o[i][4 * g + 2], s.o[i][4 * g + 3]};
+            const int group = (8 * i + 2 * g + half + (lane & 31)) & (D / 4 - 1);
+            *reinterpret_cast<f32x4_t*>(own + (lane & 31) * D + 4 * group) = v;
+        }
+    __syncthreads();
+    constexpr int kGroups = D / 4;                           // a thread joins 4 columns of a row
+    uint32_t bad_rows = 0;
+    const bool whole = t.span.parts == 1;
+    const int rows_here = (int)imin(kNarrowRows, t.rows - t.row0);
+    for (int i = tid; i < rows_here * kGroups; i += kNarrowThreads) {
+        const int row = i / kGroups, g = i % kGroups;
+        float m = kNegInf;
+#pragma unroll
+        for (int w = 0; w < kNarrowWaves; ++w) m = fmaxf(m, sm[w][row]);
+        float sum = 0.0f;
+        f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int w = 0; w < kNarrowWaves; ++w) {
+            const float mw = sm[w][row];
+            const float f = mw == kNegInf ? 0.0f : exp2_fast(mw - m);
+            const f32x4_t ow = *reinterpret_cast<const f32x4_t*>(reinterpret_cast<const float*>(tiles_lds[w]) +
+                                                                row * D + 4 * ((g + row) & (kGroups - 1)));
+            sum += f * sl[w][row];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] += f * ow[j];
+        }
+        bool bad = !isfinite(sum);
+        const Place pr = row_place(a, t, kv, t.row0 + row);
+        const float inv = inverse(sum, whole && pr.hi >= 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            bad |= !isfinite(v[j]);
+            v[j] *= inv;
+        }
+        if (bad) bad_rows |= 1u << row;
+        store4<false>(a, t, part, row, pr.row, D, 4 * g, v);
+        if (g == 0 && !whole) store_ml<false>(a, t, part, row, m, sum);
+    }
+    __shared__ uint32_t redo;
+    if (tid == 0) redo = 0;
+    __syncthreads();
+    if (bad_rows) atomicOr(&redo, bad_rows);
+    __syncthreads();
+    if (redo) {
+        __threadfence();                                     // the rows' first results have landed
+        __syncthreads();
+        if (wave == 0) redo_rows<D, FP8, false>(a, t, part, kv, 0, redo);
+    }
+}
+
+// Joins the parts of the rows that were split: one wave a row, the tiles numbered as in the
+// launch that wrote them.
+template <int D, bool WIDE>
+__global__ __launch_bounds__(256) void combine_kernel(AttendArgs a) {
+    constexpr int E = D / 64, kSets = (WIDE ? kWideRows : kNarrowRows) / 4;
+    const int lane = threadIdx.x & 63;
+    int kv;
+    const Tile t = find_tile<WIDE>(a, blockIdx.x / kSets, 0, kv);
+    const int r = (int)(blockIdx.x % kSets) * 4 + (threadIdx.x >> 6);
+    if (!t.run || t.span.parts == 1 || t.row0 + r >= t.rows) return;
+    const Place place = row_place(a, t, kv, t.row0 + r);
+    const Parts<WIDE> w(a);
+    float m = kNegInf;
+    for (int p = lane; p < t.span.parts; p += 64) m = fmaxf(m, w.ml[2 * w.at(t, p, r)]);
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
+    float sum = 0.0f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+    for (int p = 0; p < t.span.parts; ++p) {
+        const int64_t at = w.at(t, p, r);
+        const float mp = w.ml[2 * at], lp = w.ml[2 * at + 1];
+        if (lp == 0.0f) continue;                            // nothing of weight in this part
+        const float f = exp2_fast(mp - m) * lp;              // NaN where lp or mp is
+        sum += f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] += f * w.o[at * D + lane * E + e];
+    }
+    const float inv = inverse(sum, place.hi >= 0);
+    if constexpr (E == 2)
+        *reinterpret_cast<uint32_t*>(a.o + place.row * D + 2 * lane) = bf16_pair(o[0] * inv, o[1] * inv);
+    else
+        a.o[place.row * D + lane] = (uint16_t)bf16_pair(o[0] * inv, o[0] * inv);
+}
+
+// Parts that a launch allows per tile: enough to give every compute unit `target` / 256 workgroups.
+int parts_for(int64_t tiles, int64_t target, int64_t longest, int64_t least) {
+    const int64_t want = ceil_div(target, tiles);
+    return (int)imax(1, imin(want, imin(ceil_div(longest, least), kMaxParts)));
+}
+
+}  // namespace
+
+void plan_attend(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int64_t capacity, AttendPlan* p) {
+    const int64_t G = heads / kv_heads;
+    // One token a sequence, or too few rows for the wide kernel: no sequence needs it.
+    p->both = T != B && T * G > kNarrowRows;
+    p->narrow_tiles = (p->both ? B : tile_bound(T, B, G, kNarrowRows)) * kv_heads;
+    p->narrow_parts = parts_for(p->narrow_tiles, 512, capacity, kNarrowLeast);
+    p->wide_tiles = p->both ? tile_bound(T, B, G, kWideRows) * kv_heads : 0;
+    p->wide_parts = p->both ? parts_for(p->wide_tiles, 512, capacity, kWideLeast) : 1;
+}
+
+static int64_t split_rows(bool wide, const AttendPlan& p) {
+    const int64_t tiles = wide ? p.wide_tiles : p.narrow_tiles;
+    return (wide ? p.wide_parts : p.narrow_parts) > 1 ? tiles * (wide ? kWideRows : kNarrowRows) : 0;
+}
+
+size_t attend_workspace(int64_t D, const AttendPlan& p) {
+    return (size_t)(split_rows(false, p) * p.narrow_parts + split_rows(true, p) * p.wide_parts) * (D + 2) * 4;
+}
+
+template <int D, bool FP8>
+static hipError_t launch_attend_d(const AttendArgs& a, const AttendPlan& p, hipStream_t s) {
+    if (p.both)
+        hipLaunchKernelGGL((attend_wide_kernel<D, FP8>), dim3((unsigned)p.wide_tiles, (unsigned)p.wide_parts),
+                           dim3(kWideThreads), 0, s, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((attend_narrow_kernel<D, FP8>), dim3((unsigned)p.narrow_tiles, (unsigned)p.narrow_parts),
+                       dim3(kNarrowThreads), 0, s, a);
+    e = hipGetLastError();
+    if (e == hipSuccess && a.wide_rows > 0) {
+        hipLaunchKernelGGL((combine_kernel<D, true>), dim3((unsigned)(a.wide_rows / 4)), dim3(256), 0, s, a);
+        e = hipGetLastError();
+    }
+    if (e == hipSuccess && a.narrow_rows > 0) {
+        hipLaunchKernelGGL((combine_kernel<D, false>), dim3((unsigned)(a.narrow_rows / 4)), dim3(256), 0, s, a);
+        e = hipGetLastError();
+    }
+    return e;
+}
+
+hipError_t launch_attend(AttendArgs a, int head_dim, bool fp8, const AttendPlan& p, void* workspace, hipStream_t s) {
+    a.both = p.both;
+    a.narrow_parts = p.narrow_parts;
+    a.wide_parts = p.wide_parts;
+    a.narrow_rows = split_rows(false, p);
+    a.wide_rows = split_rows(true, p);
+    a.narrow_o = static_cast<float*>(workspace);
+    a.wide_o = a.narrow_o + a.narrow_rows * p.narrow_parts * head_dim;
+    a.narrow_ml = a.wide_o + a.wide_rows * p.wide_parts * head_dim;
+    a.wide_ml = a.narrow_ml + a.narrow_rows * p.narrow_parts * 2;
+    if (head_dim == 128) return fp8 ? launch_attend_d<128, true>(a, p, s) : launch_attend_d<128, false>(a, p, s);
+    return fp8 ? launch_attend_d<64, true>(a, p, s) : launch_attend_d<64, false>(a, p, s);
+}
+
+}  // namespace w4

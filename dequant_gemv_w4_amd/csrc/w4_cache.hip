@@ -1,0 +1,302 @@
+// What stands between the fused q|k|v product and the attention: rotary positions with the write
+// of K and V into the paged cache, and the block tables and slots that the write goes by.
+//
+// Rotary positions: the pair (x0, x1) of a head at position p turns by the angle p * f,
+//     (A (x0 cos - x1 sin), A (x0 sin + x1 cos)),
+// with f and the amplitude A from w4_rope_frequencies.  Pairs are (i, i + R/2) of the first R
+// elements of a head, or (2i, 2i+1).  p * f passes 2^24 turns' worth of binary32 at far
+// positions, so the turns p * f / 2 pi are formed in binary64 and only their fraction goes on in
+// binary32 (angles are off by less than 2^-24 turns wherever p * f < 2^28).  A workgroup takes
+// one token, so the R/2 sines and cosines are formed once for all heads.
+//
+// Bound by memory: each row is read once and written once.  A lane takes two chunks of 8
+// elements that hold 8 whole pairs, so no element moves between lanes, and D / 16 neighbouring
+// lanes hold a head, which gives the E4M3 row its largest value by shuffles.
+#include "w4_codes.h"
+#include "w4_internal.h"
+#include "w4_paging.h"
+
+namespace w4 {
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kMaxPairs = 64;   // head_dim 128
+
+__device__ __forceinline__ uint32_t bf16_pair2(float a, float b) {
+    typedef float f2_t __attribute__((ext_vector_type(2)));
+    typedef __bf16 b2_t __attribute__((ext_vector_type(2)));
+    const f2_t f = {a, b};
+    const b2_t h = __builtin_convertvector(f, b2_t);
+    return __builtin_bit_cast(uint32_t, h);
+}
+
+__device__ __forceinline__ void store8_bf16(uint16_t* p, const float* v) {
+    u32x4_t a;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) a[q] = bf16_pair2(v[2 * q], v[2 * q + 1]);
+    *reinterpret_cast<u32x4_t*>(p) = a;
+}
+
+template <bool XF32, bool FP8>
+__global__ __launch_bounds__(kRopeThreads) void rope_cache_kernel(RopeArgs a) {
+    __shared__ float cs[kMaxPairs], sn[kMaxPairs];
+    const int64_t t = blockIdx.x;
+    const int64_t slot = a.slots[t];
+    if (slot < 0) return;                                    // padding: nothing is written
+    if (slot >= a.pages << a.page_shift) {
+        if (threadIdx.x == 0 && blockIdx.y == 0 && a.status) atomicOr(a.status, kStatusPage);
+        return;
+    }
+    const int half = a.rotary >> 1;
+    if ((int)threadIdx.x < half) {
+        const double turns = (double)a.positions[t] * a.freqs[threadIdx.x] * 0.15915494309189533577;
+        const float part = (float)(turns - rint(turns));     // [-1/2, 1/2]
+        float s, c;
+        sincospif(2.0f * part, &s, &c);
+        cs[threadIdx.x] = c * a.amplitude;
+        sn[threadIdx.x] = s * a.amplitude;
+    }
+    __syncthreads();
+    const int D = a.head_dim;
+    const int lanes = D >> 4;                                // lanes of a head: 4 or 8
+    const int total = (a.heads + 2 * a.kv_heads) * lanes;
+    const int64_t page = slot >> a.page_shift;
+    const int64_t in_page = slot & ((1 << a.page_shift) - 1);
+    const int64_t row0 = t * (int64_t)(a.heads + 2 * a.kv_heads) * D;
+    bool finite = true;
+    for (int item = blockIdx.y * kRopeThreads + threadIdx.x; item < total;
+         item += gridDim.y * kRopeThreads) {
+        const int head = item / lanes, u = item & (lanes - 1);
+        const bool rotates = u < (a.rotary >> 4) && head < a.heads + a.kv_heads;
+        const bool split = u < (a.rotary >> 4) && !a.interleaved;
+        const int c0 = split ? 8 * u : 16 * u;
+        const int c1 = split ? 8 * u + half : 16 * u + 8;
+        float v[16];
+        load8<!XF32>(a.qkv, row0 + (int64_t)head * D + c0, v);
+        load8<!XF32>(a.qkv, row0 + (int64_t)head * D + c1, v + 8);
+        if (rotates) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float c = cs[8 * u + j], s = sn[8 * u + j];
+                if (a.interleaved) {
+                    const float x0 = v[2 * j], x1 = v[2 * j + 1];
+                    v[2 * j] = x0 * c - x1 * s;
+                    v[2 * j + 1] = x0 * s + x1 * c;
+                } else {
+                    const float x0 = v[j], x1 = v[8 + j];
+                    v[j] = x0 * c - x1 * s;
+                    v[8 + j] = x0 * s + x1 * c;
+                }
+            }
+        }
+        if (head < a.heads) {
+            uint16_t* q = a.q + (t * a.heads + head) * D;
+            store8_bf16(q + c0, v);
+            store8_bf16(q + c1, v + 8);
+            continue;
+        }
+        const bool is_v = head >= a.heads + a.kv_heads;
+        const int kvh = head - a.heads - (is_v ? a.kv_heads : 0);
+        const int64_t row = ((page * a.kv_heads + kvh) << a.page_shift) + in_page;
+        if constexpr (!FP8) {
+            uint16_t* dst = static_cast<uint16_t*>(is_v ? a.v : a.k) + row * D;
+            store8_bf16(dst + c0, v);
+            store8_bf16(dst + c1, v + 8);
+        } else {
+            float amax = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                amax = fmaxf(amax, fabsf(v[j]));
+                finite &= isfinite(v[j]);
+            }
+            for (int off = lanes >> 1; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor(amax, off));
+            const double s = amax == 0.0f ? 1.0 : (double)amax / kFp8Max;
+            const float rs = (float)(1.0 / s);
+            const bool ok = s >= 0x1p-100 && s <= 0x1p100;
+            if (u == 0) (is_v ? a.v_scales : a.k_scales)[row] = (float)s;
+            uint8_t* dst = static_cast<uint8_t*>(is_v ? a.v : a.k) + row * D;
+            *reinterpret_cast<uint2*>(dst + c0) = w8_codes8<false>(v, s, rs, ok);
+            *reinterpret_cast<uint2*>(dst + c1) = w8_codes8<false>(v + 8, s, rs, ok);
+        }
+    }
+    if (FP8 && !finite && a.status) atomicOr(a.status, kStatusNonfinite);
+}
+
+// --------------------------------------------------------------------------
+// Block tables and slots
+// --------------------------------------------------------------------------
+//
+// Two exclusive sums over the requests, of their new tokens and of the pages they take, place
+// everything; each new token then finds its request by a search in the first sum.  Every
+// workgroup scans the requests itself (8 bytes a request, read from the cache by all but the
+// first), which is cheaper than a launch of its own: a single workgroup also writes the new
+// lengths and the rest of the list after all have read the old ones; with more workgroups a
+// second launch does, so that lengths and list may be updated in place.
+
+constexpr int kTableThreads = 1024;
+
+struct Scan {
+    int cu[kMaxSeqs + 1];        // first token of each request
+    int taken[kMaxSeqs];         // pages taken ahead of it
+    int cached[kMaxSeqs];        // its cached tokens; -1: not served
+    long long wave_n[kTableThreads / 64], wave_p[kTableThreads / 64];
+    long long carry_n, carry_p, served_p;
+    unsigned status;
+};
+
+__device__ __forceinline__ void scan_requests(const TableArgs& a, Scan& sc) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    if (tid == 0) {
+        sc.carry_n = sc.carry_p = sc.served_p = 0;
+        sc.status = 0;
+    }
+    __syncthreads();
+    const int64_t count = imin(imax(*a.count_in, 0), a.free_capacity);
+    const int64_t page = 1 << a.page_shift;
+    for (int b0 = 0; b0 < a.B; b0 += kTableThreads) {
+        const int b = b0 + tid;
+        const int64_t len = b < a.B ? a.lens_in[b] : 0;
+        const int64_t fresh = b < a.B ? a.new_lens[b] : 0;
+        const Need d = page_need(len, fresh, page, a.max_pages);
+        long long n = fresh > 0 ? fresh : 0, p = d.take;
+        const long long own_n = n, own_p = p;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const long long un = __shfl_up(n, off), up = __shfl_up(p, off);
+            if (lane >= off) {
+                n += un;
+                p += up;
+            }
+        }
+        if (lane == 63) {
+            sc.wave_n[wave] = n;
+            sc.wave_p[wave] = p;
+        }
+        __syncthreads();
+        long long before_n = sc.carry_n, before_p = sc.carry_p;
+        for (int w = 0; w < wave; ++w) {
+            before_n += sc.wave_n[w];
+            before_p += sc.wave_p[w];
+        }
+        const long long start = before_n + n - own_n, ahead = before_p + p - own_p;
+        if (b < a.B) {
+            unsigned st = 0;
+            if (len < 0 || fresh < 0 || start + own_n > a.T) st |= kStatusLength;
+            else if (!d.fits || (own_p > 0 && ahead + own_p > count)) st |= kStatusPagesShort;
+            sc.cu[b] = (int)imin(start, a.T);
+            sc.taken[b] = (int)imin(ahead, INT32_MAX);
+            sc.cached[b] = st ? -1 : (int)len;
+            if (st) atomicOr(&sc.status, st);
+            else if (own_p > 0) atomicMax(&sc.served_p, ahead + own_p);
+        }
+        __syncthreads();
+        if (tid == kTableThreads - 1) {
+            sc.carry_n = before_n + n;
+            sc.carry_p = before_p + p;
+        }
+        __syncthreads();
+    }
+    if (tid == 0) sc.cu[a.B] = (int)imin(sc.carry_n, a.T);
+    __syncthreads();
+}
+
+__device__ __forceinline__ void write_lengths(const TableArgs& a, const Scan& sc) {
+    const int64_t count = imin(imax(*a.count_in, 0), a.free_capacity);
+    for (int b = threadIdx.x; b < a.B; b += kTableThreads) {
+        const int len = a.lens_in[b];
+        a.lens_out[b] = sc.cached[b] < 0 ? len : len + a.new_lens[b];
+    }
+    __syncthreads();                                         // count_out may be count_in
+    if (threadIdx.x == 0) {
+        *a.count_out = (int)(count - sc.served_p);
+        if (sc.status && a.status) atomicOr(a.status, sc.status);
+    }
+}
+
+// WHOLE: one workgroup does everything.  Otherwise the tokens are spread over the workgroups.
+template <bool WHOLE>
+__global__ __launch_bounds__(kTableThreads) void block_tables_kernel(TableArgs a) {
+    __shared__ Scan sc;
+    scan_requests(a, sc);
+    const int64_t count = imin(imax(*a.count_in, 0), a.free_capacity);
+    const int total = sc.cu[a.B];
+    if (blockIdx.x == 0)
+        for (int b = threadIdx.x; b <= a.B; b += kTableThreads) a.cu[b] = sc.cu[b];
+    const int64_t page_size = 1 << a.page_shift;
+    for (int64_t t = (int64_t)blockIdx.x * kTableThreads + threadIdx.x; t < a.T;
+         t += (int64_t)gridDim.x * kTableThreads) {
+        if (t >= total) {
+            a.positions[t] = 0;
+            a.slots[t] = -1;
+            continue;
+        }
+        int lo = 0, hi = a.B;                                // cu[lo] <= t < cu[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (sc.cu[mid] <= t)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        if (sc.cached[lo] < 0) {
+            a.positions[t] = 0;
+            a.slots[t] = -1;
+            continue;
+        }
+        const int64_t pos = (int64_t)sc.cached[lo] + (t - sc.cu[lo]);
+        const int64_t at = pos >> a.page_shift;
+        const int64_t have = ceil_div(sc.cached[lo], page_size);
+        int32_t* entry = a.table + (int64_t)lo * a.max_pages + at;
+        int64_t page;
+        if (at >= have) {
+            page = a.free_pages[count - 1 - (sc.taken[lo] + at - have)];
+            if ((pos & (page_size - 1)) == 0) *entry = (int32_t)page;   // its first token writes it
+        } else {
+            page = *entry;
+        }
+        a.positions[t] = (int32_t)pos;
+        a.slots[t] = page < 0 ? -1 : (page << a.page_shift) + (pos & (page_size - 1));
+    }
+    if (WHOLE) {
+        __syncthreads();
+        write_lengths(a, sc);
+    }
+}
+
+__global__ __launch_bounds__(kTableThreads) void table_lengths_kernel(TableArgs a) {
+    __shared__ Scan sc;
+    scan_requests(a, sc);
+    write_lengths(a, sc);
+}
+
+}  // namespace
+
+hipError_t launch_rope_cache(const RopeArgs& a, bool x_f32, bool fp8, hipStream_t s) {
+    const int64_t items = (int64_t)(a.heads + 2 * a.kv_heads) * (a.head_dim / 16);
+    const dim3 grid((unsigned)a.T, (unsigned)ceil_div(items, kRopeThreads)), block(kRopeThreads);
+    if (x_f32 && fp8)
+        hipLaunchKernelGGL((rope_cache_kernel<true, true>), grid, block, 0, s, a);
+    else if (x_f32)
+        hipLaunchKernelGGL((rope_cache_kernel<true, false>), grid, block, 0, s, a);
+    else if (fp8)
+        hipLaunchKernelGGL((rope_cache_kernel<false, true>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((rope_cache_kernel<false, false>), grid, block, 0, s, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_block_tables(const TableArgs& a, hipStream_t s) {
+    // one workgroup up to 8 tokens a thread; beyond that the tokens take longer than a launch
+    if (a.T <= 8 * kTableThreads) {
+        hipLaunchKernelGGL(block_tables_kernel<true>, dim3(1), dim3(kTableThreads), 0, s, a);
+        return hipGetLastError();
+    }
+    const int64_t wgs = imin(ceil_div(a.T, kTableThreads), 256);
+    hipLaunchKernelGGL(block_tables_kernel<false>, dim3((unsigned)wgs), dim3(kTableThreads), 0, s, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(table_lengths_kernel, dim3(1), dim3(kTableThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace w4

@@ -124,4 +124,99 @@ hipError_t launch_fp8_gemm(const uint8_t* xq, const float* sx, int64_t m, const 
 hipError_t launch_gemm(const uint8_t* prepared, int64_t n, int64_t k, const void* X, int64_t m,
                        void* Y, bool y_bf16, void* workspace, hipStream_t s);
 
+// Rows that the norm and the gate write: values, or 8-bit codes with one scale per row.
+struct RowOut {
+    enum Kind { kF32, kBf16, kFp8, kInt8 };
+    int kind;
+    void* y;            // rows of values or codes
+    float* scales;      // with codes
+    uint32_t* status;   // with codes, optional
+};
+struct RmsnormArgs {
+    const void* x;
+    const void* r;      // residual (optional) and where its sum with x goes (r itself, or apart)
+    void* r_out;
+    const void* w;
+    bool x_f32, r_f32, w_f32;
+    float eps;
+    int64_t rows, K;
+};
+hipError_t launch_rmsnorm(const RmsnormArgs& a, const RowOut& o, hipStream_t s);
+hipError_t launch_silu_mul(const void* gu, bool f32, int64_t rows, int64_t F, const RowOut& o,
+                           hipStream_t s);
+
+// Bits of a device status word (the header's W4_STATUS_* values).
+constexpr uint32_t kStatusNonfinite = 1, kStatusPage = 8, kStatusLength = 16, kStatusPagesShort = 32;
+constexpr int kMaxSeqs = 4096;      // sequences of a batch
+
+struct RopeArgs {
+    const void* qkv;
+    const int32_t* positions;
+    const int64_t* slots;
+    const double* freqs;
+    uint16_t* q;
+    void* k;
+    void* v;
+    float* k_scales;
+    float* v_scales;
+    uint32_t* status;
+    int64_t T, pages;
+    int heads, kv_heads, head_dim, page_shift, rotary, interleaved;
+    float amplitude;
+};
+hipError_t launch_rope_cache(const RopeArgs& a, bool x_f32, bool fp8, hipStream_t s);
+
+struct TableArgs {
+    const int32_t* new_lens;
+    const int32_t* lens_in;
+    const int32_t* free_pages;
+    const int32_t* count_in;
+    int32_t* lens_out;
+    int32_t* count_out;
+    int32_t* table;
+    int32_t* cu;
+    int32_t* positions;
+    int64_t* slots;
+    uint32_t* status;
+    int64_t free_capacity, max_pages, T;
+    int B, page_shift;
+};
+hipError_t launch_block_tables(const TableArgs& a, hipStream_t s);
+
+// Attention: query rows of a tile in the two kernels, keys a part takes at least, parts at most.
+constexpr int kNarrowRows = 32, kWideRows = 256;
+constexpr int kNarrowLeast = 512, kWideLeast = 512, kMaxParts = 128;
+
+struct AttendArgs {
+    const uint16_t* q;
+    uint16_t* o;
+    const void* k;
+    const void* v;
+    const float* k_scales;
+    const float* v_scales;
+    const int32_t* table;
+    const int32_t* cu;
+    const int32_t* lens;
+    uint32_t* status;
+    // of tiles whose keys are split: per part and tile row O / l [head_dim], and m, l
+    float *narrow_o, *wide_o, *narrow_ml, *wide_ml;
+    int64_t narrow_rows, wide_rows;
+    int64_t T, pages, max_pages;
+    int B, heads, kv_heads, group, page_shift, window;
+    float scale_log2;    // softmax scale / ln 2
+    int narrow_parts, wide_parts;
+    bool both;           // both kernels are launched
+};
+// What the host knows of a call decides the launches; the parts that a tile really has follow
+// from the lengths on the device.
+struct AttendPlan {
+    int64_t narrow_tiles, wide_tiles;   // workgroups of one part
+    int narrow_parts, wide_parts;
+    bool both;
+};
+void plan_attend(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int64_t capacity, AttendPlan* p);
+size_t attend_workspace(int64_t D, const AttendPlan& p);
+hipError_t launch_attend(AttendArgs a, int head_dim, bool fp8, const AttendPlan& p, void* workspace,
+                         hipStream_t s);
+
 }  // namespace w4

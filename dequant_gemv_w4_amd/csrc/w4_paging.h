@@ -1,0 +1,98 @@
+// Index arithmetic of the paged cache and of the attention's work split, in plain C++ so that
+// the kernels and a host program share it.
+//
+// A sequence b has the query rows cu[b] .. cu[b+1] of the packed batch and lens[b] keys, its new
+// tokens' among them.  Its key j lies in row j % page of page table[b][j / page].  Query t of a
+// sequence with n new tokens stands at position lens - n + t and sees the keys up to itself,
+// with a window the last `window` of them.
+//
+// Attention works on tiles of R rows, one kv head each: row r of a sequence is head r % G of its
+// token r / G (G query heads share a kv head), so that one pass over the keys serves all of them.
+#pragma once
+
+#include <stdint.h>
+
+#ifdef __HIPCC__
+#define W4_HD __host__ __device__ __forceinline__
+#else
+#define W4_HD inline
+#endif
+
+namespace w4 {
+
+W4_HD int64_t imin(int64_t a, int64_t b) { return a < b ? a : b; }
+W4_HD int64_t imax(int64_t a, int64_t b) { return a > b ? a : b; }
+W4_HD int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// First tile of sequence b when the tiles of all sequences are numbered without knowing their
+// lengths: floor(cu[b] G / R) + b.  It grows by at least ceil(n G / R) and at least 1 from one
+// sequence to the next (floor(a + c) - floor(a) + 1 >= ceil(c)); numbers past a sequence's
+// tiles stay idle.  All tiles lie below floor(T G / R) + B.
+W4_HD int64_t first_tile(int64_t cu_b, int64_t b, int64_t G, int64_t R) { return cu_b * G / R + b; }
+W4_HD int64_t tile_bound(int64_t T, int64_t B, int64_t G, int64_t R) { return T * G / R + B; }
+
+// A sequence as the kernels read it, whatever the arrays hold: its rows lie in [0, T) and its
+// keys in the table.
+struct Seq {
+    int64_t start;   // first query row
+    int64_t n;       // query rows
+    int64_t ctx;     // keys
+};
+W4_HD Seq clamp_seq(int64_t cu0, int64_t cu1, int64_t len, int64_t T, int64_t capacity) {
+    Seq s;
+    s.start = imin(imax(cu0, 0), T);
+    s.n = imax(imin(cu1, T) - s.start, 0);
+    s.ctx = imin(imax(len, 0), capacity);
+    return s;
+}
+
+// Keys of a tile of rows [row0, row0 + rows) of a sequence (rows >= 1), and their split:
+// [begin, end) is what any row sees, begin rounded down to a multiple of kKeyTile; part p of
+// `parts` takes [begin + p * chunk, begin + (p + 1) * chunk).  The parts are cut by the actual
+// lengths, at least `least` keys each, whatever number the launch allows.
+constexpr int kKeyTile = 64;
+struct Span {
+    int64_t begin, end, chunk;
+    int parts;
+};
+W4_HD Span key_span(const Seq& s, int64_t row0, int64_t rows, int64_t G, int64_t window,
+                    int64_t max_parts, int64_t least) {
+    Span k;
+    const int64_t pos0 = s.ctx - s.n;                        // position of the first new token
+    k.end = imin(s.ctx, pos0 + (row0 + rows - 1) / G + 1);
+    k.begin = window > 0 ? imax(0, pos0 + row0 / G - window + 1) / kKeyTile * kKeyTile : 0;
+    if (k.end <= k.begin) {
+        k.end = k.begin;
+        k.chunk = least;
+        k.parts = 1;
+        return k;
+    }
+    const int64_t len = k.end - k.begin;
+    k.chunk = imax(least, ceil_div(ceil_div(len, max_parts), kKeyTile) * kKeyTile);
+    k.parts = (int)ceil_div(len, k.chunk);
+    return k;
+}
+
+// Number of a page if the cache has it, else -1.
+W4_HD int64_t checked_page(int64_t page, int64_t pages) { return page >= 0 && page < pages ? page : -1; }
+
+// Pages that a request takes for its new tokens: the list has `count` pages left, `before` of
+// them are taken by the requests ahead of it (those that were served or would have been).
+struct Need {
+    int64_t have;    // pages of the cached tokens
+    int64_t take;    // pages more
+    bool fits;       // lengths valid, table wide enough
+};
+W4_HD Need page_need(int64_t len, int64_t fresh, int64_t page, int64_t max_pages) {
+    Need d;
+    d.have = d.take = 0;
+    d.fits = len >= 0 && fresh >= 0;
+    if (!d.fits) return d;
+    d.have = ceil_div(len, page);
+    const int64_t want = ceil_div(len + fresh, page);
+    d.fits = want <= max_pages && len + fresh <= INT32_MAX;
+    d.take = d.fits ? want - d.have : 0;
+    return d;
+}
+
+}  // namespace w4

@@ -54,6 +54,10 @@ extern "C" {
 #define W4_GEMV_MAX_K 32768
 #define W4_FP8_MAX_K 65536
 #define W4_GEMM_MAX_K (1 << 20)
+#define W4_ROWS_MAX_K 65536
+#define W4_MAX_SEQUENCES 4096
+#define W4_MAX_TOKENS (1 << 22)
+#define W4_MAX_CONTEXT (1 << 30)
 
 typedef enum {
     W4_OK = 0,
@@ -65,15 +69,20 @@ typedef enum {
     W4_ERR_ARCH = 6,         /* current device is not gfx950 */
     W4_ERR_WORKSPACE = 7,    /* workspace missing or too small */
     W4_ERR_HIP = 8,          /* HIP runtime error; see w4_last_hip_error() */
-    W4_ERR_BUFFER = 9        /* destination buffer smaller than required */
+    W4_ERR_BUFFER = 9,       /* destination buffer smaller than required */
+    W4_ERR_VALUE = 10        /* a number outside its range (eps, a scale, a window, a rope record) */
 } w4_status;
 
 typedef enum { W4_F32 = 0, W4_BF16 = 1 } w4_dtype;
 
-/* Device status word bits written by w4_quantize (OR-ed, never cleared). */
+/* Device status word bits (OR-ed, never cleared), written by w4_quantize and, the last three,
+ * by the paged-cache calls. */
 #define W4_STATUS_NONFINITE      1u  /* a weight was NaN or +-inf (outputs undefined) */
 #define W4_STATUS_SCALE_OVERFLOW 2u  /* a binary32 scale rounded to binary16 infinity */
 #define W4_STATUS_SCALE_ZERO     4u  /* a non-empty group's scale rounded to binary16 zero */
+#define W4_STATUS_PAGE           8u  /* a page or slot number outside the cache */
+#define W4_STATUS_LENGTH        16u  /* a negative length, or more new tokens than the arrays hold */
+#define W4_STATUS_PAGES_SHORT   32u  /* a request found too few free pages or table entries */
 
 /*
  * w4_quantize -- round-to-nearest quantization of W (page "Weight quantization",
@@ -319,6 +328,188 @@ w4_status w4_int8_quantize_rows(const void* A, w4_dtype at, int64_t rows, int64_
 w4_status w4_int8_gemm(const int8_t* xq, const float* sx, int64_t M, const int8_t* wq,
                        const float* sw, int64_t N, int64_t K, void* Y, w4_dtype yt,
                        hipStream_t stream);
+
+/*
+ * Operators between the products of a decoder layer.  They take what the products write and
+ * write what the products take: binary32 or bfloat16 rows, or 8-bit codes with row scales.
+ *
+ * w4_rmsnorm -- root-mean-square norm of rows, with the residual's addition.
+ *   h = x + residual, rounded to the residual's type and written to residual_out;
+ *   y[i] = h[i] * s * weight[i], s = 1 / sqrt(mean(h^2) + eps) (sum in binary64, s and the
+ *   products in binary32).  Without a residual h = x.
+ *   x             [rows, K] binary32 or bfloat16.   weight  [K] binary32 or bfloat16.
+ *   residual      [rows, K] binary32 or bfloat16, or NULL.
+ *   residual_out  [rows, K] of the residual's type; may be residual itself (in place); NULL
+ *                 with residual, and only then.
+ *   y             [rows, K] binary32 or bfloat16.
+ * w4_rmsnorm_fp8, w4_rmsnorm_int8 -- the same y, quantized per row without being stored: codes
+ *   [rows, K] and scales [rows] as w4_fp8_quantize_rows / w4_int8_quantize_rows write them for
+ *   the binary32 y, bit for bit; d_status (optional) receives W4_STATUS_NONFINITE.
+ * Requires rows >= 1, K a multiple of 128, 128 <= K <= W4_ROWS_MAX_K, eps finite and > 0
+ * (W4_ERR_VALUE).  All arrays 16-B aligned (scales, d_status 4-B); outputs must not overlap
+ * inputs except residual_out as stated.  Deterministic.
+ */
+w4_status w4_rmsnorm(const void* x, w4_dtype xt, const void* residual, void* residual_out,
+                     w4_dtype rt, const void* weight, w4_dtype wt, float eps, int64_t rows,
+                     int64_t K, void* y, w4_dtype yt, hipStream_t stream);
+w4_status w4_rmsnorm_fp8(const void* x, w4_dtype xt, const void* residual, void* residual_out,
+                         w4_dtype rt, const void* weight, w4_dtype wt, float eps, int64_t rows,
+                         int64_t K, uint8_t* codes, float* scales, uint32_t* d_status,
+                         hipStream_t stream);
+w4_status w4_rmsnorm_int8(const void* x, w4_dtype xt, const void* residual, void* residual_out,
+                          w4_dtype rt, const void* weight, w4_dtype wt, float eps, int64_t rows,
+                          int64_t K, int8_t* codes, float* scales, uint32_t* d_status,
+                          hipStream_t stream);
+
+/*
+ * w4_silu_mul -- the gate between the fused gate|up product and the down product:
+ *   y[r, i] = g / (1 + exp(-g)) * u in binary32, g = gate_up[r, i], u = gate_up[r, F + i].
+ *   gate_up  [rows, 2F] binary32 or bfloat16.   y  [rows, F] binary32 or bfloat16.
+ * w4_silu_mul_fp8, w4_silu_mul_int8 -- the same y as codes [rows, F] and scales [rows], as above.
+ * Requires F a multiple of 128, 128 <= F <= W4_ROWS_MAX_K.  Alignment, errors as w4_rmsnorm.
+ */
+w4_status w4_silu_mul(const void* gate_up, w4_dtype gt, int64_t rows, int64_t F, void* y,
+                      w4_dtype yt, hipStream_t stream);
+w4_status w4_silu_mul_fp8(const void* gate_up, w4_dtype gt, int64_t rows, int64_t F,
+                          uint8_t* codes, float* scales, uint32_t* d_status, hipStream_t stream);
+w4_status w4_silu_mul_int8(const void* gate_up, w4_dtype gt, int64_t rows, int64_t F,
+                           int8_t* codes, float* scales, uint32_t* d_status, hipStream_t stream);
+
+/*
+ * A paged cache of keys and values.  Row j of page p and kv head h is row
+ * (p * kv_heads + h) * page_size + j of k and v, head_dim elements; a slot is
+ * p * page_size + j.
+ *   type       W4_CACHE_BF16: bfloat16 rows; W4_CACHE_FP8: E4M3 codes, one binary32 scale per
+ *              row in k_scales and v_scales [pages, kv_heads, page_size] (NULL otherwise).
+ *   page_size  a power of two, 16 to 4096.   head_dim  64 or 128.   kv_heads  1 to 1024.
+ * k and v 16-B aligned, scales 4-B.  W4_ERR_UNSUPPORTED for another type, page size or head
+ * dimension.  pages >= 1; kv_heads * page_size * pages < 2^40.
+ */
+typedef enum { W4_CACHE_BF16 = 0, W4_CACHE_FP8 = 1 } w4_cache_type;
+typedef struct {
+    void* k;
+    void* v;
+    float* k_scales;
+    float* v_scales;
+    int64_t pages;
+    int32_t page_size;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t type;
+} w4_kv_cache;
+
+/*
+ * Rotary positions.  Pair i (0 <= i < rotary_dim / 2) of a head turns by position * f[i], with
+ * f[i] = base^(-2 i / rotary_dim) and, for contexts longer than the original_positions trained:
+ *   W4_ROPE_NONE    f as it is.
+ *   W4_ROPE_LINEAR  f / factor.
+ *   W4_ROPE_BANDS   by the turns t = original_positions * f / (2 pi): f / factor where t <= low,
+ *                   f where t >= high, between them f * (k + (1 - k) / factor) with
+ *                   k = (t - low) / (high - low).
+ *   W4_ROPE_RAMP    f * (1 - r + r / factor), r rising from 0 to 1 between the pairs
+ *                   floor(c(high)) (at least 0) and ceil(c(low)) (at most rotary_dim - 1;
+ *                   0.001 more if both are the same), c(t) = rotary_dim *
+ *                   ln(original_positions / (2 pi t)) / (2 ln base); cosines and sines are
+ *                   multiplied by the amplitude 1 + 0.1 ln(factor).
+ *   rotary_dim   elements of a head that turn: a multiple of 16 (the rest stays as it is).
+ *   interleaved  0: pairs (i, i + rotary_dim / 2); 1: pairs (2i, 2i + 1).
+ * Requires base > 1, factor >= 1 (but for NONE), and for BANDS and RAMP 0 < low < high and
+ * original_positions >= 1; all finite (W4_ERR_VALUE).
+ *
+ * w4_rope_frequencies -- f on the host, binary64: freqs [rotary_dim / 2]; *amplitude (may be
+ *   NULL) is 1 except for RAMP.  No device work.
+ *
+ * w4_rope_cache -- rotates the rows of the fused q|k|v product and stores K and V in the cache.
+ *   qkv        [T, (heads + 2 kv_heads) * head_dim] binary32 or bfloat16: the query heads, the
+ *              key heads, the value heads; 16-B aligned.
+ *   positions  [T] device.   slots  [T] device: where the token's K and V go.  A token with a
+ *              negative slot is padding: neither its q nor the cache is written; one with a slot
+ *              past the cache is skipped too and sets W4_STATUS_PAGE.  Slots must differ from
+ *              each other (two tokens with one slot leave either's values, element by element).
+ *   d_freqs    [rotary_dim / 2] device binary64 from w4_rope_frequencies; 8-B aligned.
+ *   q          out [T, heads, head_dim] bfloat16; 16-B aligned; must not overlap qkv.
+ * Angles are formed in binary64, rotations in binary32, results rounded once: q and a bfloat16
+ * cache to nearest even, rows of an E4M3 cache as w4_fp8_quantize_rows with K = head_dim would
+ * the binary32 row (d_status: W4_STATUS_NONFINITE).  Requires 1 <= T <= W4_MAX_TOKENS,
+ * heads a multiple of kv_heads, T * heads < 2^26, rotary_dim <= head_dim.
+ */
+typedef enum { W4_ROPE_NONE = 0, W4_ROPE_LINEAR = 1, W4_ROPE_BANDS = 2, W4_ROPE_RAMP = 3 } w4_rope_scaling;
+typedef struct {
+    int32_t rotary_dim;
+    int32_t interleaved;
+    int32_t scaling;
+    int32_t reserved;            /* 0 */
+    double base;
+    double factor;
+    double low;
+    double high;
+    int64_t original_positions;
+} w4_rope;
+w4_status w4_rope_frequencies(const w4_rope* rope, double* freqs, double* amplitude);
+w4_status w4_rope_cache(const void* qkv, w4_dtype xt, int64_t T, int64_t heads,
+                        const w4_kv_cache* cache, const int32_t* positions, const int64_t* slots,
+                        const w4_rope* rope, const double* d_freqs, void* q, uint32_t* d_status,
+                        hipStream_t stream);
+
+/*
+ * w4_block_tables -- places the new tokens of a batch of requests in pages, on the device.
+ * Request b has lens_in[b] cached tokens in the pages that row b of block_table names, and
+ * new_lens[b] tokens more in this step; the batch packs the new tokens request by request.
+ *   free_pages   [free_capacity] page numbers, of which the first *free_count_in are free; pages
+ *                are taken from the end.
+ *   lens_out     [B] lens_in + new_lens (may be lens_in).
+ *   free_count_out  pages left (may be free_count_in).
+ *   block_table  [B, max_pages], in and out: entries of newly taken pages are written.
+ *   cu_q         out [B + 1]: first new token of each request in the batch; cu_q[B] their number.
+ *   positions, slots  out [T]: of each new token; 0 and -1 behind the last one.
+ * A request whose length is negative or whose tokens do not end within T (W4_STATUS_LENGTH), or
+ * whose pages do not fit its table row, or are not there once the requests ahead of it are
+ * served (W4_STATUS_PAGES_SHORT), is left as it is: it takes no page, its length stays and its
+ * tokens get position 0 and slot -1; cu_q still counts them.  A negative new length counts as
+ * none, a taken page with a negative number gives slot -1.
+ * Requires 1 <= B <= W4_MAX_SEQUENCES, 1 <= T <= W4_MAX_TOKENS, page_size as in w4_kv_cache,
+ * max_pages * page_size <= W4_MAX_CONTEXT, free_capacity >= 0; int32 arrays 4-B aligned, slots
+ * 8-B.  Outputs must not overlap inputs except as stated.  Deterministic.
+ */
+w4_status w4_block_tables(const int32_t* new_lens, const int32_t* lens_in, int64_t B,
+                          const int32_t* free_pages, int64_t free_capacity,
+                          const int32_t* free_count_in, int32_t* lens_out,
+                          int32_t* free_count_out, int32_t* block_table, int64_t max_pages,
+                          int32_t page_size, int32_t* cu_q, int32_t* positions, int64_t* slots,
+                          int64_t T, uint32_t* d_status, hipStream_t stream);
+
+/*
+ * w4_paged_attention -- attention of the new tokens of each request over its cached tokens, the
+ * new ones among them (w4_rope_cache has stored them):
+ *   o = sum_j p_j v_j / sum_j p_j, p_j = exp(scale * q . k_j), over the keys j <= position, with
+ *   a window the last `window` of them.
+ * Token t of request b (rows cu_q[b] .. cu_q[b+1] of the batch) has position
+ * lens[b] - (cu_q[b+1] - cu_q[b]) + t.  Query head h reads kv head h / (heads / kv_heads).
+ *   q            [T, heads, head_dim] bfloat16; 16-B aligned.
+ *   block_table  [B, max_pages] device; cu_q [B + 1], lens [B] device (as w4_block_tables
+ *                writes them: lens counts the new tokens).
+ *   scale        finite, > 0.   window  0 (none) or >= 1.   (else W4_ERR_VALUE)
+ *   o            out [T, heads, head_dim] bfloat16; 16-B aligned; must not overlap q.  Rows that
+ *                belong to no request stay as they are; a row that sees no key gets zeros.
+ *   workspace    w4_paged_attention_workspace_bytes(...) bytes of device scratch (may be 0),
+ *                16-B aligned; contents need no initialisation.  Calls (and captured graphs)
+ *                sharing a workspace must be ordered.
+ * A key in a page that the cache does not have reads as zeros (K and V) and sets W4_STATUS_PAGE
+ * in d_status (optional).  What lies in the cache behind a request's keys, and at keys that a
+ * row does not see, does not reach the row, NaN and infinities included.
+ * Scores, softmax sums and outputs are formed in binary32; the weights are rounded to bfloat16
+ * for the matrix units and o once.  Deterministic; the split of the work depends on the
+ * arguments and lengths only.
+ * Requires 1 <= T <= W4_MAX_TOKENS, 1 <= B <= W4_MAX_SEQUENCES, heads a multiple of kv_heads,
+ * T * heads < 2^26, 1 <= max_pages, max_pages * page_size <= W4_MAX_CONTEXT.
+ */
+size_t w4_paged_attention_workspace_bytes(int64_t T, int64_t heads, const w4_kv_cache* cache,
+                                          int64_t B, int64_t max_pages);
+w4_status w4_paged_attention(const void* q, int64_t T, int64_t heads, const w4_kv_cache* cache,
+                             const int32_t* block_table, int64_t max_pages, const int32_t* cu_q,
+                             const int32_t* lens, int64_t B, float scale, int64_t window, void* o,
+                             void* workspace, size_t workspace_bytes, uint32_t* d_status,
+                             hipStream_t stream);
 
 /*
  * w4_stream_read -- measurement probe, not part of the method: reads `bytes` bytes of

@@ -19,3 +19,7 @@ from .fp8_oracle import (  # noqa: F401
 from .int8_oracle import (  # noqa: F401
     INT8_MAX, quantize_rows_int8_ref, dequant_int8_ref, gemm_int8_ref, tolerance_int8_ref,
 )
+from .layer_oracle import (  # noqa: F401
+    bf16_round, residual_sum_ref, rmsnorm_ref, silu_mul_ref, rope_frequencies_ref, rope_ref,
+    block_tables_ref, attention_ref,
+)
