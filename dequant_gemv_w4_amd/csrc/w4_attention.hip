@@ -459,33 +459,41 @@ __global__ __launch_bounds__(kWideThreads, 2) void attend_wide_kernel(AttendArgs
 
     const int k0 = (int)t.k0, k1 = (int)t.k1;
     const int tiles = (k1 - k0 + kKeyTile - 1) / kKeyTile;
+    const int page_mask = (1 << a.page_shift) - 1;
     const int crow = tid / kChunks, chunk = tid % kChunks;
     const bool loads = crow < kKeyTile;                      // more threads than chunks of a tile
-    int64_t at[kLoads];                                      // cache rows of the tile after next
+    // The rows that one load of a wave covers lie in one aligned group of 16, so in one page.
+    const int granule = __builtin_amdgcn_readfirstlane(crow & ~15);
+    const int32_t* table = a.table + (int64_t)t.b * a.max_pages;
+    int entry[kLoads];                                       // table entries of the next tile
     u32x4_t kw[kLoads], vw[kLoads];
     float sc = 1.0f;
     bool keep[kLoads], bad_page = false;
-    auto look_up = [&](int i) {
+    auto look_up = [&](int i, int* e) {                      // read here, used a tile later
 #pragma unroll
         for (int c = 0; c < kLoads; ++c) {
             const int key = k0 + i * kKeyTile + crow + c * kStepRows;
-            at[c] = -2;
-            if (loads && key < k1) {
-                at[c] = key_row(a, t.b, kv, key);
-                bad_page |= at[c] == -1;
-            }
+            e[c] = table[(key < k1 ? key : k1 - 1) >> a.page_shift];
         }
     };
-    auto fetch = [&]() {                                     // rows found by look_up
+    auto fetch = [&](int i, const int* e) {
 #pragma unroll
         for (int c = 0; c < kLoads; ++c) {
-            keep[c] = at[c] >= 0;
-            const int64_t row = keep[c] ? at[c] : 0;         // the cache has at least one row
-            kw[c] = *reinterpret_cast<const u32x4_t*>(static_cast<const uint8_t*>(a.k) + row * kRowBytes + 16 * chunk);
-            vw[c] = *reinterpret_cast<const u32x4_t*>(static_cast<const uint8_t*>(a.v) + row * kRowBytes + 16 * chunk);
+            const int first = k0 + i * kKeyTile + granule + c * kStepRows;   // key of the group's first row
+            const int64_t page = checked_page(__builtin_amdgcn_readfirstlane(e[c]), a.pages);
+            const bool there = loads && first < k1;
+            bad_page |= there && page < 0;
+            keep[c] = page >= 0 && k0 + i * kKeyTile + crow + c * kStepRows < k1;
+            // another page's rows stand in for those of a page that is not there; put() drops them
+            const int64_t row0 = there && page >= 0 ? ((page * a.kv_heads + kv) << a.page_shift) + (first & page_mask) : 0;
+            const int lane_row = loads ? crow & 15 : 0;
+            const uint8_t* kp = static_cast<const uint8_t*>(a.k) + row0 * kRowBytes;
+            const uint8_t* vp = static_cast<const uint8_t*>(a.v) + row0 * kRowBytes;
+            kw[c] = *reinterpret_cast<const u32x4_t*>(kp + lane_row * kRowBytes + 16 * chunk);
+            vw[c] = *reinterpret_cast<const u32x4_t*>(vp + lane_row * kRowBytes + 16 * chunk);
             if constexpr (FP8) {
                 static_assert(kLoads == 1, "one row a thread");
-                if (chunk < 2) sc = keep[c] ? (chunk == 0 ? a.k_scales : a.v_scales)[row] : 1.0f;
+                sc = (chunk & 1 ? a.v_scales : a.k_scales)[row0 + lane_row];
             }
         }
     };
@@ -497,21 +505,24 @@ __global__ __launch_bounds__(kWideThreads, 2) void attend_wide_kernel(AttendArgs
             stage<D, FP8, true>(vt[buf], crow + c * kStepRows, chunk, vw[c], keep[c]);
         }
         if constexpr (FP8) {
-            if (chunk < 2) (chunk == 0 ? ksc[buf] : vsc[buf])[crow] = sc;
+            if (chunk < 2) (chunk == 0 ? ksc[buf] : vsc[buf])[crow] = keep[0] ? sc : 1.0f;
         }
     };
     if (tiles > 0) {
-        look_up(0);
-        fetch();
-        look_up(1);
+        look_up(0, entry);
+        fetch(0, entry);
+        look_up(1, entry);
         put(0);
     }
     __syncthreads();
     for (int i = 0; i < tiles; ++i) {
         const int buf = i & 1;
         if (i + 1 < tiles) {
-            fetch();
-            look_up(i + 2);
+            int later[kLoads];
+            look_up(i + 2, later);                           // ahead of the rows, whose wait covers it
+            fetch(i + 1, entry);
+#pragma unroll
+            for (int c = 0; c < kLoads; ++c) entry[c] = later[c];
         }
         const int first = k0 + i * kKeyTile, last = first + kKeyTile - 1;
         if (first <= any_hi && last >= any_lo)
@@ -564,7 +575,7 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void attend_narrow_kernel(Attend
     __shared__ __attribute__((aligned(16))) float scales[kNarrowWaves][2 * kKeys];
     __shared__ float sm[kNarrowWaves][32], sl[kNarrowWaves][32];
     static_assert(2 * kTileBytes == 32 * D * 4, "O fits the tiles' place");
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int part = blockIdx.y;
     int kv;
     const Tile t = find_tile<false>(a, blockIdx.x, part, kv);
@@ -585,48 +596,55 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void attend_narrow_kernel(Attend
     const int k0 = (int)t.k0, k1 = (int)t.k1;
     uint8_t* kt = tiles_lds[wave];
     uint8_t* vt = kt + kTileBytes;
+    const int page_mask = (1 << a.page_shift) - 1;
     const int crow = lane / kChunks, chunk = lane % kChunks;
     // A page holds 16 keys at least and tiles begin at multiples of 32, so either half of a tile
     // lies in one page: two lookups a tile, the same for all lanes.
-    int64_t base[2];                                         // cache row of each half's first key
+    const int32_t* table = a.table + (int64_t)t.b * a.max_pages;
+    int entry[2];                                            // table entries of the next tile
     u32x4_t kw[kLoads], vw[kLoads];
     float sc = 1.0f;
     bool bad_page = false, ok[2] = {false, false};
-    auto look_up = [&](int i) {
+    auto look_up = [&](int i, int* e) {                      // read here, used a tile later
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int key = k0 + i * kKeys + 16 * h;
-            base[h] = -2;
-            if (key < k1) {
-                base[h] = key_row(a, t.b, kv, key);
-                bad_page |= base[h] == -1;
-            }
+            e[h] = table[(key < k1 ? key : k1 - 1) >> a.page_shift];
         }
     };
-    auto fetch = [&]() {
+    auto fetch = [&](int i, const int* e) {
+        int64_t base[2];                                     // cache row of each half's first key
 #pragma unroll
-        for (int h = 0; h < 2; ++h) ok[h] = base[h] >= 0;
+        for (int h = 0; h < 2; ++h) {
+            const int key = k0 + i * kKeys + 16 * h;
+            const int64_t page = checked_page(__builtin_amdgcn_readfirstlane(e[h]), a.pages);
+            bad_page |= key < k1 && page < 0;
+            ok[h] = key < k1 && page >= 0;
+            // another page's rows stand in for those of a page that is not there
+            base[h] = ok[h] ? ((page * a.kv_heads + kv) << a.page_shift) + (key & page_mask) : 0;
+        }
 #pragma unroll
         for (int c = 0; c < kLoads; ++c) {
-            const int row = c * kStepRows + crow, h = (c * kStepRows) >> 4;
-            const int64_t at = (ok[h] ? base[h] : 0) + (row & 15);   // a page has 16 rows at least
-            kw[c] = *reinterpret_cast<const u32x4_t*>(static_cast<const uint8_t*>(a.k) + at * kRowBytes + 16 * chunk);
-            vw[c] = *reinterpret_cast<const u32x4_t*>(static_cast<const uint8_t*>(a.v) + at * kRowBytes + 16 * chunk);
+            const int row = (c * kStepRows + crow) & 15;
+            const int64_t from = base[(c * kStepRows) >> 4] * kRowBytes;
+            kw[c] = *reinterpret_cast<const u32x4_t*>(static_cast<const uint8_t*>(a.k) + from + row * kRowBytes + 16 * chunk);
+            vw[c] = *reinterpret_cast<const u32x4_t*>(static_cast<const uint8_t*>(a.v) + from + row * kRowBytes + 16 * chunk);
         }
         if constexpr (FP8) {
-            const int key = lane & 31, h = key >> 4;
-            const int64_t at = (ok[h] ? base[h] : 0) + (key & 15);
+            const int64_t at = (lane & 16 ? base[1] : base[0]) + (lane & 15);
             sc = (lane < 32 ? a.k_scales : a.v_scales)[at];
         }
     };
     const int tiles = (k1 - k0 + kKeys - 1) / kKeys;
     if (wave < tiles) {
-        look_up(wave);
-        fetch();
-        look_up(wave + kNarrowWaves);
+        look_up(wave, entry);
+        fetch(wave, entry);
+        look_up(wave + kNarrowWaves, entry);
     }
     for (int i = wave; i < tiles; i += kNarrowWaves) {
         const int first = k0 + i * kKeys;
+        int later[2];
+        look_up(i + 2 * kNarrowWaves, later);                // there by the time these rows are
 #pragma unroll
         for (int c = 0; c < kLoads; ++c) {
             const int row = c * kStepRows + crow;
@@ -636,8 +654,9 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void attend_narrow_kernel(Attend
         }
         if constexpr (FP8) scales[wave][lane] = ok[(lane & 31) >> 4] && first + (lane & 31) < k1 ? sc : 1.0f;
         if (i + kNarrowWaves < tiles) {
-            fetch();
-            look_up(i + 2 * kNarrowWaves);
+            fetch(i + kNarrowWaves, entry);
+            entry[0] = later[0];
+            entry[1] = later[1];
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // rows staged by other lanes
         attend_step<D, FP8, 1>(s, kt, vt, scales[wave], scales[wave] + kKeys, a.scale_log2, first, p.lo, p.hi,
@@ -721,21 +740,32 @@ __global__ __launch_bounds__(256) void combine_kernel(AttendArgs a) {
     if (!t.run || t.span.parts == 1 || t.row0 + r >= t.rows) return;
     const Place place = row_place(a, t, kv, t.row0 + r);
     const Parts<WIDE> w(a);
-    float m = kNegInf;
-    for (int p = lane; p < t.span.parts; p += 64) m = fmaxf(m, w.ml[2 * w.at(t, p, r)]);
+    // lane p weighs part p (kMaxParts is 64): 2^(m_p - m) l_p, 0 where the part has nothing of weight
+    const int parts = t.span.parts;
+    float mp = kNegInf, lp = 0.0f;
+    if (lane < parts) {
+        const int64_t at = w.at(t, lane, r);
+        mp = w.ml[2 * at];
+        lp = w.ml[2 * at + 1];
+    }
+    float m = mp;
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
-    float sum = 0.0f, o[E];
+    const float f = lp == 0.0f ? 0.0f : exp2_fast(mp - m) * lp;   // NaN where lp or mp is
+    float sum = f;
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
+    float o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.0f;
-    for (int p = 0; p < t.span.parts; ++p) {
-        const int64_t at = w.at(t, p, r);
-        const float mp = w.ml[2 * at], lp = w.ml[2 * at + 1];
-        if (lp == 0.0f) continue;                            // nothing of weight in this part
-        const float f = exp2_fast(mp - m) * lp;              // NaN where lp or mp is
-        sum += f;
+#pragma unroll 8
+    for (int p = 0; p < parts; ++p) {
+        const float fp = __shfl(f, p);
+        float x[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] += f * w.o[at * D + lane * E + e];
+        for (int e = 0; e < E; ++e) x[e] = w.o[w.at(t, p, r) * D + lane * E + e];
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] += fp == 0.0f ? 0.0f : fp * x[e];
     }
     const float inv = inverse(sum, place.hi >= 0);
     if constexpr (E == 2)
