@@ -120,5 +120,58 @@ __device__ __forceinline__ uint2 w8_codes8(const float* v, double s, float rs, b
     return make_uint2(lo, hi);
 }
 
+// The same codes for the kernels that have 8 values of a row in registers, with one branch for
+// all of them.  E4M3: t = v * r32 is within 2^-23 relative of v / s, and rounding is monotonic,
+// so where t (1 - 2^-21) and t (1 + 2^-21) have the same byte it is the byte of v / s; about one
+// value in 10^5 differs and sends the 8 to the binary64 quotients.  The conversion instruction
+// rounds halves to even, subnormals included, and keeps the sign of a value that rounds to zero;
+// the 0 added to the product makes an exact -0 the code 0x00.  INT8: v * r32 + 1.5 * 2^23 in one
+// FMA leaves the nearest integer i in the low bits (halves to even), and v * r32 - i in another
+// how far it is; within 2^-15 of a half (r32 accounts for 127 * 2^-24) the quotient decides.
+template <bool INT8>
+__device__ __forceinline__ uint2 w8_codes8_of(const float* v, double s, float rs, bool rcp_ok) {
+    uint32_t w[2];
+    if constexpr (INT8) {
+        float far = 0.0f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t b[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float x = v[4 * h + q];
+                const float i = fmaf(x, rs, 0x1.8p23f);
+                b[q] = __float_as_uint(i);
+                far = fmaxf(far, fabsf(fmaf(x, rs, 0x1.8p23f - i)));
+            }
+            // byte 0 of each word
+            w[h] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[3], b[2], 0x0c0c0400u),
+                                         __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u), 0x05040100u);
+        }
+        if (rcp_ok && far < 0.5f - 0x1p-15f) return make_uint2(w[0], w[1]);
+    } else {
+        uint32_t differ = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            int lo = 0, hi = 0;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const float t0 = fmaf(v[4 * h + 2 * q], rs, 0.0f), t1 = fmaf(v[4 * h + 2 * q + 1], rs, 0.0f);
+                const float k0 = 1.0f - 0x1p-21f, k1 = 1.0f + 0x1p-21f;
+                if (q == 0) {
+                    lo = __builtin_amdgcn_cvt_pk_fp8_f32(t0 * k0, t1 * k0, lo, false);
+                    hi = __builtin_amdgcn_cvt_pk_fp8_f32(t0 * k1, t1 * k1, hi, false);
+                } else {
+                    lo = __builtin_amdgcn_cvt_pk_fp8_f32(t0 * k0, t1 * k0, lo, true);
+                    hi = __builtin_amdgcn_cvt_pk_fp8_f32(t0 * k1, t1 * k1, hi, true);
+                }
+            }
+            differ |= (uint32_t)(lo ^ hi);
+            w[h] = (uint32_t)lo;
+        }
+        if (rcp_ok && differ == 0) return make_uint2(w[0], w[1]);
+    }
+    return w8_codes8<INT8>(v, s, rs, rcp_ok);
+}
+
 }  // namespace
 }  // namespace w4

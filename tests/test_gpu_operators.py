@@ -154,6 +154,32 @@ def test_silu_mul_extremes():
     assert int(st) == 1
 
 
+@pytest.mark.parametrize("kind", ["fp8", "int8"])
+@pytest.mark.parametrize("top", [1.0, 0.37, 2.0 ** -110, 3.0e30])
+def test_codes_at_and_next_to_rounding_boundaries(kind, top):
+    # silu(64) is 64 in binary32, so y = 64 * u takes any value: quotients at the midpoints between
+    # neighbouring codes (exact ties where the scale is a power of two) and up to 40 binary32 ulps
+    # around them, zeros of either sign and values that round to zero
+    grid = oracle.E4M3_VALUES[:0x7F] if kind == "fp8" else np.arange(128.0)
+    most = grid[-1]
+    mids = (grid[:-1] + grid[1:]) / 2
+    base = np.concatenate([mids, grid])
+    near = [base.astype(np.float32)]
+    for n in (1, 2, 3, 7, 20, 40):
+        near += [(base * (1 + n * 2.0 ** -23)).astype(np.float32), (base * (1 - n * 2.0 ** -24)).astype(np.float32)]
+    v = np.concatenate(near)
+    v = np.concatenate([v, -v, [0.0, -0.0, 1e-6, -1e-6, 1e-12, -1e-12, 1e-30, -1e-30, most]]).astype(np.float32)
+    v = np.minimum(np.maximum(v, -most), most).astype(np.float64) * top
+    k = -(-len(v) // 128) * 128
+    u = np.zeros((1, k), np.float32)
+    u[0, : len(v)] = v / 64
+    x = np.concatenate([np.full((1, k), 64.0, np.float32), u], 1)
+    y = w4.w4_silu_mul(_dev(x), out_dtype=F32)
+    assert np.array_equal(to_np32(y), u * np.float32(64))
+    codes, scales = (w4.w4_silu_mul_fp8 if kind == "fp8" else w4.w4_silu_mul_int8)(_dev(x))
+    _same_codes(codes, scales, to_np32(y), kind, f"{kind} {top}")
+
+
 # --------------------------------------------------------------------------
 # Rotary positions into the cache
 # --------------------------------------------------------------------------
