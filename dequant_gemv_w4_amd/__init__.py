@@ -584,192 +584,20 @@ def w4_int8_gemm(xq, sx, wq, sw, Y=None, out_dtype=None):
 
 
 # --------------------------------------------------------------------------
-# Operators between the products of a decoder layer
+# Operators between the products of a decoder layer: layer.py, loaded (with torch) on first use
 # --------------------------------------------------------------------------
 
-def _want(t, dtypes, shape, name, device):
-    """_require, and that the tensor lies on the device of the call."""
-    _require(t, dtypes, shape, name)
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+_LAYER = ("w4_rmsnorm", "w4_rmsnorm_fp8", "w4_rmsnorm_int8", "w4_silu_mul", "w4_silu_mul_fp8", "w4_silu_mul_int8",
+          "W4KVCache", "w4_rope_cache", "w4_block_tables", "w4_paged_attention", "w4_paged_attention_workspace_bytes")
 
 
-def _float_code(t):
-    import torch
-    return W4_F32 if t.dtype == torch.float32 else W4_BF16
-
-
-def _opt(t):
-    return None if t is None else t.data_ptr()
-
-
-def _status_ptr(status, device):
-    import torch
-    if status is None:
-        return None
-    _want(status, torch.int32, None, "status", device)
-    if status.numel() < 1:
-        raise ValueError("status must hold one element")
-    return status.data_ptr()
-
-
-def _call(name, device, *args):
-    """Run an entry point on the device of its tensors and that device's current stream."""
-    import torch
-    fn = getattr(lib(), name)
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
-    else:
-        status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
-    _check(status, name)
-
-
-def _rows_of(x, name):
-    import torch
-    _require(x, (torch.float32, torch.bfloat16), None, name)
-    if x.dim() == 1:
-        x = x.unsqueeze(0)
-    if x.dim() != 2:
-        raise ValueError(f"{name} must be [rows, values]")
-    return x
-
-
-def _value_rows(y, out_dtype, shape, device):
-    import torch
-    if y is None:
-        y = torch.empty(shape, dtype=out_dtype or torch.bfloat16, device=device)
-    _want(y, (torch.float32, torch.bfloat16), shape, "y", device)
-    return y
-
-
-def _code_rows(codes, scales, dtype, shape, device):
-    import torch
-    if codes is None:
-        codes = torch.empty(shape, dtype=dtype, device=device)
-    if scales is None:
-        scales = torch.empty(shape[0], dtype=torch.float32, device=device)
-    _want(codes, dtype, shape, "codes", device)
-    _want(scales, torch.float32, shape[:1], "scales", device)
-    return codes, scales
-
-
-def _norm_args(x, weight, eps, residual, residual_out):
-    import torch
-    x = _rows_of(x, "x")
-    rows, k = x.shape
-    _want(weight, (torch.float32, torch.bfloat16), (k,), "weight", x.device)
-    rt = W4_F32
-    if residual is not None:
-        if residual.dim() == 1:
-            residual = residual.unsqueeze(0)
-        _want(residual, (torch.float32, torch.bfloat16), (rows, k), "residual", x.device)
-        if residual_out is None:
-            residual_out = residual
-        if residual_out.dim() == 1:
-            residual_out = residual_out.unsqueeze(0)
-        _want(residual_out, residual.dtype, (rows, k), "residual_out", x.device)
-        rt = _float_code(residual)
-    elif residual_out is not None:
-        raise ValueError("residual_out without residual")
-    return x, (x.data_ptr(), _float_code(x), _opt(residual), _opt(residual_out), rt, weight.data_ptr(),
-               _float_code(weight), eps, rows, k)
-
-
-def w4_rmsnorm(x, weight, eps, residual=None, residual_out=None, y=None, out_dtype=None):
-    """Root-mean-square norm of x [rows, K] (after adding ``residual``, which is updated in place
-    unless ``residual_out`` is given); y [rows, K] bfloat16 by default."""
-    x, args = _norm_args(x, weight, eps, residual, residual_out)
-    y = _value_rows(y, out_dtype, x.shape, x.device)
-    _call("w4_rmsnorm", x.device, *args, y.data_ptr(), _float_code(y))
-    return y
-
-
-def _rmsnorm_codes(name, dtype, x, weight, eps, residual, residual_out, codes, scales, status):
-    x, args = _norm_args(x, weight, eps, residual, residual_out)
-    codes, scales = _code_rows(codes, scales, dtype, x.shape, x.device)
-    _call(name, x.device, *args, codes.data_ptr(), scales.data_ptr(), _status_ptr(status, x.device))
-    return codes, scales
-
-
-def w4_rmsnorm_fp8(x, weight, eps, residual=None, residual_out=None, codes=None, scales=None, status=None):
-    """w4_rmsnorm quantized per row: E4M3 codes [rows, K] uint8 and scales [rows]."""
-    import torch
-    return _rmsnorm_codes("w4_rmsnorm_fp8", torch.uint8, x, weight, eps, residual, residual_out, codes, scales, status)
-
-
-def w4_rmsnorm_int8(x, weight, eps, residual=None, residual_out=None, codes=None, scales=None, status=None):
-    """w4_rmsnorm quantized per row: symmetric INT8 codes [rows, K] and steps [rows]."""
-    import torch
-    return _rmsnorm_codes("w4_rmsnorm_int8", torch.int8, x, weight, eps, residual, residual_out, codes, scales, status)
-
-
-def _gate_args(gate_up):
-    x = _rows_of(gate_up, "gate_up")
-    rows, width = x.shape
-    if width % 2:
-        raise ValueError("gate_up must be [rows, 2F]")
-    return x, (rows, width // 2), (x.data_ptr(), _float_code(x), rows, width // 2)
-
-
-def w4_silu_mul(gate_up, y=None, out_dtype=None):
-    """silu(gate) * up of gate_up [rows, 2F] (gate first); y [rows, F] bfloat16 by default."""
-    x, shape, args = _gate_args(gate_up)
-    y = _value_rows(y, out_dtype, shape, x.device)
-    _call("w4_silu_mul", x.device, *args, y.data_ptr(), _float_code(y))
-    return y
-
-
-def _silu_mul_codes(name, dtype, gate_up, codes, scales, status):
-    x, shape, args = _gate_args(gate_up)
-    codes, scales = _code_rows(codes, scales, dtype, shape, x.device)
-    _call(name, x.device, *args, codes.data_ptr(), scales.data_ptr(), _status_ptr(status, x.device))
-    return codes, scales
-
-
-def w4_silu_mul_fp8(gate_up, codes=None, scales=None, status=None):
-    """w4_silu_mul quantized per row: E4M3 codes [rows, F] uint8 and scales [rows]."""
-    import torch
-    return _silu_mul_codes("w4_silu_mul_fp8", torch.uint8, gate_up, codes, scales, status)
-
-
-def w4_silu_mul_int8(gate_up, codes=None, scales=None, status=None):
-    """w4_silu_mul quantized per row: symmetric INT8 codes [rows, F] and steps [rows]."""
-    import torch
-    return _silu_mul_codes("w4_silu_mul_int8", torch.int8, gate_up, codes, scales, status)
-
-
-class W4KVCache:
-    """A paged cache: k and v [pages, kv_heads, page_size, head_dim], bfloat16, or uint8 (E4M3
-    codes) with float32 scales [pages, kv_heads, page_size].  Keeps its tensors alive."""
-
-    def __init__(self, k, v, k_scales=None, v_scales=None):
-        import torch
-        _require(k, (torch.bfloat16, torch.uint8), None, "k")
-        if k.dim() != 4:
-            raise ValueError("k must be [pages, kv_heads, page_size, head_dim]")
-        _want(v, k.dtype, k.shape, "v", k.device)
-        fp8 = k.dtype == torch.uint8
-        if fp8:
-            _want(k_scales, torch.float32, k.shape[:3], "k_scales", k.device)
-            _want(v_scales, torch.float32, k.shape[:3], "v_scales", k.device)
-        elif k_scales is not None or v_scales is not None:
-            raise ValueError("a bfloat16 cache has no scales")
-        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
-        self.pages, self.kv_heads, self.page_size, self.head_dim = k.shape
-        self.device = k.device
-        self._c = _KVCacheStruct(k.data_ptr(), v.data_ptr(), _opt(k_scales), _opt(v_scales), self.pages,
-                                 self.page_size, self.kv_heads, self.head_dim, int(fp8))
-        self._ref = ctypes.byref(self._c)
-
-    @classmethod
-    def empty(cls, pages, page_size, kv_heads, head_dim, fp8=False, device="cuda"):
-        """A cache of that shape (zeros)."""
-        import torch
-        shape = (pages, kv_heads, page_size, head_dim)
-        kv = [torch.zeros(shape, dtype=torch.uint8 if fp8 else torch.bfloat16, device=device) for _ in range(2)]
-        scales = [torch.ones(shape[:3], dtype=torch.float32, device=device) if fp8 else None for _ in range(2)]
-        return cls(*kv, *scales)
+def __getattr__(name):
+    if name not in _LAYER:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import layer
+    for n in _LAYER:
+        globals()[n] = getattr(layer, n)
+    return globals()[name]
 
 
 def w4_rope_frequencies(rope: W4Rope, device=None):
@@ -782,106 +610,3 @@ def w4_rope_frequencies(rope: W4Rope, device=None):
         return list(freqs), amplitude.value
     import torch
     return torch.tensor(list(freqs), dtype=torch.float64, device=device), amplitude.value
-
-
-def w4_rope_cache(qkv, cache: W4KVCache, positions, slots, rope: W4Rope, freqs, q=None, status=None):
-    """Rotate the rows of the fused q|k|v product qkv [T, (heads + 2 kv_heads) * head_dim] and store
-    K and V at ``slots``; returns q [T, heads, head_dim] bfloat16.  ``freqs``: float64 device tensor
-    of w4_rope_frequencies.  Rows with a negative slot are left out (of q too)."""
-    import torch
-    x = _rows_of(qkv, "qkv")
-    dev = x.device
-    T, width = x.shape
-    d = cache.head_dim
-    heads = width // d - 2 * cache.kv_heads
-    if width % d or heads < 1:
-        raise ValueError("qkv must be [T, (heads + 2 kv_heads) * head_dim]")
-    if cache.device != dev:
-        raise ValueError(f"cache is on {cache.device}, expected {dev}")
-    _want(positions, torch.int32, (T,), "positions", dev)
-    _want(slots, torch.int64, (T,), "slots", dev)
-    _want(freqs, torch.float64, (rope.rotary_dim // 2,), "freqs", dev)
-    if q is None:
-        q = torch.empty(T, heads, d, dtype=torch.bfloat16, device=dev)
-    _want(q, torch.bfloat16, (T, heads, d), "q", dev)
-    _call("w4_rope_cache", dev, x.data_ptr(), _float_code(x), T, heads, cache._ref, positions.data_ptr(),
-          slots.data_ptr(), ctypes.byref(rope), freqs.data_ptr(), q.data_ptr(), _status_ptr(status, dev))
-    return q
-
-
-def w4_block_tables(new_lens, lens, free_pages, free_count, block_table, page_size, tokens=None, lens_out=None,
-                    free_count_out=None, cu_q=None, positions=None, slots=None, status=None):
-    """Place the new tokens of a batch in pages; returns (cu_q, positions, slots).
-
-    ``lens`` and ``free_count`` are updated in place unless ``lens_out`` / ``free_count_out`` are
-    given; ``block_table`` is.  ``tokens``: places of positions and slots where those are not given."""
-    import torch
-    i32 = torch.int32
-    _require(new_lens, i32, None, "new_lens")
-    dev = new_lens.device
-    if new_lens.dim() != 1:
-        raise ValueError("new_lens must be [B]")
-    B = new_lens.shape[0]
-    lens_out = lens if lens_out is None else lens_out
-    free_count_out = free_count if free_count_out is None else free_count_out
-    if positions is None or slots is None:
-        if tokens is None:
-            raise ValueError("tokens is needed where positions or slots are not given")
-        positions = torch.empty(tokens, dtype=i32, device=dev) if positions is None else positions
-        slots = torch.empty(tokens, dtype=torch.int64, device=dev) if slots is None else slots
-    if cu_q is None:
-        cu_q = torch.empty(B + 1, dtype=i32, device=dev)
-    _want(lens, i32, (B,), "lens", dev)
-    _want(lens_out, i32, (B,), "lens_out", dev)
-    _want(free_pages, i32, None, "free_pages", dev)
-    _want(free_count, i32, (1,), "free_count", dev)
-    _want(free_count_out, i32, (1,), "free_count_out", dev)
-    _want(block_table, i32, None, "block_table", dev)
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError("block_table must be [B, max_pages]")
-    _want(cu_q, i32, (B + 1,), "cu_q", dev)
-    _want(positions, i32, None, "positions", dev)
-    _want(slots, torch.int64, positions.shape, "slots", dev)
-    _call("w4_block_tables", dev, new_lens.data_ptr(), lens.data_ptr(), B, free_pages.data_ptr(),
-          free_pages.numel(), free_count.data_ptr(), lens_out.data_ptr(), free_count_out.data_ptr(),
-          block_table.data_ptr(), block_table.shape[1], page_size, cu_q.data_ptr(), positions.data_ptr(),
-          slots.data_ptr(), positions.numel(), _status_ptr(status, dev))
-    return cu_q, positions, slots
-
-
-def w4_paged_attention_workspace_bytes(T: int, heads: int, cache: W4KVCache, B: int, max_pages: int) -> int:
-    return int(lib().w4_paged_attention_workspace_bytes(T, heads, cache._ref, B, max_pages))
-
-
-def w4_paged_attention(q, cache: W4KVCache, block_table, cu_q, lens, scale, window=0, o=None, workspace=None,
-                       status=None):
-    """Attention of q [T, heads, head_dim] (bfloat16) over the paged cache; returns o like q.
-
-    ``cu_q`` [B + 1] and ``lens`` [B] as w4_block_tables gives them (lens counts the new tokens);
-    rows of q behind cu_q[B] are left out of o.  The workspace is allocated where it is not given."""
-    import torch
-    _require(q, torch.bfloat16, None, "q")
-    dev = q.device
-    if q.dim() != 3 or q.shape[2] != cache.head_dim:
-        raise ValueError("q must be [T, heads, head_dim]")
-    if cache.device != dev:
-        raise ValueError(f"cache is on {cache.device}, expected {dev}")
-    T, heads, _ = q.shape
-    _want(block_table, torch.int32, None, "block_table", dev)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_pages]")
-    B, max_pages = block_table.shape
-    _want(cu_q, torch.int32, (B + 1,), "cu_q", dev)
-    _want(lens, torch.int32, (B,), "lens", dev)
-    if o is None:
-        o = torch.empty_like(q)
-    _want(o, torch.bfloat16, q.shape, "o", dev)
-    if workspace is None:
-        need = lib().w4_paged_attention_workspace_bytes(T, heads, cache._ref, B, max_pages)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    else:
-        _want(workspace, torch.uint8, None, "workspace", dev)
-    _call("w4_paged_attention", dev, q.data_ptr(), T, heads, cache._ref, block_table.data_ptr(), max_pages,
-          cu_q.data_ptr(), lens.data_ptr(), B, scale, window, o.data_ptr(), _opt(workspace),
-          0 if workspace is None else workspace.numel(), _status_ptr(status, dev))
-    return o
