@@ -18,7 +18,8 @@
 // binary32.
 //
 // attend_wide: 256 rows a workgroup, 8 waves of 32 rows; tiles of 64 keys pass through LDS for
-// all of them, double-buffered, the next tile's loads in flight during the products.
+// all of them, the next tile's loads in flight, and the two waves of a SIMD take turns on the
+// matrix unit.
 // attend_narrow: up to 32 rows, for single tokens: the waves take 32-key tiles in turn, each with
 // its own piece of LDS, and join their sums at the end.
 // Either may split the keys of a tile over several workgroups, which then leave (m, l, O / l) in
@@ -28,9 +29,12 @@
 // meets a weight of zero in the matrix unit, where an infinity or NaN would survive as NaN: rows
 // past the context are replaced by zeros when they are staged, and a query row whose result is not
 // finite is computed again by attend_row, which skips masked keys.
+#include "w4a16.h"
 #include "w4_codes.h"
 #include "w4_internal.h"
 #include "w4_paging.h"
+
+#include <type_traits>
 
 namespace w4 {
 namespace {
@@ -90,10 +94,13 @@ __device__ __forceinline__ uint64_t read_tr(const uint8_t* p) {
     return __builtin_bit_cast(uint64_t, r);
 }
 
-// Stages the 16 bytes that a lane loaded of key row r (chunk c of the stored row).
+// Stages the 16 bytes that a lane loaded of key row r (chunk c of the stored row), zeros where r is not
+// below `left` (the same for the wave; the rows of most tiles all stay).
 template <int D, bool FP8, bool IS_V>
-__device__ __forceinline__ void stage(uint8_t* tile, int r, int c, u32x4_t w, bool keep) {
-    if (!keep) w = u32x4_t{0u, 0u, 0u, 0u};
+__device__ __forceinline__ void stage(uint8_t* tile, int r, int c, u32x4_t w, int left) {
+    if (left < kKeyTile) {
+        if (r >= left) w = u32x4_t{0u, 0u, 0u, 0u};
+    }
     if constexpr (FP8) {
         u32x4_t lo, hi;
         fp8_to_bf16(w, lo, hi);
@@ -124,26 +131,40 @@ __device__ __forceinline__ void clear_rows(Rows<D>& s) {
     s.l = 0.0f;
 }
 
-// One step over NB blocks of 32 keys.  kt, vt: staged tiles; ks, vs: their row scales (FP8).
-// first: position of the first key; lo, hi: the row sees lo <= key <= hi; mask: whether the step
-// reaches outside some row's keys.
-template <int D, bool FP8, int NB>
-__device__ __forceinline__ void attend_step(Rows<D>& s, const uint8_t* kt, const uint8_t* vt,
-                                            const float* ks, const float* vs, float scale,
-                                            int first, int lo, int hi, bool mask) {
+// A step takes NB blocks of 32 keys in three parts.  scores: z = K q for the staged keys kt.
+template <int D, int NB>
+__device__ __forceinline__ void scores(const Rows<D>& s, const uint8_t* kt, f32x16_t (&z)[NB]) {
     const int lane = threadIdx.x & 63, half = lane >> 5, l32 = lane & 31;
-    f32x16_t z[NB];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int r = 0; r < 16; ++r) z[b][r] = 0.0f;
 #pragma unroll
-        for (int d = 0; d < D / 16; ++d) {
+    for (int d = 0; d < D / 16; ++d) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
             const u32x4_t a = *reinterpret_cast<const u32x4_t*>(kt + k_place<D>(32 * b + l32, 2 * d + half));
             z[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
                                                            __builtin_bit_cast(bf16x8_t, s.q[d]), z[b], 0, 0, 0);
         }
     }
+}
+
+// Maximum over a lane and the one 32 lanes away.
+__device__ __forceinline__ float half_max(float x) {
+    const uint32_t u = __float_as_uint(x);
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// weights: the running maximum and sum, and the bfloat16 weights p (as the right operand of 16 keys
+// each: p[4 c .. 4 c + 3]).  ks, vs: scales of the keys' and values' rows (FP8); first: position of
+// the first key; the row sees the `count` keys from lo; mask: whether the step reaches outside some
+// row's.
+template <int D, bool FP8, int NB>
+__device__ __forceinline__ void weights(Rows<D>& s, f32x16_t (&z)[NB], uint32_t (&p)[8 * NB], const float* ks,
+                                        const float* vs, float scale, int first, int lo, int count, bool mask) {
+    const int half = (threadIdx.x & 63) >> 5;
     if constexpr (FP8) {
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -155,20 +176,19 @@ __device__ __forceinline__ void attend_step(Rows<D>& s, const uint8_t* kt, const
             }
     }
     if (mask) {
+        const uint32_t from = (uint32_t)(first + 4 * half - lo);
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int key = first + 32 * b + 8 * (r >> 2) + 4 * half + (r & 3);
-                if (key < lo || key > hi) z[b][r] = kNegInf;
-            }
+            for (int r = 0; r < 16; ++r)
+                if (from + (32 * b + 8 * (r >> 2) + (r & 3)) >= (uint32_t)count) z[b][r] = kNegInf;
     }
     float mx = z[0][0];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int r = 0; r < 16; ++r) mx = fmaxf(mx, z[b][r]);
-    mx = fmaxf(mx, __shfl_xor(mx, 32)) * scale;              // scale > 0
+    mx = half_max(mx) * scale;                               // scale > 0
     if (__any(mx > s.m + kSlack)) {
         const float m = fmaxf(s.m, mx);
         const float f = m == s.m ? 1.0f : exp2_fast(s.m - m);
@@ -180,7 +200,7 @@ __device__ __forceinline__ void attend_step(Rows<D>& s, const uint8_t* kt, const
             for (int r = 0; r < 16; ++r) s.o[i][r] *= f;
     }
     const float sub = s.m == kNegInf ? 0.0f : s.m;           // nothing seen yet: every weight is 0
-    uint32_t p[NB][8];
+    float sum[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
         f32x4_t f = {1.0f, 1.0f, 1.0f, 1.0f};
@@ -188,20 +208,26 @@ __device__ __forceinline__ void attend_step(Rows<D>& s, const uint8_t* kt, const
         for (int i = 0; i < 8; ++i) {
             const float e0 = exp2_fast(fmaf(z[b][2 * i], scale, -sub));
             const float e1 = exp2_fast(fmaf(z[b][2 * i + 1], scale, -sub));
-            s.l += e0 + e1;
+            sum[0] += e0;
+            sum[1] += e1;
             if constexpr (FP8) {
                 if ((i & 1) == 0) f = *reinterpret_cast<const f32x4_t*>(vs + 32 * b + 4 * i + 4 * half);
-                p[b][i] = bf16_pair(e0 * f[2 * (i & 1)], e1 * f[2 * (i & 1) + 1]);
+                p[8 * b + i] = bf16_pair(e0 * f[2 * (i & 1)], e1 * f[2 * (i & 1) + 1]);
             } else {
-                p[b][i] = bf16_pair(e0, e1);
+                p[8 * b + i] = bf16_pair(e0, e1);
             }
         }
     }
-    const int i16 = lane & 15, g16 = (lane >> 4) & 1;
+    s.l += sum[0] + sum[1];
+}
+
+// accumulate: O += V p for the staged values vt.
+template <int D, int NB>
+__device__ __forceinline__ void accumulate(Rows<D>& s, const uint8_t* vt, const uint32_t (&p)[8 * NB]) {
+    const int lane = threadIdx.x & 63, half = lane >> 5, i16 = lane & 15, g16 = (lane >> 4) & 1;
 #pragma unroll
     for (int c = 0; c < 2 * NB; ++c) {                       // 16 keys each
-        const u32x4_t pb = {p[c >> 1][4 * (c & 1)], p[c >> 1][4 * (c & 1) + 1], p[c >> 1][4 * (c & 1) + 2],
-                            p[c >> 1][4 * (c & 1) + 3]};
+        const u32x4_t pb = {p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]};
         const int r0 = 16 * c + 4 * half + (i16 >> 2);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
@@ -254,29 +280,35 @@ __device__ void attend_row(const AttendArgs& a, int b, int kv, int64_t row, int6
         q[e] = __uint_as_float((uint32_t)a.q[row * D + lane * E + e] << 16);
         o[e] = 0.0f;
     }
-    for (int64_t j = k0 > lo ? k0 : lo; j < k1 && j <= hi; ++j) {
+    const int64_t last = imin(k1 - 1, hi), page_rows = (int64_t)1 << a.page_shift;
+    for (int64_t j = k0 > lo ? k0 : lo; j <= last;) {
         const int64_t at = key_row(a, b, kv, j);
-        float k[E], v[E];
-        for (int e = 0; e < E; ++e) {
-            k[e] = v[e] = 0.0f;
-            if (at >= 0) {
+        float z = 0.0f, v[E], count = 1.0f;
+        for (int e = 0; e < E; ++e) v[e] = 0.0f;
+        if (at < 0) {                                        // zeros up to the end of the page
+            const int64_t next = imin(last + 1, (j / page_rows + 1) * page_rows);
+            count = (float)(next - j);
+            j = next;
+        } else {
+            for (int e = 0; e < E; ++e) {
                 const int64_t i = at * D + lane * E + e;
+                float k;
                 if constexpr (FP8) {
-                    k[e] = __builtin_amdgcn_cvt_f32_fp8(static_cast<const uint8_t*>(a.k)[i], 0) * a.k_scales[at];
+                    k = __builtin_amdgcn_cvt_f32_fp8(static_cast<const uint8_t*>(a.k)[i], 0) * a.k_scales[at];
                     v[e] = __builtin_amdgcn_cvt_f32_fp8(static_cast<const uint8_t*>(a.v)[i], 0) * a.v_scales[at];
                 } else {
-                    k[e] = __uint_as_float((uint32_t) static_cast<const uint16_t*>(a.k)[i] << 16);
+                    k = __uint_as_float((uint32_t) static_cast<const uint16_t*>(a.k)[i] << 16);
                     v[e] = __uint_as_float((uint32_t) static_cast<const uint16_t*>(a.v)[i] << 16);
                 }
+                z = fmaf(q[e], k, z);
             }
+            for (int off = 32; off > 0; off >>= 1) z += __shfl_xor(z, off);
+            z *= a.scale_log2;
+            ++j;
         }
-        float z = 0.0f;
-        for (int e = 0; e < E; ++e) z = fmaf(q[e], k[e], z);
-        for (int off = 32; off > 0; off >>= 1) z += __shfl_xor(z, off);
-        z *= a.scale_log2;
         const float mn = z != z ? z : fmaxf(m, z);
         const float keep = mn == m ? 1.0f : exp2_fast(m - mn);
-        const float p = mn == kNegInf ? 0.0f : exp2_fast(z - mn);
+        const float p = mn == kNegInf ? 0.0f : count * exp2_fast(z - mn);
         const float ln = l * keep + p;
         if (!(ln == 0.0f)) {
             const float fo = l * keep / ln, fv = p / ln;
@@ -340,7 +372,7 @@ __device__ __forceinline__ Tile find_tile(const AttendArgs& a, int64_t index, in
 // The place of a row of the tile: its row in q and o, and the keys it sees.
 struct Place {
     int64_t row;       // token * heads + head
-    int lo, hi;
+    int lo, hi, count; // lo <= key <= hi
     bool real;
 };
 __device__ __forceinline__ Place row_place(const AttendArgs& a, const Tile& t, int kv, int64_t r) {
@@ -350,6 +382,7 @@ __device__ __forceinline__ Place row_place(const AttendArgs& a, const Tile& t, i
     p.row = (t.seq.start + token) * a.heads + (int64_t)kv * a.group + (p.real ? r - token * a.group : 0);
     p.hi = p.real ? (int)(t.seq.ctx - t.seq.n + token) : -1;
     p.lo = a.window > 0 ? (int)imax(0, p.hi - (int64_t)a.window + 1) : 0;
+    p.count = (int)imax(0, (int64_t)p.hi - p.lo + 1);
     return p;
 }
 
@@ -361,6 +394,10 @@ __device__ __forceinline__ void load_q(const AttendArgs& a, const Place& p, Rows
         s.q[d] = u32x4_t{0u, 0u, 0u, 0u};
         if (p.real) s.q[d] = *reinterpret_cast<const u32x4_t*>(a.q + p.row * D + 16 * d + 8 * half);
     }
+    // The wait for these loads belongs here: left to the first product, inside the loop, it would be
+    // a wait for the tile loads in flight at every step.
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) asm volatile("" : "+v"(s.q[d]));
 }
 
 // Stores 4 neighbouring columns of a row that are already divided by its sum.
@@ -420,7 +457,65 @@ __device__ void redo_rows(const AttendArgs& a, const Tile& t, int part, int kv, 
     }
 }
 
+// The rows of one sequence and kv head, for loads whose page is the same for a whole wave: offsets
+// are formed once per 16 keys, in scalar registers.
+template <int ROW_BYTES>
+struct Rows16 {
+    const uint8_t *k, *v;
+    const float *ks, *vs;
+    const int32_t* table;
+    uint32_t pages, page_bytes, worst;                       // worst: the largest page number met
+    int shift, end;                                          // keys below `end` are wanted
+
+    __device__ Rows16(const AttendArgs& a, int b, int kv, int end_) {
+        const int64_t head = (int64_t)kv << a.page_shift;
+        k = static_cast<const uint8_t*>(a.k) + head * ROW_BYTES;
+        v = static_cast<const uint8_t*>(a.v) + head * ROW_BYTES;
+        ks = a.k_scales + head;
+        vs = a.v_scales + head;
+        table = a.table + (int64_t)b * a.max_pages;
+        pages = (uint32_t)a.pages;
+        page_bytes = (uint32_t)(a.kv_heads * ROW_BYTES) << a.page_shift;   // < 2^31
+        shift = a.page_shift;
+        end = end_;
+        worst = 0;
+    }
+    __device__ __forceinline__ bool missing() const { return worst >= pages; }
+    // Table entry of a key (the same for the wave); keys past the end read the last one's.
+    __device__ __forceinline__ int entry(int key) const {
+        // through the scalar cache: the answer does not pass in the order of the vector loads
+        const auto t = (__attribute__((address_space(4))) const int32_t*)(uintptr_t)table;
+        return t[(uint32_t)(min(__builtin_amdgcn_readfirstlane(key), end - 1) >> shift)];
+    }
+    // Byte offset of the row of `key` (a multiple of 16, the same for the wave) by its entry.  For a
+    // page that the cache does not have it is that of a row of its last page: the kernel then computes
+    // its rows again (attend_row).
+    __device__ __forceinline__ uint64_t offset(int e, int key) {
+        worst = max(worst, (uint32_t)e);
+        return (uint64_t)min((uint32_t)e, pages - 1) * page_bytes + (uint32_t)((key & ((1 << shift) - 1)) * ROW_BYTES);
+    }
+};
+
+__device__ __forceinline__ u32x4_t load16(const uint8_t* base, uint64_t offset, uint32_t lane_byte) {
+    return *reinterpret_cast<const u32x4_t*>(base + offset + lane_byte);
+}
+
+// 16 bytes a lane from the cache straight into LDS: lane l of the wave writes bytes [16 l, 16 l + 16)
+// after the wave-uniform LDS address.  Inline assembly, so that the compiler does not hold the LDS
+// reads of other tiles back behind these loads; the kernel waits for them itself (vmcnt) before the
+// barrier that publishes them.
+__device__ __forceinline__ void load_lds16(const uint8_t* base, uint32_t lane_byte, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 :
+                 : "v"(lane_byte), "s"(base), "s"(__builtin_amdgcn_readfirstlane(lds))
+                 : "memory", "m0");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)p;
+}
+
 constexpr int kWideWaves = 8;
+constexpr int kWideStages = 4;
 constexpr int kWideThreads = 64 * kWideWaves;
 
 template <int D, bool FP8>
@@ -430,9 +525,10 @@ __global__ __launch_bounds__(kWideThreads, 2) void attend_wide_kernel(AttendArgs
     constexpr int kStepRows = kWideThreads / kChunks;        // rows that one load of all threads covers
     constexpr int kLoads = kStepRows >= kKeyTile ? 1 : kKeyTile / kStepRows;
     constexpr int kTileBytes = kKeyTile * 2 * D;
-    __shared__ __attribute__((aligned(16))) uint8_t kt[2][kTileBytes], vt[2][kTileBytes];
-    __shared__ __attribute__((aligned(16))) float ksc[2][kKeyTile], vsc[2][kKeyTile];
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    __shared__ __attribute__((aligned(16))) uint8_t kt[kWideStages][kTileBytes], vt[kWideStages][kTileBytes];
+    __shared__ __attribute__((aligned(16))) float ksc[FP8 ? kWideStages : 1][kKeyTile], vsc[FP8 ? kWideStages : 1][kKeyTile];
+    __shared__ int any_missing;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int part = blockIdx.y;
     int kv;
     // the last tiles of a sequence see the most keys: they start first
@@ -444,7 +540,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void attend_wide_kernel(AttendArgs
     load_q<D>(a, p, s);
     clear_rows<D>(s);
     // keys that any row of this wave sees, and those that all of them see
-    int any_lo = p.real ? p.lo : INT32_MAX, any_hi = p.hi, all_lo = p.lo, all_hi = p.real ? p.hi : INT32_MAX;
+    int any_lo = p.real ? p.lo : W4_MAX_CONTEXT, any_hi = p.hi, all_lo = p.lo, all_hi = p.real ? p.hi : W4_MAX_CONTEXT;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
         any_lo = min(any_lo, __shfl_xor(any_lo, off));
@@ -459,79 +555,163 @@ __global__ __launch_bounds__(kWideThreads, 2) void attend_wide_kernel(AttendArgs
 
     const int k0 = (int)t.k0, k1 = (int)t.k1;
     const int tiles = (k1 - k0 + kKeyTile - 1) / kKeyTile;
-    const int page_mask = (1 << a.page_shift) - 1;
     const int crow = tid / kChunks, chunk = tid % kChunks;
-    const bool loads = crow < kKeyTile;                      // more threads than chunks of a tile
+    const bool loads = kStepRows * kLoads == kKeyTile || crow < kKeyTile;   // else more threads than chunks
     // The rows that one load of a wave covers lie in one aligned group of 16, so in one page.
-    const int granule = __builtin_amdgcn_readfirstlane(crow & ~15);
-    const int32_t* table = a.table + (int64_t)t.b * a.max_pages;
-    int entry[kLoads];                                       // table entries of the next tile
-    u32x4_t kw[kLoads], vw[kLoads];
-    float sc = 1.0f;
-    bool keep[kLoads], bad_page = false;
-    auto look_up = [&](int i, int* e) {                      // read here, used a tile later
+    const int granule = __builtin_amdgcn_readfirstlane(crow & ~15) & (kKeyTile - 1);
+    Rows16<kRowBytes> rows(a, t.b, kv, k1);
+    int entry[kLoads];                                       // of the tile whose keys are brought next
+    uint64_t off[kLoads];                                    // of the tile whose values are brought next
+    auto look_up = [&](int i) {                              // read here, used by locate
 #pragma unroll
-        for (int c = 0; c < kLoads; ++c) {
-            const int key = k0 + i * kKeyTile + crow + c * kStepRows;
-            e[c] = table[(key < k1 ? key : k1 - 1) >> a.page_shift];
-        }
+        for (int c = 0; c < kLoads; ++c) entry[c] = rows.entry(k0 + i * kKeyTile + granule + c * kStepRows);
     };
-    auto fetch = [&](int i, const int* e) {
+    auto locate = [&](int i) {
 #pragma unroll
-        for (int c = 0; c < kLoads; ++c) {
-            const int first = k0 + i * kKeyTile + granule + c * kStepRows;   // key of the group's first row
-            const int64_t page = checked_page(__builtin_amdgcn_readfirstlane(e[c]), a.pages);
-            const bool there = loads && first < k1;
-            bad_page |= there && page < 0;
-            keep[c] = page >= 0 && k0 + i * kKeyTile + crow + c * kStepRows < k1;
-            // another page's rows stand in for those of a page that is not there; put() drops them
-            const int64_t row0 = there && page >= 0 ? ((page * a.kv_heads + kv) << a.page_shift) + (first & page_mask) : 0;
-            const int lane_row = loads ? crow & 15 : 0;
-            const uint8_t* kp = static_cast<const uint8_t*>(a.k) + row0 * kRowBytes;
-            const uint8_t* vp = static_cast<const uint8_t*>(a.v) + row0 * kRowBytes;
-            kw[c] = *reinterpret_cast<const u32x4_t*>(kp + lane_row * kRowBytes + 16 * chunk);
-            vw[c] = *reinterpret_cast<const u32x4_t*>(vp + lane_row * kRowBytes + 16 * chunk);
-            if constexpr (FP8) {
-                static_assert(kLoads == 1, "one row a thread");
-                sc = (chunk & 1 ? a.v_scales : a.k_scales)[row0 + lane_row];
+        for (int c = 0; c < kLoads; ++c) off[c] = rows.offset(entry[c], k0 + i * kKeyTile + granule + c * kStepRows);
+    };
+    // Rows of a tile that are past the part become zeros, so that what lies there in the cache does not
+    // meet a weight of zero.
+    auto left = [&](int i) { return k1 - k0 - i * kKeyTile; };
+
+    // A bfloat16 tile goes straight into LDS: a lane loads the chunk whose place it is.  An E4M3 tile
+    // passes through registers (kw, vw), where its codes are widened.
+    const int crow16 = crow & 15;
+    const uint32_t lane_k = crow16 * kRowBytes + (FP8 ? 16 * chunk : k_place<D>(crow, chunk) - crow * 2 * D);
+    const uint32_t lane_v = crow16 * kRowBytes + (FP8 ? 16 * chunk : v_place<D>(crow, chunk) - crow * 2 * D);
+    const uint32_t lds_k = lds_address(&kt[0][0]) + wave * 1024, lds_v = lds_address(&vt[0][0]) + wave * 1024;
+    u32x4_t kw, vw;
+    float sc = 1.0f;
+    auto bring = [&](int i, bool values) {
+        const uint8_t* from = values ? rows.v : rows.k;
+        const uint32_t lane_byte = values ? lane_v : lane_k;
+        if constexpr (FP8) {
+            static_assert(!FP8 || kLoads == 1, "one row a thread");
+            (values ? vw : kw) = load16(from, off[0], lane_byte);
+            if (!values) sc = (chunk & 1 ? rows.vs : rows.ks)[off[0] / kRowBytes + crow16];
+        } else {
+            const uint32_t lds = (values ? lds_v : lds_k) + (i % kWideStages) * kTileBytes;
+            if (left(i) >= kKeyTile) {
+#pragma unroll
+                for (int c = 0; c < kLoads; ++c) load_lds16(from + off[c], lane_byte, lds + c * (kStepRows * 2 * D));
+            } else {
+                uint8_t* tile = values ? vt[i % kWideStages] : kt[i % kWideStages];
+#pragma unroll
+                for (int c = 0; c < kLoads; ++c) {
+                    if (crow + c * kStepRows < left(i))
+                        load_lds16(from + off[c], lane_byte, lds + c * (kStepRows * 2 * D));
+                    else
+                        *reinterpret_cast<u32x4_t*>(tile + c * (kStepRows * 2 * D) + 16 * tid) = u32x4_t{0u, 0u, 0u, 0u};
+                }
             }
         }
     };
-    auto put = [&](int buf) {
+    auto put = [&](int i, bool values) {                     // FP8: what bring loaded
         if (!loads) return;
-#pragma unroll
-        for (int c = 0; c < kLoads; ++c) {
-            stage<D, FP8, false>(kt[buf], crow + c * kStepRows, chunk, kw[c], keep[c]);
-            stage<D, FP8, true>(vt[buf], crow + c * kStepRows, chunk, vw[c], keep[c]);
-        }
-        if constexpr (FP8) {
-            if (chunk < 2) (chunk == 0 ? ksc[buf] : vsc[buf])[crow] = keep[0] ? sc : 1.0f;
+        if (values) {
+            stage<D, true, true>(vt[i % kWideStages], crow, chunk, vw, left(i));
+        } else {
+            stage<D, true, false>(kt[i % kWideStages], crow, chunk, kw, left(i));
+            if (chunk < 2) (chunk == 0 ? ksc : vsc)[FP8 ? i % kWideStages : 0][crow] = crow < left(i) ? sc : 1.0f;
         }
     };
+    // Waits for this wave's LDS accesses and then for the other waves; loads of the cache stay in
+    // flight, and nothing is moved across.
+    auto meet = [&]() {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // Tiles that some row of this wave sees, and those among them that all rows see whole.
+    const int seen_lo = (any_lo - k0) >> 6, seen_hi = min(tiles - 1, (any_hi - k0) >> 6);
+    const int whole_lo = (all_lo - k0 + kKeyTile - 1) >> 6, whole_hi = ((all_hi - k0 + 1) >> 6) - 1;
+    static_assert(kKeyTile == 64, "shifts by 6");
+    auto seen = [&](int i) { return i >= seen_lo && i <= seen_hi; };
+
+    // Waves 0-3 and 4-7 (one of either on each SIMD) take turns: while one half is on the matrix
+    // unit with O += V(i) P(i) and S = K(i+1) q, the other is on the vector unit with the weights of
+    // its tile.  Phase by phase (A: weights, B: products; a barrier after each), the second half one
+    // phase behind:
+    //     phase        2i            2i+1          2i+2
+    //     waves 0-3    A(i)          B(i)          A(i+1)
+    //     waves 4-7    B(i-1)        A(i)          B(i)
+    // "Pair n", V(n) and K(n+1), is read in phases 2n+1 and 2n+2; LDS has four places for either.
+    // Each wave brings its share of pair n at the end of its A: of a bfloat16 cache at A(n-2) of waves
+    // 0-3 and A(n-3) of waves 4-7, phases 2n-4 and 2n-5, two pairs ahead of the one that has landed
+    // by the end of that phase; its place was pair n-4's, read last in phase 2n-6.  E4M3 rows are one
+    // pair ahead in registers and staged in phases 2n (A(n)) and 2n-1 (A(n-1)).  Row scales come with
+    // the keys of their tile: those of tile i are staged in phase 2i-2 at the latest, read in A(i), and
+    // written over by those of tile i+4 in phase 2i+5 at the earliest.
+    constexpr int kAhead = FP8 ? 1 : 2;                      // pairs in flight
+    const int behind = wave >> 2;                            // 1 for waves 4-7
+    f32x16_t z[2];
+    uint32_t pw[16];
+    if (tid == 0) any_missing = 0;
     if (tiles > 0) {
-        look_up(0, entry);
-        fetch(0, entry);
-        look_up(1, entry);
-        put(0);
-    }
-    __syncthreads();
-    for (int i = 0; i < tiles; ++i) {
-        const int buf = i & 1;
-        if (i + 1 < tiles) {
-            int later[kLoads];
-            look_up(i + 2, later);                           // ahead of the rows, whose wait covers it
-            fetch(i + 1, entry);
-#pragma unroll
-            for (int c = 0; c < kLoads; ++c) entry[c] = later[c];
+        for (int i = 0; i <= kAhead + 1; ++i) {              // K(0), V(0), K(1), V(1) ...
+            if (i >= tiles) break;
+            look_up(i);
+            locate(i);
+            bring(i, false);
+            if (FP8 && i <= 1) put(i, false);
+            if (i <= kAhead) bring(i, true);
+            if (FP8 && i == 0) put(i, true);
+            if (!FP8 && i == 1) {                            // K(0), V(0) and K(1) are needed at once
+                if (left(1) >= kKeyTile)
+                    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads) : "memory");
+                else
+                    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            }
         }
-        const int first = k0 + i * kKeyTile, last = first + kKeyTile - 1;
-        if (first <= any_hi && last >= any_lo)
-            attend_step<D, FP8, 2>(s, kt[buf], vt[buf], ksc[buf], vsc[buf], a.scale_log2, first, p.lo, p.hi,
-                                   first < all_lo || last > all_hi);
-        if (i + 1 < tiles) put(buf ^ 1);
-        __syncthreads();
+        if (!FP8 && tiles < 2) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
-    if (bad_page && a.status) atomicOr(a.status, kStatusPage);
+    meet();
+    if (seen(0)) scores<D, 2>(s, kt[0], z);
+    if (behind) meet();
+    // One step, tile i in place S = i % kWideStages.
+    auto step = [&](auto place, int i) {
+        constexpr int S = decltype(place)::value;
+        const int n = i + behind;
+        look_up(n + kAhead + 1);
+        if (seen(i))
+            weights<D, FP8, 2>(s, z, pw, ksc[FP8 ? S : 0], vsc[FP8 ? S : 0], a.scale_log2, k0 + i * kKeyTile, p.lo,
+                               p.count, i < whole_lo || i > whole_hi);
+        if (n >= 1 && n < tiles) {
+            if constexpr (FP8) {
+                put(n, true);
+                if (n + 1 < tiles) put(n + 1, false);
+            } else if (left(n + 2) >= kKeyTile) {            // pair n + 1 may stay in flight
+                asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kLoads) : "memory");
+            } else {
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            }
+            if (n + kAhead < tiles) bring(n + kAhead, true);
+            if (n + kAhead + 1 < tiles) {
+                locate(n + kAhead + 1);
+                bring(n + kAhead + 1, false);
+            }
+        }
+        meet();
+        __builtin_amdgcn_s_setprio(1);
+        if (seen(i)) accumulate<D, 2>(s, vt[S], pw);
+        if (seen(i + 1)) scores<D, 2>(s, kt[(S + 1) % kWideStages], z);
+        __builtin_amdgcn_s_setprio(0);
+        meet();
+    };
+    static_assert(kWideStages == 4, "the loop is unrolled over the places");
+    for (int i = 0; i < tiles; i += 4) {
+        step(std::integral_constant<int, 0>(), i);
+        if (i + 1 < tiles) step(std::integral_constant<int, 1>(), i + 1);
+        if (i + 2 < tiles) step(std::integral_constant<int, 2>(), i + 2);
+        if (i + 3 < tiles) step(std::integral_constant<int, 3>(), i + 3);
+    }
+    if (!behind) meet();
+    if (rows.missing()) any_missing = 1;
+    __syncthreads();
+    const bool missing = any_missing != 0;
+    if (missing && tid == 0 && a.status) atomicOr(a.status, kStatusPage);
 
     const float l = s.l + __shfl_xor(s.l, 32);
     const bool whole = t.span.parts == 1;
@@ -551,11 +731,11 @@ __global__ __launch_bounds__(kWideThreads, 2) void attend_wide_kernel(AttendArgs
             if (p.real) store4<true>(a, t, part, r, p.row, D, 32 * i + 8 * g + 4 * half, v);
         }
     if (p.real && !whole && half == 0) store_ml<true>(a, t, part, r, s.m, l);
-    const uint64_t mask = __ballot(bad && p.real);
-    const uint32_t rows = (uint32_t)mask | (uint32_t)(mask >> 32);
-    if (rows) {
+    const uint64_t mask = __ballot((bad || missing) && p.real);
+    const uint32_t again = (uint32_t)mask | (uint32_t)(mask >> 32);
+    if (again) {
         __threadfence();                                     // the rows' first results have landed
-        redo_rows<D, FP8, true>(a, t, part, kv, 32 * wave, rows);
+        redo_rows<D, FP8, true>(a, t, part, kv, 32 * wave, again);
     }
 }
 
@@ -584,7 +764,7 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void attend_narrow_kernel(Attend
     Rows<D> s;
     load_q<D>(a, p, s);
     clear_rows<D>(s);
-    int all_lo = p.lo, all_hi = p.real ? p.hi : INT32_MAX;
+    int all_lo = p.lo, all_hi = p.real ? p.hi : W4_MAX_CONTEXT;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
         all_lo = max(all_lo, __shfl_xor(all_lo, off));
@@ -596,49 +776,37 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void attend_narrow_kernel(Attend
     const int k0 = (int)t.k0, k1 = (int)t.k1;
     uint8_t* kt = tiles_lds[wave];
     uint8_t* vt = kt + kTileBytes;
-    const int page_mask = (1 << a.page_shift) - 1;
     const int crow = lane / kChunks, chunk = lane % kChunks;
+    const uint32_t lane_byte = (crow & 15) * kRowBytes + 16 * chunk;
     // A page holds 16 keys at least and tiles begin at multiples of 32, so either half of a tile
     // lies in one page: two lookups a tile, the same for all lanes.
-    const int32_t* table = a.table + (int64_t)t.b * a.max_pages;
+    Rows16<kRowBytes> rows(a, t.b, kv, k1);
     int entry[2];                                            // table entries of the next tile
     u32x4_t kw[kLoads], vw[kLoads];
     float sc = 1.0f;
-    bool bad_page = false, ok[2] = {false, false};
     auto look_up = [&](int i, int* e) {                      // read here, used a tile later
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int key = k0 + i * kKeys + 16 * h;
-            e[h] = table[(key < k1 ? key : k1 - 1) >> a.page_shift];
-        }
+        for (int h = 0; h < 2; ++h) e[h] = rows.entry(k0 + i * kKeys + 16 * h);
     };
-    auto fetch = [&](int i, const int* e) {
-        int64_t base[2];                                     // cache row of each half's first key
+    auto fetch = [&](int i) {
+        uint64_t off[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int key = k0 + i * kKeys + 16 * h;
-            const int64_t page = checked_page(__builtin_amdgcn_readfirstlane(e[h]), a.pages);
-            bad_page |= key < k1 && page < 0;
-            ok[h] = key < k1 && page >= 0;
-            // another page's rows stand in for those of a page that is not there
-            base[h] = ok[h] ? ((page * a.kv_heads + kv) << a.page_shift) + (key & page_mask) : 0;
-        }
+        for (int h = 0; h < 2; ++h) off[h] = rows.offset(entry[h], k0 + i * kKeys + 16 * h);
 #pragma unroll
         for (int c = 0; c < kLoads; ++c) {
-            const int row = (c * kStepRows + crow) & 15;
-            const int64_t from = base[(c * kStepRows) >> 4] * kRowBytes;
-            kw[c] = *reinterpret_cast<const u32x4_t*>(static_cast<const uint8_t*>(a.k) + from + row * kRowBytes + 16 * chunk);
-            vw[c] = *reinterpret_cast<const u32x4_t*>(static_cast<const uint8_t*>(a.v) + from + row * kRowBytes + 16 * chunk);
+            const uint64_t from = off[(c * kStepRows) >> 4] + (c * kStepRows & 15) * kRowBytes;
+            kw[c] = load16(rows.k, from, lane_byte);
+            vw[c] = load16(rows.v, from, lane_byte);
         }
         if constexpr (FP8) {
-            const int64_t at = (lane & 16 ? base[1] : base[0]) + (lane & 15);
-            sc = (lane < 32 ? a.k_scales : a.v_scales)[at];
+            const uint64_t at = (lane & 16 ? off[1] : off[0]) / kRowBytes + (lane & 15);
+            sc = (lane < 32 ? rows.ks : rows.vs)[at];
         }
     };
     const int tiles = (k1 - k0 + kKeys - 1) / kKeys;
     if (wave < tiles) {
         look_up(wave, entry);
-        fetch(wave, entry);
+        fetch(wave);
         look_up(wave + kNarrowWaves, entry);
     }
     for (int i = wave; i < tiles; i += kNarrowWaves) {
@@ -648,22 +816,24 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void attend_narrow_kernel(Attend
 #pragma unroll
         for (int c = 0; c < kLoads; ++c) {
             const int row = c * kStepRows + crow;
-            const bool keep = ok[(c * kStepRows) >> 4] && first + row < k1;
-            stage<D, FP8, false>(kt, row, chunk, kw[c], keep);
-            stage<D, FP8, true>(vt, row, chunk, vw[c], keep);
+            stage<D, FP8, false>(kt, row, chunk, kw[c], k1 - first);
+            stage<D, FP8, true>(vt, row, chunk, vw[c], k1 - first);
         }
-        if constexpr (FP8) scales[wave][lane] = ok[(lane & 31) >> 4] && first + (lane & 31) < k1 ? sc : 1.0f;
+        if constexpr (FP8) scales[wave][lane] = first + (lane & 31) < k1 ? sc : 1.0f;
         if (i + kNarrowWaves < tiles) {
-            fetch(i + kNarrowWaves, entry);
+            fetch(i + kNarrowWaves);
             entry[0] = later[0];
             entry[1] = later[1];
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // rows staged by other lanes
-        attend_step<D, FP8, 1>(s, kt, vt, scales[wave], scales[wave] + kKeys, a.scale_log2, first, p.lo, p.hi,
-                               first < all_lo || first + kKeys - 1 > all_hi);
+        f32x16_t z[1];
+        uint32_t pw[8];
+        scores<D, 1>(s, kt, z);
+        weights<D, FP8, 1>(s, z, pw, scales[wave], scales[wave] + kKeys, a.scale_log2, first, p.lo, p.count,
+                           first < all_lo || first + kKeys - 1 > all_hi);
+        accumulate<D, 1>(s, vt, pw);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // read before the next rows land
     }
-    if (bad_page && lane == 0 && a.status) atomicOr(a.status, kStatusPage);
 
     // Join the waves: O of wave w counts 2^(m_w - m).
     const int half = lane >> 5;
@@ -719,6 +889,10 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void attend_narrow_kernel(Attend
     __shared__ uint32_t redo;
     if (tid == 0) redo = 0;
     __syncthreads();
+    if (rows.missing()) {
+        bad_rows = (uint32_t)(((uint64_t)1 << rows_here) - 1);
+        if (lane == 0 && a.status) atomicOr(a.status, kStatusPage);
+    }
     if (bad_rows) atomicOr(&redo, bad_rows);
     __syncthreads();
     if (redo) {
