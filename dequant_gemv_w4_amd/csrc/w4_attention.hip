@@ -131,23 +131,58 @@ __device__ __forceinline__ void clear_rows(Rows<D>& s) {
     s.l = 0.0f;
 }
 
-// A step takes NB blocks of 32 keys in three parts.  scores: z = K q for the staged keys kt.
-template <int D, int NB>
+// A step takes NB blocks of 32 keys in three parts.  The products read their left operands from LDS,
+// which answers after about 130 cycles; a product takes 32.  With AHEAD the operands of four products
+// are read while the four before them are in the matrix unit, and held to that order: left alone the
+// compiler reads two to eight ahead, by what registers seem free (a chunk of 2048 + 1889 tokens: 737 us
+// when it read eight ahead, 790 with two).
+__device__ __forceinline__ void hold_order() { __builtin_amdgcn_sched_barrier(0); }
+
+// scores: z = K q for the staged keys kt.
+template <int D, int NB, bool AHEAD>
 __device__ __forceinline__ void scores(const Rows<D>& s, const uint8_t* kt, f32x16_t (&z)[NB]) {
+    constexpr int kSteps = 4 / NB;                           // of the inner dimension in a group
+    constexpr int kGroups = D / 16 / kSteps;
     const int lane = threadIdx.x & 63, half = lane >> 5, l32 = lane & 31;
+    auto operand = [&](int d, int b) {
+        return *reinterpret_cast<const u32x4_t*>(kt + k_place<D>(32 * b + l32, 2 * d + half));
+    };
+    auto multiply = [&](u32x4_t a, int d, int b) {
+        z[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                       __builtin_bit_cast(bf16x8_t, s.q[d]), z[b], 0, 0, 0);
+    };
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int r = 0; r < 16; ++r) z[b][r] = 0.0f;
+    if constexpr (AHEAD) {
+        u32x4_t a[2][4];
 #pragma unroll
-    for (int d = 0; d < D / 16; ++d) {
+        for (int g = 0; g <= kGroups; ++g) {
+            if (g < kGroups) {
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            const u32x4_t a = *reinterpret_cast<const u32x4_t*>(kt + k_place<D>(32 * b + l32, 2 * d + half));
-            z[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
-                                                           __builtin_bit_cast(bf16x8_t, s.q[d]), z[b], 0, 0, 0);
+                for (int j = 0; j < 4; ++j) a[g & 1][j] = operand(g * kSteps + j / NB, j % NB);
+            }
+            hold_order();
+            if (g > 0) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) multiply(a[(g - 1) & 1][j], (g - 1) * kSteps + j / NB, j % NB);
+            }
+            hold_order();
         }
+    } else {
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) multiply(operand(d, b), d, b);
     }
+}
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)p;
+}
+__device__ __forceinline__ f32x4_t read_lds_f32x4(uint32_t address) {
+    return *(__attribute__((address_space(3))) const f32x4_t*)(uintptr_t)address;
 }
 
 // Maximum over a lane and the one 32 lanes away.
@@ -158,19 +193,19 @@ __device__ __forceinline__ float half_max(float x) {
 }
 
 // weights: the running maximum and sum, and the bfloat16 weights p (as the right operand of 16 keys
-// each: p[4 c .. 4 c + 3]).  ks, vs: scales of the keys' and values' rows (FP8); first: position of
+// each: p[4 c .. 4 c + 3]).  ks, vs: LDS addresses of the scales of the keys' and values' rows, from row 4 half on (FP8); first: position of
 // the first key; the row sees the `count` keys from lo; mask: whether the step reaches outside some
 // row's.
 template <int D, bool FP8, int NB>
-__device__ __forceinline__ void weights(Rows<D>& s, f32x16_t (&z)[NB], uint32_t (&p)[8 * NB], const float* ks,
-                                        const float* vs, float scale, int first, int lo, int count, bool mask) {
+__device__ __forceinline__ void weights(Rows<D>& s, f32x16_t (&z)[NB], uint32_t (&p)[8 * NB], uint32_t ks,
+                                        uint32_t vs, float scale, int first, int lo, int count, bool mask) {
     const int half = (threadIdx.x & 63) >> 5;
     if constexpr (FP8) {
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const f32x4_t f = *reinterpret_cast<const f32x4_t*>(ks + 32 * b + 8 * i + 4 * half);
+                const f32x4_t f = read_lds_f32x4(ks + 4 * (32 * b + 8 * i));
 #pragma unroll
                 for (int j = 0; j < 4; ++j) z[b][4 * i + j] *= f[j];
             }
@@ -211,7 +246,7 @@ __device__ __forceinline__ void weights(Rows<D>& s, f32x16_t (&z)[NB], uint32_t 
             sum[0] += e0;
             sum[1] += e1;
             if constexpr (FP8) {
-                if ((i & 1) == 0) f = *reinterpret_cast<const f32x4_t*>(vs + 32 * b + 4 * i + 4 * half);
+                if ((i & 1) == 0) f = read_lds_f32x4(vs + 4 * (32 * b + 4 * i));
                 p[8 * b + i] = bf16_pair(e0 * f[2 * (i & 1)], e1 * f[2 * (i & 1) + 1]);
             } else {
                 p[8 * b + i] = bf16_pair(e0, e1);
@@ -222,39 +257,64 @@ __device__ __forceinline__ void weights(Rows<D>& s, f32x16_t (&z)[NB], uint32_t 
 }
 
 // accumulate: O += V p for the staged values vt.
-template <int D, int NB>
+template <int D, int NB, bool AHEAD>
 __device__ __forceinline__ void accumulate(Rows<D>& s, const uint8_t* vt, const uint32_t (&p)[8 * NB]) {
+    constexpr int kBlocks = D / 32, kSteps = 4 / kBlocks;    // blocks of columns; steps of 16 keys in a group
+    constexpr int kGroups = 2 * NB / kSteps;
     const int lane = threadIdx.x & 63, half = lane >> 5, i16 = lane & 15, g16 = (lane >> 4) & 1;
-#pragma unroll
-    for (int c = 0; c < 2 * NB; ++c) {                       // 16 keys each
-        const u32x4_t pb = {p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]};
+    auto operand = [&](int c, int i) {                       // 16 keys, 32 columns
         const int r0 = 16 * c + 4 * half + (i16 >> 2);
+        const int chunk = 4 * i + 2 * g16 + ((i16 & 3) >> 1), off = 8 * (i16 & 1);
+        const uint64_t a0 = read_tr(vt + v_place<D>(r0, chunk) + off);
+        const uint64_t a1 = read_tr(vt + v_place<D>(r0 + 8, chunk) + off);
+        return u32x4_t{(uint32_t)a0, (uint32_t)(a0 >> 32), (uint32_t)a1, (uint32_t)(a1 >> 32)};
+    };
+    auto multiply = [&](u32x4_t a, int c, int i) {
+        const u32x4_t pb = {p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]};
+        s.o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                         __builtin_bit_cast(bf16x8_t, pb), s.o[i], 0, 0, 0);
+    };
+    if constexpr (AHEAD) {
+        u32x4_t a[2][4];
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            const int chunk = 4 * i + 2 * g16 + ((i16 & 3) >> 1), off = 8 * (i16 & 1);
-            const uint64_t a0 = read_tr(vt + v_place<D>(r0, chunk) + off);
-            const uint64_t a1 = read_tr(vt + v_place<D>(r0 + 8, chunk) + off);
-            const u32x4_t a = {(uint32_t)a0, (uint32_t)(a0 >> 32), (uint32_t)a1, (uint32_t)(a1 >> 32)};
-            s.o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
-                                                             __builtin_bit_cast(bf16x8_t, pb), s.o[i], 0, 0, 0);
+        for (int g = 0; g <= kGroups; ++g) {
+            if (g < kGroups) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) a[g & 1][j] = operand(g * kSteps + j / kBlocks, j % kBlocks);
+            }
+            hold_order();
+            if (g > 0) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) multiply(a[(g - 1) & 1][j], (g - 1) * kSteps + j / kBlocks, j % kBlocks);
+            }
+            hold_order();
         }
+    } else {
+#pragma unroll
+        for (int c = 0; c < 2 * NB; ++c)
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i) multiply(operand(c, i), c, i);
     }
 }
 
-// Which sequence a number belongs to: the last b with key(b) <= x, by all lanes of a wave (the
-// keys of 64 sequences at a time, so two rounds of loads for up to 4096 sequences).
+// The last sequence b with key(cu[b], b) <= x, by all lanes of a wave: 64 sequences at a time, so two
+// rounds of loads for up to 4096 sequences.  The sequence's own numbers are loaded in the same round.
 template <typename Key>
-__device__ __forceinline__ int find_seq(int B, Key key, int64_t x) {
+__device__ __forceinline__ Seq find_seq(const AttendArgs& a, Key key, int64_t x, int& found, int64_t& cu_found) {
     const int lane = threadIdx.x & 63;
     int base = 0;
-    for (int step = B > 64 ? 64 : 1;; step = 1) {
-        const int b = base + lane * step;
-        const bool below = b < B && key(b) <= x;
-        const int n = __popcll(__ballot(below));
-        if (n == 0) return base;                             // only at the start: key(0) > x
-        base += (n - 1) * step;
-        if (step == 1) return base;
+    if (a.B > 64) {
+        const int b = lane * 64;
+        const bool below = b < a.B && key(a.cu[b], b) <= x;
+        base = __builtin_amdgcn_readfirstlane(max(__popcll(__ballot(below)) - 1, 0) * 64);
     }
+    const int b = min(base + lane, a.B - 1);
+    const int cu0 = a.cu[b], cu1 = a.cu[b + 1], len = a.lens[b];
+    const int at = __builtin_amdgcn_readfirstlane(max(__popcll(__ballot(base + lane < a.B && key(cu0, b) <= x)) - 1, 0));
+    found = base + at;
+    const int f0 = __builtin_amdgcn_readlane(cu0, at), f1 = __builtin_amdgcn_readlane(cu1, at);
+    cu_found = f0;
+    return clamp_seq(f0, f1, __builtin_amdgcn_readlane(len, at), a.T, a.max_pages << a.page_shift);
 }
 
 __device__ __forceinline__ Seq load_seq(const AttendArgs& a, int b) {
@@ -342,21 +402,22 @@ struct Tile {
 // sequence of at most kNarrowRows rows is the narrow kernel's, as its only tile, and the narrow
 // launch has one tile a sequence.
 template <bool WIDE>
-__device__ __forceinline__ Tile find_tile(const AttendArgs& a, int64_t index, int part, int& kv) {
+__device__ __forceinline__ Tile find_tile(const AttendArgs& a, uint32_t index, int part, int& kv) {
     constexpr int R = WIDE ? kWideRows : kNarrowRows;
     Tile t;
     const int G = a.group;
-    kv = (int)(index % a.kv_heads);
-    const int64_t tile = index / a.kv_heads;
-    t.part_row = index * R;
+    const int tile = __builtin_amdgcn_readfirstlane((int)(index / (uint32_t)a.kv_heads));
+    kv = (int)index - tile * a.kv_heads;
+    t.part_row = (int64_t)index * R;
     if (!WIDE && a.both) {
-        t.b = (int)tile;
+        t.b = tile;
         t.row0 = 0;
+        t.seq = load_seq(a, t.b);
     } else {
-        t.b = find_seq(a.B, [&](int b) { return first_tile(a.cu[b], b, G, R); }, tile);
-        t.row0 = (tile - first_tile(a.cu[t.b], t.b, G, R)) * R;
+        int64_t cu;
+        t.seq = find_seq(a, [&](int64_t cu_b, int64_t b) { return first_tile(cu_b, b, G, R); }, tile, t.b, cu);
+        t.row0 = (tile - first_tile(cu, t.b, G, R)) * R;
     }
-    t.seq = load_seq(a, t.b);
     t.rows = t.seq.n * G;
     const bool few = t.rows <= kNarrowRows;
     t.run = t.row0 >= 0 && t.row0 < t.rows && (WIDE ? !few : few || !a.both);
@@ -510,9 +571,6 @@ __device__ __forceinline__ void load_lds16(const uint8_t* base, uint32_t lane_by
                  : "v"(lane_byte), "s"(base), "s"(__builtin_amdgcn_readfirstlane(lds))
                  : "memory", "m0");
 }
-__device__ __forceinline__ uint32_t lds_address(const void* p) {
-    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)p;
-}
 
 constexpr int kWideWaves = 8;
 constexpr int kWideStages = 4;
@@ -526,16 +584,15 @@ __global__ __launch_bounds__(kWideThreads, 2) void attend_wide_kernel(AttendArgs
     constexpr int kLoads = kStepRows >= kKeyTile ? 1 : kKeyTile / kStepRows;
     constexpr int kTileBytes = kKeyTile * 2 * D;
     __shared__ __attribute__((aligned(16))) uint8_t kt[kWideStages][kTileBytes], vt[kWideStages][kTileBytes];
-    __shared__ __attribute__((aligned(16))) float ksc[FP8 ? kWideStages : 1][kKeyTile], vsc[FP8 ? kWideStages : 1][kKeyTile];
+    __shared__ __attribute__((aligned(16))) float sc_lds[2][FP8 ? kWideStages : 1][kKeyTile];   // of keys, of values
     __shared__ int any_missing;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int part = blockIdx.y;
     int kv;
     // the last tiles of a sequence see the most keys: they start first
-    const Tile t = find_tile<true>(a, (int64_t)gridDim.x - 1 - blockIdx.x, part, kv);
+    const Tile t = find_tile<true>(a, gridDim.x - 1 - blockIdx.x, part, kv);
     if (!t.run) return;
-    const int r = 32 * wave + (lane & 31);
-    const Place p = row_place(a, t, kv, t.row0 + r);
+    Place p = row_place(a, t, kv, t.row0 + 32 * wave + (lane & 31));
     Rows<D> s;
     load_q<D>(a, p, s);
     clear_rows<D>(s);
@@ -553,13 +610,14 @@ __global__ __launch_bounds__(kWideThreads, 2) void attend_wide_kernel(AttendArgs
     all_lo = __builtin_amdgcn_readfirstlane(all_lo);
     all_hi = __builtin_amdgcn_readfirstlane(all_hi);
 
-    const int k0 = (int)t.k0, k1 = (int)t.k1;
+    // the same for all, which the compiler has to know for what follows to stay in scalar registers
+    const int k0 = __builtin_amdgcn_readfirstlane((int)t.k0), k1 = __builtin_amdgcn_readfirstlane((int)t.k1);
     const int tiles = (k1 - k0 + kKeyTile - 1) / kKeyTile;
     const int crow = tid / kChunks, chunk = tid % kChunks;
     const bool loads = kStepRows * kLoads == kKeyTile || crow < kKeyTile;   // else more threads than chunks
     // The rows that one load of a wave covers lie in one aligned group of 16, so in one page.
     const int granule = __builtin_amdgcn_readfirstlane(crow & ~15) & (kKeyTile - 1);
-    Rows16<kRowBytes> rows(a, t.b, kv, k1);
+    Rows16<kRowBytes> rows(a, __builtin_amdgcn_readfirstlane(t.b), __builtin_amdgcn_readfirstlane(kv), k1);
     int entry[kLoads];                                       // of the tile whose keys are brought next
     uint64_t off[kLoads];                                    // of the tile whose values are brought next
     auto look_up = [&](int i) {                              // read here, used by locate
@@ -608,11 +666,13 @@ __global__ __launch_bounds__(kWideThreads, 2) void attend_wide_kernel(AttendArgs
     };
     auto put = [&](int i, bool values) {                     // FP8: what bring loaded
         if (!loads) return;
+        int at = i % kWideStages;
+        asm volatile("" : "+s"(at));                         // addresses formed here, not kept for every place
         if (values) {
-            stage<D, true, true>(vt[i % kWideStages], crow, chunk, vw, left(i));
+            stage<D, true, true>(vt[at], crow, chunk, vw, left(i));
         } else {
-            stage<D, true, false>(kt[i % kWideStages], crow, chunk, kw, left(i));
-            if (chunk < 2) (chunk == 0 ? ksc : vsc)[FP8 ? i % kWideStages : 0][crow] = crow < left(i) ? sc : 1.0f;
+            stage<D, true, false>(kt[at], crow, chunk, kw, left(i));
+            if (chunk < 2) sc_lds[chunk][FP8 ? at : 0][crow] = crow < left(i) ? sc : 1.0f;
         }
     };
     // Waits for this wave's LDS accesses and then for the other waves; loads of the cache stay in
@@ -646,6 +706,8 @@ __global__ __launch_bounds__(kWideThreads, 2) void attend_wide_kernel(AttendArgs
     // written over by those of tile i+4 in phase 2i+5 at the earliest.
     constexpr int kAhead = FP8 ? 1 : 2;                      // pairs in flight
     const int behind = wave >> 2;                            // 1 for waves 4-7
+    uint32_t sc_lane = lds_address(&sc_lds[0][0][0]) + 16 * (lane >> 5);
+    asm volatile("" : "+v"(sc_lane));                        // one register for all places
     f32x16_t z[2];
     uint32_t pw[16];
     if (tid == 0) any_missing = 0;
@@ -668,7 +730,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void attend_wide_kernel(AttendArgs
         if (!FP8 && tiles < 2) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
     meet();
-    if (seen(0)) scores<D, 2>(s, kt[0], z);
+    if (seen(0)) scores<D, 2, true>(s, kt[0], z);
     if (behind) meet();
     // One step, tile i in place S = i % kWideStages.
     auto step = [&](auto place, int i) {
@@ -676,7 +738,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void attend_wide_kernel(AttendArgs
         const int n = i + behind;
         look_up(n + kAhead + 1);
         if (seen(i))
-            weights<D, FP8, 2>(s, z, pw, ksc[FP8 ? S : 0], vsc[FP8 ? S : 0], a.scale_log2, k0 + i * kKeyTile, p.lo,
+            weights<D, FP8, 2>(s, z, pw, sc_lane + 4 * S * kKeyTile, sc_lane + 4 * (kWideStages + S) * kKeyTile, a.scale_log2, k0 + i * kKeyTile, p.lo,
                                p.count, i < whole_lo || i > whole_hi);
         if (n >= 1 && n < tiles) {
             if constexpr (FP8) {
@@ -695,8 +757,12 @@ __global__ __launch_bounds__(kWideThreads, 2) void attend_wide_kernel(AttendArgs
         }
         meet();
         __builtin_amdgcn_s_setprio(1);
-        if (seen(i)) accumulate<D, 2>(s, vt[S], pw);
-        if (seen(i + 1)) scores<D, 2>(s, kt[(S + 1) % kWideStages], z);
+        if (seen(i)) {
+            accumulate<D, 2, true>(s, vt[S], pw);
+        }
+        if (seen(i + 1)) {
+            scores<D, 2, true>(s, kt[(S + 1) % kWideStages], z);
+        }
         __builtin_amdgcn_s_setprio(0);
         meet();
     };
@@ -713,6 +779,10 @@ __global__ __launch_bounds__(kWideThreads, 2) void attend_wide_kernel(AttendArgs
     const bool missing = any_missing != 0;
     if (missing && tid == 0 && a.status) atomicOr(a.status, kStatusPage);
 
+    // where the row goes is found again here: kept through the loop it would cost registers
+    int r = 32 * wave + (lane & 31);
+    asm volatile("" : "+v"(r));
+    p = row_place(a, t, kv, t.row0 + r);
     const float l = s.l + __shfl_xor(s.l, 32);
     const bool whole = t.span.parts == 1;
     const float inv = inverse(l, whole && p.hi >= 0);
@@ -773,14 +843,15 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void attend_narrow_kernel(Attend
     all_lo = __builtin_amdgcn_readfirstlane(all_lo);
     all_hi = __builtin_amdgcn_readfirstlane(all_hi);
 
-    const int k0 = (int)t.k0, k1 = (int)t.k1;
+    // the same for all, which the compiler has to know for what follows to stay in scalar registers
+    const int k0 = __builtin_amdgcn_readfirstlane((int)t.k0), k1 = __builtin_amdgcn_readfirstlane((int)t.k1);
     uint8_t* kt = tiles_lds[wave];
     uint8_t* vt = kt + kTileBytes;
     const int crow = lane / kChunks, chunk = lane % kChunks;
     const uint32_t lane_byte = (crow & 15) * kRowBytes + 16 * chunk;
     // A page holds 16 keys at least and tiles begin at multiples of 32, so either half of a tile
     // lies in one page: two lookups a tile, the same for all lanes.
-    Rows16<kRowBytes> rows(a, t.b, kv, k1);
+    Rows16<kRowBytes> rows(a, __builtin_amdgcn_readfirstlane(t.b), __builtin_amdgcn_readfirstlane(kv), k1);
     int entry[2];                                            // table entries of the next tile
     u32x4_t kw[kLoads], vw[kLoads];
     float sc = 1.0f;
@@ -803,6 +874,7 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void attend_narrow_kernel(Attend
             sc = (lane < 32 ? rows.ks : rows.vs)[at];
         }
     };
+    const uint32_t sc_lane = lds_address(scales[wave]) + 16 * (lane >> 5);
     const int tiles = (k1 - k0 + kKeys - 1) / kKeys;
     if (wave < tiles) {
         look_up(wave, entry);
@@ -828,10 +900,10 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void attend_narrow_kernel(Attend
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // rows staged by other lanes
         f32x16_t z[1];
         uint32_t pw[8];
-        scores<D, 1>(s, kt, z);
-        weights<D, FP8, 1>(s, z, pw, scales[wave], scales[wave] + kKeys, a.scale_log2, first, p.lo, p.count,
+        scores<D, 1, false>(s, kt, z);
+        weights<D, FP8, 1>(s, z, pw, sc_lane, sc_lane + 4 * kKeys, a.scale_log2, first, p.lo, p.count,
                            first < all_lo || first + kKeys - 1 > all_hi);
-        accumulate<D, 1>(s, vt, pw);
+        accumulate<D, 1, false>(s, vt, pw);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // read before the next rows land
     }
 
@@ -905,12 +977,12 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void attend_narrow_kernel(Attend
 // Joins the parts of the rows that were split: one wave a row, the tiles numbered as in the
 // launch that wrote them.
 template <int D, bool WIDE>
-__global__ __launch_bounds__(256) void combine_kernel(AttendArgs a) {
+__device__ __forceinline__ void combine_rows(const AttendArgs& a, uint32_t set) {
     constexpr int E = D / 64, kSets = (WIDE ? kWideRows : kNarrowRows) / 4;
     const int lane = threadIdx.x & 63;
     int kv;
-    const Tile t = find_tile<WIDE>(a, blockIdx.x / kSets, 0, kv);
-    const int r = (int)(blockIdx.x % kSets) * 4 + (threadIdx.x >> 6);
+    const Tile t = find_tile<WIDE>(a, set / kSets, 0, kv);
+    const int r = (int)(set % kSets) * 4 + (threadIdx.x >> 6);
     if (!t.run || t.span.parts == 1 || t.row0 + r >= t.rows) return;
     const Place place = row_place(a, t, kv, t.row0 + r);
     const Parts<WIDE> w(a);
@@ -932,14 +1004,18 @@ __global__ __launch_bounds__(256) void combine_kernel(AttendArgs a) {
     float o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.0f;
-#pragma unroll 8
-    for (int p = 0; p < parts; ++p) {
-        const float fp = __shfl(f, p);
-        float x[E];
+    for (int p0 = 0; p0 < parts; p0 += 4) {                  // the loads of four parts at once
+        float x[4][E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = w.o[w.at(t, p, r) * D + lane * E + e];
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] += fp == 0.0f ? 0.0f : fp * x[e];
+            for (int e = 0; e < E; ++e) x[j][e] = w.o[w.at(t, min(p0 + j, parts - 1), r) * D + lane * E + e];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float fp = p0 + j < parts ? __shfl(f, p0 + j) : 0.0f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] += fp == 0.0f ? 0.0f : fp * x[j][e];
+        }
     }
     const float inv = inverse(sum, place.hi >= 0);
     if constexpr (E == 2)
@@ -948,7 +1024,19 @@ __global__ __launch_bounds__(256) void combine_kernel(AttendArgs a) {
         a.o[place.row * D + lane] = (uint16_t)bf16_pair(o[0] * inv, o[0] * inv);
 }
 
-// Parts that a launch allows per tile: enough to give every compute unit `target` / 256 workgroups.
+template <int D>
+__global__ __launch_bounds__(256) void combine_kernel(AttendArgs a) {
+    const uint32_t narrow = (uint32_t)(a.narrow_rows / 4);
+    if (blockIdx.x < narrow)
+        combine_rows<D, false>(a, blockIdx.x);
+    else
+        combine_rows<D, true>(a, blockIdx.x - narrow);
+}
+
+// Parts that a launch allows per tile, to make `target` workgroups.  Narrow: 256, one a compute unit
+// (LDS holds no second): 32 requests of up to 8192 tokens take 155 us with 256 (unsplit), 165 with 512,
+// 168 with 1024; two of 100,000 tokens 85, 92 and 110.  At least 512 keys a part: one request of 4000
+// tokens (8 kv heads) takes 16 us with parts of 512, 17.3 with 256, 18.5 with 1024.
 int parts_for(int64_t tiles, int64_t target, int64_t longest, int64_t least) {
     const int64_t want = ceil_div(target, tiles);
     return (int)imax(1, imin(want, imin(ceil_div(longest, least), kMaxParts)));
@@ -961,7 +1049,7 @@ void plan_attend(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int64_t 
     // One token a sequence, or too few rows for the wide kernel: no sequence needs it.
     p->both = T != B && T * G > kNarrowRows;
     p->narrow_tiles = (p->both ? B : tile_bound(T, B, G, kNarrowRows)) * kv_heads;
-    p->narrow_parts = parts_for(p->narrow_tiles, 512, capacity, kNarrowLeast);
+    p->narrow_parts = parts_for(p->narrow_tiles, 256, capacity, kNarrowLeast);
     p->wide_tiles = p->both ? tile_bound(T, B, G, kWideRows) * kv_heads : 0;
     p->wide_parts = p->both ? parts_for(p->wide_tiles, 512, capacity, kWideLeast) : 1;
 }
@@ -985,12 +1073,8 @@ static hipError_t launch_attend_d(const AttendArgs& a, const AttendPlan& p, hipS
     hipLaunchKernelGGL((attend_narrow_kernel<D, FP8>), dim3((unsigned)p.narrow_tiles, (unsigned)p.narrow_parts),
                        dim3(kNarrowThreads), 0, s, a);
     e = hipGetLastError();
-    if (e == hipSuccess && a.wide_rows > 0) {
-        hipLaunchKernelGGL((combine_kernel<D, true>), dim3((unsigned)(a.wide_rows / 4)), dim3(256), 0, s, a);
-        e = hipGetLastError();
-    }
-    if (e == hipSuccess && a.narrow_rows > 0) {
-        hipLaunchKernelGGL((combine_kernel<D, false>), dim3((unsigned)(a.narrow_rows / 4)), dim3(256), 0, s, a);
+    if (e == hipSuccess && a.wide_rows + a.narrow_rows > 0) {
+        hipLaunchKernelGGL(combine_kernel<D>, dim3((unsigned)((a.wide_rows + a.narrow_rows) / 4)), dim3(256), 0, s, a);
         e = hipGetLastError();
     }
     return e;
