@@ -11,11 +11,13 @@
 // the lanes holds the keys 4h..4h+3 and 8+4h..8+4h+3 of each 16).  V stays in its row order and
 // is turned by ds_read_b64_tr_b16, which gives a lane four keys of one column.
 //
-// Rounding: scores, maximum, sum and O are binary32.  P is rounded to bfloat16 for the matrix
-// unit (each weight within 2^-8 relative; the same size as the rounding of the bfloat16 output,
-// and averaged over the keys), the sum takes the unrounded P.  E4M3 codes enter as exact bfloat16
-// values; the scale of a key's row multiplies its scores, that of a value's row its P, both in
-// binary32.
+// Rounding: scores, maximum, sum and O are binary32; the sum takes the unrounded P.  For the matrix unit
+// attend_wide rounds P to bfloat16 (each weight within 2^-8 relative; the same size as the rounding of
+// the bfloat16 output, and averaged over the keys: outputs are 1.4 times as far from 64 bits as an
+// unrounded P would leave them).  attend_narrow, which waits for memory, multiplies V by what that
+// rounding leaves as well (P = p + rest, both bfloat16, together within 2^-16): a decode step of 32
+// requests takes 156.5 us instead of 154.4.  E4M3 codes enter as exact bfloat16 values; the scale of a
+// key's row multiplies its scores, that of a value's row its P, both in binary32.
 //
 // attend_wide: 256 rows a workgroup, 8 waves of 32 rows; tiles of 64 keys pass through LDS for
 // all of them, the next tile's loads in flight, and the two waves of a SIMD take turns on the
@@ -193,11 +195,11 @@ __device__ __forceinline__ float half_max(float x) {
 }
 
 // weights: the running maximum and sum, and the bfloat16 weights p (as the right operand of 16 keys
-// each: p[4 c .. 4 c + 3]).  ks, vs: LDS addresses of the scales of the keys' and values' rows, from row 4 half on (FP8); first: position of
+// each: p[4 c .. 4 c + 3]), with REST followed by what their rounding leaves.  ks, vs: LDS addresses of the scales of the keys' and values' rows, from row 4 half on (FP8); first: position of
 // the first key; the row sees the `count` keys from lo; mask: whether the step reaches outside some
 // row's.
-template <int D, bool FP8, int NB>
-__device__ __forceinline__ void weights(Rows<D>& s, f32x16_t (&z)[NB], uint32_t (&p)[8 * NB], uint32_t ks,
+template <int D, bool FP8, int NB, bool REST>
+__device__ __forceinline__ void weights(Rows<D>& s, f32x16_t (&z)[NB], uint32_t (&p)[8 * NB * (REST ? 2 : 1)], uint32_t ks,
                                         uint32_t vs, float scale, int first, int lo, int count, bool mask) {
     const int half = (threadIdx.x & 63) >> 5;
     if constexpr (FP8) {
@@ -245,20 +247,24 @@ __device__ __forceinline__ void weights(Rows<D>& s, f32x16_t (&z)[NB], uint32_t 
             const float e1 = exp2_fast(fmaf(z[b][2 * i + 1], scale, -sub));
             sum[0] += e0;
             sum[1] += e1;
+            float w0 = e0, w1 = e1;
             if constexpr (FP8) {
                 if ((i & 1) == 0) f = read_lds_f32x4(vs + 4 * (32 * b + 4 * i));
-                p[8 * b + i] = bf16_pair(e0 * f[2 * (i & 1)], e1 * f[2 * (i & 1) + 1]);
-            } else {
-                p[8 * b + i] = bf16_pair(e0, e1);
+                w0 *= f[2 * (i & 1)];
+                w1 *= f[2 * (i & 1) + 1];
             }
+            p[8 * b + i] = bf16_pair(w0, w1);
+            if constexpr (REST)                              // what the rounding left, itself within 2^-8
+                p[8 * NB + 8 * b + i] = bf16_pair(w0 - __uint_as_float(p[8 * b + i] << 16),
+                                                  w1 - __uint_as_float(p[8 * b + i] & 0xFFFF0000u));
         }
     }
     s.l += sum[0] + sum[1];
 }
 
 // accumulate: O += V p for the staged values vt.
-template <int D, int NB, bool AHEAD>
-__device__ __forceinline__ void accumulate(Rows<D>& s, const uint8_t* vt, const uint32_t (&p)[8 * NB]) {
+template <int D, int NB, bool AHEAD, bool REST>
+__device__ __forceinline__ void accumulate(Rows<D>& s, const uint8_t* vt, const uint32_t (&p)[8 * NB * (REST ? 2 : 1)]) {
     constexpr int kBlocks = D / 32, kSteps = 4 / kBlocks;    // blocks of columns; steps of 16 keys in a group
     constexpr int kGroups = 2 * NB / kSteps;
     const int lane = threadIdx.x & 63, half = lane >> 5, i16 = lane & 15, g16 = (lane >> 4) & 1;
@@ -273,6 +279,11 @@ __device__ __forceinline__ void accumulate(Rows<D>& s, const uint8_t* vt, const 
         const u32x4_t pb = {p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]};
         s.o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
                                                          __builtin_bit_cast(bf16x8_t, pb), s.o[i], 0, 0, 0);
+        if constexpr (REST) {
+            const u32x4_t pr = {p[8 * NB + 4 * c], p[8 * NB + 4 * c + 1], p[8 * NB + 4 * c + 2], p[8 * NB + 4 * c + 3]};
+            s.o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                             __builtin_bit_cast(bf16x8_t, pr), s.o[i], 0, 0, 0);
+        }
     };
     if constexpr (AHEAD) {
         u32x4_t a[2][4];
@@ -738,7 +749,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void attend_wide_kernel(AttendArgs
         const int n = i + behind;
         look_up(n + kAhead + 1);
         if (seen(i))
-            weights<D, FP8, 2>(s, z, pw, sc_lane + 4 * S * kKeyTile, sc_lane + 4 * (kWideStages + S) * kKeyTile, a.scale_log2, k0 + i * kKeyTile, p.lo,
+            weights<D, FP8, 2, false>(s, z, pw, sc_lane + 4 * S * kKeyTile, sc_lane + 4 * (kWideStages + S) * kKeyTile, a.scale_log2, k0 + i * kKeyTile, p.lo,
                                p.count, i < whole_lo || i > whole_hi);
         if (n >= 1 && n < tiles) {
             if constexpr (FP8) {
@@ -758,7 +769,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void attend_wide_kernel(AttendArgs
         meet();
         __builtin_amdgcn_s_setprio(1);
         if (seen(i)) {
-            accumulate<D, 2, true>(s, vt[S], pw);
+            accumulate<D, 2, true, false>(s, vt[S], pw);
         }
         if (seen(i + 1)) {
             scores<D, 2, true>(s, kt[(S + 1) % kWideStages], z);
@@ -899,11 +910,11 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void attend_narrow_kernel(Attend
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // rows staged by other lanes
         f32x16_t z[1];
-        uint32_t pw[8];
+        uint32_t pw[16];
         scores<D, 1, false>(s, kt, z);
-        weights<D, FP8, 1>(s, z, pw, sc_lane, sc_lane + 4 * kKeys, a.scale_log2, first, p.lo, p.count,
+        weights<D, FP8, 1, true>(s, z, pw, sc_lane, sc_lane + 4 * kKeys, a.scale_log2, first, p.lo, p.count,
                            first < all_lo || first + kKeys - 1 > all_hi);
-        accumulate<D, 1, false>(s, vt, pw);
+        accumulate<D, 1, false, true>(s, vt, pw);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // read before the next rows land
     }
 

@@ -497,8 +497,9 @@ w4_status w4_block_tables(const int32_t* new_lens, const int32_t* lens_in, int64
  * A key in a page that the cache does not have reads as zeros (K and V) and sets W4_STATUS_PAGE
  * in d_status (optional).  What lies in the cache behind a request's keys, and at keys that a
  * row does not see, does not reach the row, NaN and infinities included.
- * Scores, softmax sums and outputs are formed in binary32; the weights are rounded to bfloat16
- * for the matrix units and o once.  Deterministic; the split of the work depends on the
+ * Scores, softmax sums and outputs are formed in binary32 and o is rounded once; requests with at
+ * most 32 rows (tokens times query heads of a kv head), or all where T = B, multiply V by weights
+ * held in two bfloat16 parts (2^-16), longer chunks by weights rounded to bfloat16.  Deterministic; the split of the work depends on the
  * arguments and lengths only.
  * Requires 1 <= T <= W4_MAX_TOKENS, 1 <= B <= W4_MAX_SEQUENCES, heads a multiple of kv_heads,
  * T * heads < 2^26, 1 <= max_pages, max_pages * page_size <= W4_MAX_CONTEXT.
