@@ -100,7 +100,7 @@ w4_status check_cache_pointers(const w4_kv_cache* c) {
 
 w4_status check_heads(int64_t T, int64_t heads, const w4_kv_cache* c) {
     if (T < 1 || T > W4_MAX_TOKENS || heads < c->kv_heads || heads % c->kv_heads != 0 ||
-        heads >= ((int64_t)1 << 26) / T)
+        heads > 65536 || heads >= ((int64_t)1 << 26) / T)
         return W4_ERR_SHAPE;
     return W4_OK;
 }

@@ -431,7 +431,7 @@ typedef struct {
  * Angles are formed in binary64, rotations in binary32, results rounded once: q and a bfloat16
  * cache to nearest even, rows of an E4M3 cache as w4_fp8_quantize_rows with K = head_dim would
  * the binary32 row (d_status: W4_STATUS_NONFINITE).  Requires 1 <= T <= W4_MAX_TOKENS,
- * heads a multiple of kv_heads, T * heads < 2^26, rotary_dim <= head_dim.
+ * heads a multiple of kv_heads, at most 65536, T * heads < 2^26, rotary_dim <= head_dim.
  */
 typedef enum { W4_ROPE_NONE = 0, W4_ROPE_LINEAR = 1, W4_ROPE_BANDS = 2, W4_ROPE_RAMP = 3 } w4_rope_scaling;
 typedef struct {
@@ -501,8 +501,8 @@ w4_status w4_block_tables(const int32_t* new_lens, const int32_t* lens_in, int64
  * most 32 rows (tokens times query heads of a kv head), or all where T = B, multiply V by weights
  * held in two bfloat16 parts (2^-16), longer chunks by weights rounded to bfloat16.  Deterministic; the split of the work depends on the
  * arguments and lengths only.
- * Requires 1 <= T <= W4_MAX_TOKENS, 1 <= B <= W4_MAX_SEQUENCES, heads a multiple of kv_heads,
- * T * heads < 2^26, 1 <= max_pages, max_pages * page_size <= W4_MAX_CONTEXT.
+ * Requires 1 <= T <= W4_MAX_TOKENS, 1 <= B <= W4_MAX_SEQUENCES, heads a multiple of kv_heads, at
+ * most 65536, T * heads < 2^26, 1 <= max_pages, max_pages * page_size <= W4_MAX_CONTEXT.
  */
 size_t w4_paged_attention_workspace_bytes(int64_t T, int64_t heads, const w4_kv_cache* cache,
                                           int64_t B, int64_t max_pages);

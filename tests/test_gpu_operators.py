@@ -127,6 +127,35 @@ def test_rmsnorm_extremes():
     assert int(st) == 1
 
 
+def test_rows_past_one_grid_dimension_and_far_offsets():
+    # 70000 short rows, and rows whose elements lie past 2^31
+    x = _rows(70000, 256, 3, BF)
+    w = torch.ones(256, dtype=BF, device=DEV)
+    pick = [0, 65534, 65535, 65536, 69999]
+    ref = oracle.rmsnorm_ref(to_np32(x[pick]), np.ones(256), 1e-5)
+    _close(to_np32(w4.w4_rmsnorm(x, w, 1e-5, out_dtype=F32)[pick]), ref, 4 * U32 * np.abs(ref), "norm")
+    y = w4.w4_rmsnorm(x, w, 1e-5, out_dtype=F32)
+    codes, scales = w4.w4_rmsnorm_int8(x, w, 1e-5)
+    _same_codes(codes[pick], scales[pick], to_np32(y[pick]), "int8", "norm")
+    ref = oracle.silu_mul_ref(to_np32(x[pick]))
+    got = w4.w4_silu_mul(x, out_dtype=F32)
+    _close(to_np32(got[pick]), ref, 8 * U32 * np.abs(ref) + 2.0 ** -126, "gate")
+    codes, scales = w4.w4_silu_mul_fp8(x)
+    _same_codes(codes[pick], scales[pick], to_np32(got[pick]), "fp8", "gate")
+    rows = 270000
+    big = torch.zeros(rows, 8192, dtype=BF, device=DEV)
+    big[-1] = _rows(1, 8192, 9, BF)[0]
+    assert big.numel() > 2 ** 31
+    y = w4.w4_rmsnorm(big, torch.ones(8192, dtype=BF, device=DEV), 1e-5)
+    ref = oracle.rmsnorm_ref(to_np32(big[-1:]), np.ones(8192), 1e-5)
+    _close(to_np32(y[-1:]), ref, (UB + 8 * U32) * np.abs(ref), "last row")
+    assert not bool(y[:-1].any())
+    del y
+    g = w4.w4_silu_mul(big)
+    ref = oracle.silu_mul_ref(to_np32(big[-1:]))
+    _close(to_np32(g[-1:]), ref, (UB + 16 * U32) * np.abs(ref) + 2.0 ** -126, "last gate row")
+
+
 @pytest.mark.parametrize("rows,f", NORM_SHAPES)
 @pytest.mark.parametrize("xt", [BF, F32])
 def test_silu_mul(rows, f, xt):
@@ -482,6 +511,11 @@ ATTEND = [  # new, cached, heads, kv, d, page, fp8, window
     ([200, 3], [100, 400], 4, 2, 128, 16, False, 33),
     ([300], [700], 2, 1, 64, 64, False, 500),
     ([64, 64], [0, 64], 5, 5, 128, 16, True, 1),
+    ([6, 0, 0, 0, 0, 0, 3, 0, 0], [100, 5, 6, 7, 8, 9, 50, 1, 2], 8, 1, 128, 16, False, 0),  # as many tokens as requests, not one each
+    ([1] * 65, [(7 * i) % 90 for i in range(65)], 4, 2, 64, 16, False, 0),                    # more requests than lanes
+    ([i % 3 for i in range(200)], [(11 * i) % 60 for i in range(200)], 4, 1, 64, 16, True, 0),
+    ([40 * (i % 50 == 49) + (i % 2) for i in range(150)], [(5 * i) % 40 for i in range(150)], 8, 2, 64, 16, False, 0),
+    ([1, 5], [5000, 4200], 4, 2, 64, 4096, False, 0),
 ]
 
 
@@ -630,6 +664,26 @@ def test_attention_graph_and_streams(new, cached):
                 w4.w4_paged_attention(b.d_q, b.cache, b.d_table, b.d_cu, b.d_lens, b.scale, **{k: v for k, v in buf.items()})
     torch.cuda.synchronize()
     assert torch.equal(bufs[0]["o"], ref) and torch.equal(bufs[1]["o"], ref)
+
+
+def test_attention_of_most_requests():
+    # 4096 requests, a few of them with tokens or keys: scores 0, so each row is the mean of its values
+    B, d = 4096, 64
+    rng = np.random.default_rng(2)
+    new = (rng.random(B) < 0.2).astype(np.int32)
+    new[-1], new[0], new[63], new[64], new[4032] = 2, 1, 0, 1, 3
+    ctx = np.where(new > 0, new + rng.integers(0, 14, B), 0).astype(np.int32)
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    T = int(cu[-1])
+    v = torch.arange(B * 16, device=DEV, dtype=F32).remainder(97).view(B, 1, 16, 1).expand(B, 1, 16, d).contiguous().to(BF)
+    cache = w4.W4KVCache(torch.zeros_like(v), v)
+    table = torch.arange(B, dtype=torch.int32, device=DEV)[:, None].contiguous()
+    o = w4.w4_paged_attention(torch.zeros(T, 2, d, dtype=BF, device=DEV), cache, table, _dev(cu), _dev(ctx), 1.0)
+    got, vals = to_np32(o), to_np32(v)[:, 0, :, 0].astype(np.float64)
+    for b in np.nonzero(new)[0]:
+        for t in range(new[b]):
+            ref = vals[b, : ctx[b] - new[b] + t + 1].mean()
+            assert np.all(np.abs(got[cu[b] + t] - ref) <= (UB + 2.0 ** -14) * ref), (b, t)
 
 
 def test_attention_far_offsets():

@@ -90,6 +90,7 @@ def test_rope_cache_refusals():
     assert call(xt=2) == 4
     assert call(T=0) == 2 and call(T=(1 << 22) + 1) == 2 and call(heads=3) == 2 and call(heads=0) == 2
     assert call(T=1 << 22, heads=16) == 2                     # T * heads past its limit
+    assert call(T=1, heads=65538) == 2
     for kw, status in BAD_CACHES:
         assert call(c=cache(**kw)) == status, kw
     assert call(r=rope(24)) == 5 and call(r=rope(0)) == 5 and call(r=rope(144)) == 5
