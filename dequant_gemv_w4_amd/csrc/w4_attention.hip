@@ -986,24 +986,37 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void attend_narrow_kernel(Attend
 }
 
 // Joins the parts of the rows that were split: one wave a row, the tiles numbered as in the
-// launch that wrote them.
+// launch that wrote them.  What the parts left is loaded before it is known how many there are (the
+// launch allows a.*_parts, at most 64), so that the sequence and the parts cost one wait.
 template <int D, bool WIDE>
 __device__ __forceinline__ void combine_rows(const AttendArgs& a, uint32_t set) {
     constexpr int E = D / 64, kSets = (WIDE ? kWideRows : kNarrowRows) / 4;
     const int lane = threadIdx.x & 63;
+    const int r = (int)(set % kSets) * 4 + (threadIdx.x >> 6);
+    const int most = WIDE ? a.wide_parts : a.narrow_parts;
+    const int64_t rows = WIDE ? a.wide_rows : a.narrow_rows;
+    const int64_t row = (int64_t)(set / kSets) * (WIDE ? kWideRows : kNarrowRows) + r;
+    const float* ml = (WIDE ? a.wide_ml : a.narrow_ml) + 2 * row;
+    const float* po = (WIDE ? a.wide_o : a.narrow_o) + row * D + lane * E;
+    const int mine = min(lane, most - 1);
+    float mp = ml[2 * mine * rows], lp = ml[2 * mine * rows + 1];
+    float x[4][E];
+    auto load = [&](int p0) {                                // of four parts at once
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[j][e] = po[min(p0 + j, most - 1) * rows * D + e];
+    };
+    load(0);
     int kv;
     const Tile t = find_tile<WIDE>(a, set / kSets, 0, kv);
-    const int r = (int)(set % kSets) * 4 + (threadIdx.x >> 6);
     if (!t.run || t.span.parts == 1 || t.row0 + r >= t.rows) return;
     const Place place = row_place(a, t, kv, t.row0 + r);
-    const Parts<WIDE> w(a);
-    // lane p weighs part p (kMaxParts is 64): 2^(m_p - m) l_p, 0 where the part has nothing of weight
+    // lane p weighs part p: 2^(m_p - m) l_p, 0 where the part has nothing of weight
     const int parts = t.span.parts;
-    float mp = kNegInf, lp = 0.0f;
-    if (lane < parts) {
-        const int64_t at = w.at(t, lane, r);
-        mp = w.ml[2 * at];
-        lp = w.ml[2 * at + 1];
+    if (lane >= parts) {
+        mp = kNegInf;
+        lp = 0.0f;
     }
     float m = mp;
 #pragma unroll
@@ -1015,12 +1028,8 @@ __device__ __forceinline__ void combine_rows(const AttendArgs& a, uint32_t set) 
     float o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.0f;
-    for (int p0 = 0; p0 < parts; p0 += 4) {                  // the loads of four parts at once
-        float x[4][E];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int e = 0; e < E; ++e) x[j][e] = w.o[w.at(t, min(p0 + j, parts - 1), r) * D + lane * E + e];
+    for (int p0 = 0; p0 < parts; p0 += 4) {
+        if (p0 > 0) load(p0);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float fp = p0 + j < parts ? __shfl(f, p0 + j) : 0.0f;

@@ -48,10 +48,15 @@ def _status_ptr(status, device):
     return status.data_ptr()
 
 
+_FUNCTIONS = {}
+
+
 def _call(name, device, *args):
     """Run an entry point on ``device`` and its current stream."""
     index = device.index
-    fn = getattr(lib(), name)
+    fn = _FUNCTIONS.get(name)
+    if fn is None:
+        fn = _FUNCTIONS[name] = getattr(lib(), name)
     if index == torch._C._cuda_getDevice():
         status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
