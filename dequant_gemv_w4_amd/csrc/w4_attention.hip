@@ -3,13 +3,14 @@
 // over the keys that a query sees, in one pass with the running maximum and sum of the softmax.
 // The index arithmetic (tiles, parts, pages) is in w4_paging.h.
 //
-// Both kernels multiply on v_mfma_f32_32x32x16_bf16 with the keys as rows and the query rows as
-// columns: S^T = K Q^T leaves each lane one query row (lane % 32) and half of the keys, so the
-// running maximum is one exchange between lane halves, and the same registers, rounded to
-// bfloat16, are the right operand of O^T += V^T P^T without any movement: which key stands at
-// which place of that product's inner dimension is free, and the left operand follows (half h of
-// the lanes holds the keys 4h..4h+3 and 8+4h..8+4h+3 of each 16).  V stays in its row order and
-// is turned by ds_read_b64_tr_b16, which gives a lane four keys of one column.
+// Both kernels multiply on the matrix cores with the keys as rows and the query rows as columns
+// (32x32x16 in attend_wide, 16x16x32 in attend_narrow): S^T = K Q^T leaves each lane one query row and
+// a half or a quarter of the keys, so the running maximum is one or two exchanges between lanes, and
+// the same registers, rounded to bfloat16, are the right operand of O^T += V^T P^T without any
+// movement: which key stands at which place of that product's inner dimension is free, and the left
+// operand follows (half h of the lanes holds the keys 4h..4h+3 and 8+4h..8+4h+3 of each 16, quarter h
+// the keys 4h..4h+3 and 16+4h..16+4h+3 of 32).  V stays in its row order and is turned by
+// ds_read_b64_tr_b16, which gives a lane four keys of one column.
 //
 // Rounding: scores, maximum, sum and O are binary32; the sum takes the unrounded P.  For the matrix unit
 // attend_wide rounds P to bfloat16 (each weight within 2^-8 relative; the same size as the rounding of
@@ -22,8 +23,10 @@
 // attend_wide: 256 rows a workgroup, 8 waves of 32 rows; tiles of 64 keys pass through LDS for
 // all of them, the next tile's loads in flight, and the two waves of a SIMD take turns on the
 // matrix unit.
-// attend_narrow: up to 32 rows, for single tokens: the waves take 32-key tiles in turn, each with
-// its own piece of LDS, and join their sums at the end.
+// attend_narrow: 16 rows, for single tokens: the waves take 32-key tiles in turn, each with its own
+// piece of LDS, and join their sums at the end.  (Tiles of 32 rows, twice the registers and matrix
+// work: 157.0 us instead of 152.9 for single tokens of 32 requests over up to 8192 cached, 86.2
+// instead of 80.6 over 100,000 in E4M3, 13.8 instead of 12.8 for one request over 1000.)
 // Either may split the keys of a tile over several workgroups, which then leave (m, l, O / l) in
 // the workspace for combine_kernel.
 //
@@ -87,7 +90,7 @@ __device__ __forceinline__ int k_place(int r, int c) {
 }
 template <int D>
 __device__ __forceinline__ int v_place(int r, int c) {
-    return r * (2 * D) + 16 * (D == 128 ? c ^ ((r & 3) << 2) : c ^ (((r >> 1) & 1) << 2));
+    return r * (2 * D) + 16 * (c ^ (D == 128 ? (r & 3) << 2 : ((r >> 1) & 1) << 2) ^ (((r >> 2) & 1) << 1));
 }
 
 __device__ __forceinline__ uint64_t read_tr(const uint8_t* p) {
@@ -133,18 +136,17 @@ __device__ __forceinline__ void clear_rows(Rows<D>& s) {
     s.l = 0.0f;
 }
 
-// A step takes NB blocks of 32 keys in three parts.  The products read their left operands from LDS,
-// which answers after about 130 cycles; a product takes 32.  With AHEAD the operands of four products
-// are read while the four before them are in the matrix unit, and held to that order: left alone the
-// compiler reads two to eight ahead, by what registers seem free (a chunk of 2048 + 1889 tokens: 737 us
-// when it read eight ahead, 790 with two).
+// A step of attend_wide takes 64 keys in three parts.  The products read their left operands from LDS,
+// which answers after about 130 cycles; a product takes 32.  The operands of four products are read
+// while the four before them are in the matrix unit, and held to that order: left alone the compiler
+// reads two to eight ahead, by what registers seem free (a chunk of 2048 + 1889 tokens: 737 us when it
+// read eight ahead, 790 with two).
 __device__ __forceinline__ void hold_order() { __builtin_amdgcn_sched_barrier(0); }
 
 // scores: z = K q for the staged keys kt.
-template <int D, int NB, bool AHEAD>
-__device__ __forceinline__ void scores(const Rows<D>& s, const uint8_t* kt, f32x16_t (&z)[NB]) {
-    constexpr int kSteps = 4 / NB;                           // of the inner dimension in a group
-    constexpr int kGroups = D / 16 / kSteps;
+template <int D>
+__device__ __forceinline__ void scores(const Rows<D>& s, const uint8_t* kt, f32x16_t (&z)[2]) {
+    constexpr int kGroups = D / 32;
     const int lane = threadIdx.x & 63, half = lane >> 5, l32 = lane & 31;
     auto operand = [&](int d, int b) {
         return *reinterpret_cast<const u32x4_t*>(kt + k_place<D>(32 * b + l32, 2 * d + half));
@@ -154,29 +156,22 @@ __device__ __forceinline__ void scores(const Rows<D>& s, const uint8_t* kt, f32x
                                                        __builtin_bit_cast(bf16x8_t, s.q[d]), z[b], 0, 0, 0);
     };
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+    for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int r = 0; r < 16; ++r) z[b][r] = 0.0f;
-    if constexpr (AHEAD) {
-        u32x4_t a[2][4];
+    u32x4_t a[2][4];
 #pragma unroll
-        for (int g = 0; g <= kGroups; ++g) {
-            if (g < kGroups) {
+    for (int g = 0; g <= kGroups; ++g) {
+        if (g < kGroups) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) a[g & 1][j] = operand(g * kSteps + j / NB, j % NB);
-            }
-            hold_order();
-            if (g > 0) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) multiply(a[(g - 1) & 1][j], (g - 1) * kSteps + j / NB, j % NB);
-            }
-            hold_order();
+            for (int j = 0; j < 4; ++j) a[g & 1][j] = operand(2 * g + j / 2, j % 2);
         }
-    } else {
+        hold_order();
+        if (g > 0) {
 #pragma unroll
-        for (int d = 0; d < D / 16; ++d)
-#pragma unroll
-            for (int b = 0; b < NB; ++b) multiply(operand(d, b), d, b);
+            for (int j = 0; j < 4; ++j) multiply(a[(g - 1) & 1][j], 2 * (g - 1) + j / 2, j % 2);
+        }
+        hold_order();
     }
 }
 
@@ -193,18 +188,24 @@ __device__ __forceinline__ float half_max(float x) {
     const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
     return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
+// Over the four lanes that are multiples of 16 apart.
+__device__ __forceinline__ float quarter_max(float x) {
+    const uint32_t u = __float_as_uint(x);
+    const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    return half_max(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+}
 
 // weights: the running maximum and sum, and the bfloat16 weights p (as the right operand of 16 keys
-// each: p[4 c .. 4 c + 3]), with REST followed by what their rounding leaves.  ks, vs: LDS addresses of the scales of the keys' and values' rows, from row 4 half on (FP8); first: position of
-// the first key; the row sees the `count` keys from lo; mask: whether the step reaches outside some
-// row's.
-template <int D, bool FP8, int NB, bool REST>
-__device__ __forceinline__ void weights(Rows<D>& s, f32x16_t (&z)[NB], uint32_t (&p)[8 * NB * (REST ? 2 : 1)], uint32_t ks,
-                                        uint32_t vs, float scale, int first, int lo, int count, bool mask) {
+// each: p[4 c .. 4 c + 3]).  ks, vs: LDS addresses of the scales of the keys' and values' rows, from
+// row 4 half on (FP8); first: position of the first key; the row sees the `count` keys from lo; mask:
+// whether the step reaches outside some row's.
+template <int D, bool FP8>
+__device__ __forceinline__ void weights(Rows<D>& s, f32x16_t (&z)[2], uint32_t (&p)[16], uint32_t ks, uint32_t vs,
+                                        float scale, int first, int lo, int count, bool mask) {
     const int half = (threadIdx.x & 63) >> 5;
     if constexpr (FP8) {
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const f32x4_t f = read_lds_f32x4(ks + 4 * (32 * b + 8 * i));
@@ -215,14 +216,14 @@ __device__ __forceinline__ void weights(Rows<D>& s, f32x16_t (&z)[NB], uint32_t 
     if (mask) {
         const uint32_t from = (uint32_t)(first + 4 * half - lo);
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r)
                 if (from + (32 * b + 8 * (r >> 2) + (r & 3)) >= (uint32_t)count) z[b][r] = kNegInf;
     }
     float mx = z[0][0];
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+    for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int r = 0; r < 16; ++r) mx = fmaxf(mx, z[b][r]);
     mx = half_max(mx) * scale;                               // scale > 0
@@ -239,7 +240,7 @@ __device__ __forceinline__ void weights(Rows<D>& s, f32x16_t (&z)[NB], uint32_t 
     const float sub = s.m == kNegInf ? 0.0f : s.m;           // nothing seen yet: every weight is 0
     float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
+    for (int b = 0; b < 2; ++b) {
         f32x4_t f = {1.0f, 1.0f, 1.0f, 1.0f};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -254,19 +255,16 @@ __device__ __forceinline__ void weights(Rows<D>& s, f32x16_t (&z)[NB], uint32_t 
                 w1 *= f[2 * (i & 1) + 1];
             }
             p[8 * b + i] = bf16_pair(w0, w1);
-            if constexpr (REST)                              // what the rounding left, itself within 2^-8
-                p[8 * NB + 8 * b + i] = bf16_pair(w0 - __uint_as_float(p[8 * b + i] << 16),
-                                                  w1 - __uint_as_float(p[8 * b + i] & 0xFFFF0000u));
         }
     }
     s.l += sum[0] + sum[1];
 }
 
 // accumulate: O += V p for the staged values vt.
-template <int D, int NB, bool AHEAD, bool REST>
-__device__ __forceinline__ void accumulate(Rows<D>& s, const uint8_t* vt, const uint32_t (&p)[8 * NB * (REST ? 2 : 1)]) {
+template <int D>
+__device__ __forceinline__ void accumulate(Rows<D>& s, const uint8_t* vt, const uint32_t (&p)[16]) {
     constexpr int kBlocks = D / 32, kSteps = 4 / kBlocks;    // blocks of columns; steps of 16 keys in a group
-    constexpr int kGroups = 2 * NB / kSteps;
+    constexpr int kGroups = 4 / kSteps;
     const int lane = threadIdx.x & 63, half = lane >> 5, i16 = lane & 15, g16 = (lane >> 4) & 1;
     auto operand = [&](int c, int i) {                       // 16 keys, 32 columns
         const int r0 = 16 * c + 4 * half + (i16 >> 2);
@@ -279,32 +277,110 @@ __device__ __forceinline__ void accumulate(Rows<D>& s, const uint8_t* vt, const 
         const u32x4_t pb = {p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]};
         s.o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
                                                          __builtin_bit_cast(bf16x8_t, pb), s.o[i], 0, 0, 0);
-        if constexpr (REST) {
-            const u32x4_t pr = {p[8 * NB + 4 * c], p[8 * NB + 4 * c + 1], p[8 * NB + 4 * c + 2], p[8 * NB + 4 * c + 3]};
-            s.o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
-                                                             __builtin_bit_cast(bf16x8_t, pr), s.o[i], 0, 0, 0);
-        }
     };
-    if constexpr (AHEAD) {
-        u32x4_t a[2][4];
+    u32x4_t a[2][4];
 #pragma unroll
-        for (int g = 0; g <= kGroups; ++g) {
-            if (g < kGroups) {
+    for (int g = 0; g <= kGroups; ++g) {
+        if (g < kGroups) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) a[g & 1][j] = operand(g * kSteps + j / kBlocks, j % kBlocks);
-            }
-            hold_order();
-            if (g > 0) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) multiply(a[(g - 1) & 1][j], (g - 1) * kSteps + j / kBlocks, j % kBlocks);
-            }
-            hold_order();
+            for (int j = 0; j < 4; ++j) a[g & 1][j] = operand(g * kSteps + j / kBlocks, j % kBlocks);
         }
-    } else {
+        hold_order();
+        if (g > 0) {
 #pragma unroll
-        for (int c = 0; c < 2 * NB; ++c)
+            for (int j = 0; j < 4; ++j) multiply(a[(g - 1) & 1][j], (g - 1) * kSteps + j / kBlocks, j % kBlocks);
+        }
+        hold_order();
+    }
+}
+
+// The running state of attend_narrow's 16 query rows: lane % 16 is the row, lane / 16 picks a quarter
+// of the keys in the scores and of the columns in O (register r of block i: column 16 i +
+// 4 (lane / 16) + r).  l is the lane's own part of the sum.
+template <int D>
+struct Few {
+    u32x4_t q[D / 32];
+    f32x4_t o[D / 16];
+    float m, l;
+};
+
+// A step of attend_narrow: the 32 staged keys from position `first` on; lane as the addresses in LDS
+// take it, sc: LDS address of the keys' row scales from row 4 (lane / 16) on, the values' 32 floats on.
+template <int D, bool FP8>
+__device__ __forceinline__ void step_narrow(Few<D>& s, const uint8_t* kt, const uint8_t* vt, uint32_t sc, int lane,
+                                            float scale, int first, int lo, int count, bool mask) {
+    const int i16 = lane & 15, quarter = lane >> 4;
+    f32x4_t z[2];
 #pragma unroll
-            for (int i = 0; i < kBlocks; ++i) multiply(operand(c, i), c, i);
+    for (int b = 0; b < 2; ++b) z[b] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const u32x4_t k = *reinterpret_cast<const u32x4_t*>(kt + k_place<D>(16 * b + i16, 4 * d + quarter));
+            z[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, k),
+                                                           __builtin_bit_cast(bf16x8_t, s.q[d]), z[b], 0, 0, 0);
+        }
+    if constexpr (FP8) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const f32x4_t f = read_lds_f32x4(sc + 64 * b);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) z[b][r] *= f[r];
+        }
+    }
+    if (mask) {
+        const uint32_t from = (uint32_t)(first + 4 * quarter - lo);
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (from + (16 * b + r) >= (uint32_t)count) z[b][r] = kNegInf;
+    }
+    float mx = z[0][0];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) mx = fmaxf(mx, z[b][r]);
+    mx = quarter_max(mx) * scale;                            // scale > 0
+    if (__any(mx > s.m + kSlack)) {
+        const float m = fmaxf(s.m, mx);
+        const float f = m == s.m ? 1.0f : exp2_fast(s.m - m);
+        s.m = m;
+        s.l *= f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s.o[i][r] *= f;
+    }
+    const float sub = s.m == kNegInf ? 0.0f : s.m;           // nothing seen yet: every weight is 0
+    u32x4_t p, rest;                                         // and what the rounding left, itself within 2^-8
+    float sum = 0.0f;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        f32x4_t f = {1.0f, 1.0f, 1.0f, 1.0f};
+        if constexpr (FP8) f = read_lds_f32x4(sc + 128 + 64 * b);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float e0 = exp2_fast(fmaf(z[b][2 * i], scale, -sub));
+            const float e1 = exp2_fast(fmaf(z[b][2 * i + 1], scale, -sub));
+            sum += e0 + e1;
+            const float w0 = FP8 ? e0 * f[2 * i] : e0, w1 = FP8 ? e1 * f[2 * i + 1] : e1;
+            const uint32_t w = bf16_pair(w0, w1);
+            p[2 * b + i] = w;
+            rest[2 * b + i] = bf16_pair(w0 - __uint_as_float(w << 16), w1 - __uint_as_float(w & 0xFFFF0000u));
+        }
+    }
+    s.l += sum;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {                       // 16 columns, the 32 keys in the order of p
+        const int chunk = 2 * i + ((i16 & 3) >> 1), off = 8 * (i16 & 1), r0 = 4 * quarter + (i16 >> 2);
+        const uint64_t a0 = read_tr(vt + v_place<D>(r0, chunk) + off);
+        const uint64_t a1 = read_tr(vt + v_place<D>(r0 + 16, chunk) + off);
+        const bf16x8_t v = __builtin_bit_cast(
+            bf16x8_t, u32x4_t{(uint32_t)a0, (uint32_t)(a0 >> 32), (uint32_t)a1, (uint32_t)(a1 >> 32)});
+        s.o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, __builtin_bit_cast(bf16x8_t, p), s.o[i], 0, 0, 0);
+        s.o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, __builtin_bit_cast(bf16x8_t, rest), s.o[i], 0, 0, 0);
     }
 }
 
@@ -410,8 +486,8 @@ struct Tile {
 };
 
 // Tile number `index` of attend_wide's or attend_narrow's launch.  Where both are launched, a
-// sequence of at most kNarrowRows rows is the narrow kernel's, as its only tile, and the narrow
-// launch has one tile a sequence.
+// sequence of at most kFewRows rows is the narrow kernel's, and that launch has kFewRows /
+// kNarrowRows tiles a sequence; alone it has as many tiles a token as G rows fill.
 template <bool WIDE>
 __device__ __forceinline__ Tile find_tile(const AttendArgs& a, uint32_t index, int part, int& kv) {
     constexpr int R = WIDE ? kWideRows : kNarrowRows;
@@ -421,16 +497,18 @@ __device__ __forceinline__ Tile find_tile(const AttendArgs& a, uint32_t index, i
     kv = (int)index - tile * a.kv_heads;
     t.part_row = (int64_t)index * R;
     if (!WIDE && a.both) {
-        t.b = tile;
-        t.row0 = 0;
+        t.b = tile / (kFewRows / kNarrowRows);
+        t.row0 = tile % (kFewRows / kNarrowRows) * kNarrowRows;
         t.seq = load_seq(a, t.b);
     } else {
+        const int64_t per = ceil_div(G, R);                  // tiles a token
+        auto first = [&](int64_t cu_b, int64_t b) { return WIDE ? first_tile(cu_b, b, G, R) : cu_b * per; };
         int64_t cu;
-        t.seq = find_seq(a, [&](int64_t cu_b, int64_t b) { return first_tile(cu_b, b, G, R); }, tile, t.b, cu);
-        t.row0 = (tile - first_tile(cu, t.b, G, R)) * R;
+        t.seq = find_seq(a, first, tile, t.b, cu);
+        t.row0 = (tile - first(cu, t.b)) * R;
     }
     t.rows = t.seq.n * G;
-    const bool few = t.rows <= kNarrowRows;
+    const bool few = t.rows <= kFewRows;
     t.run = t.row0 >= 0 && t.row0 < t.rows && (WIDE ? !few : few || !a.both);
     if (!t.run) return t;
     t.span = key_span(t.seq, t.row0, imin(R, t.rows - t.row0), G, a.window,
@@ -458,18 +536,18 @@ __device__ __forceinline__ Place row_place(const AttendArgs& a, const Tile& t, i
     return p;
 }
 
-template <int D>
-__device__ __forceinline__ void load_q(const AttendArgs& a, const Place& p, Rows<D>& s) {
-    const int half = (threadIdx.x & 63) >> 5;
+// Rows past the last stand for the first: what comes of them is not stored.
+template <int N>
+__device__ __forceinline__ void load_q(const uint16_t* q, u32x4_t (&out)[N], int step) {
 #pragma unroll
-    for (int d = 0; d < D / 16; ++d) {
-        s.q[d] = u32x4_t{0u, 0u, 0u, 0u};
-        if (p.real) s.q[d] = *reinterpret_cast<const u32x4_t*>(a.q + p.row * D + 16 * d + 8 * half);
-    }
-    // The wait for these loads belongs here: left to the first product, inside the loop, it would be
-    // a wait for the tile loads in flight at every step.
+    for (int d = 0; d < N; ++d) out[d] = *reinterpret_cast<const u32x4_t*>(q + d * step);
+}
+// The wait for these loads: left to the first product, inside the loop, it would be a wait for the tile
+// loads in flight at every step.
+template <int N>
+__device__ __forceinline__ void wait_q(u32x4_t (&q)[N]) {
 #pragma unroll
-    for (int d = 0; d < D / 16; ++d) asm volatile("" : "+v"(s.q[d]));
+    for (int d = 0; d < N; ++d) asm volatile("" : "+v"(q[d]));
 }
 
 // Stores 4 neighbouring columns of a row that are already divided by its sum.
@@ -605,7 +683,8 @@ __global__ __launch_bounds__(kWideThreads, 2) void attend_wide_kernel(AttendArgs
     if (!t.run) return;
     Place p = row_place(a, t, kv, t.row0 + 32 * wave + (lane & 31));
     Rows<D> s;
-    load_q<D>(a, p, s);
+    load_q(a.q + p.row * D + 8 * (lane >> 5), s.q, 16);
+    wait_q(s.q);
     clear_rows<D>(s);
     // keys that any row of this wave sees, and those that all of them see
     int any_lo = p.real ? p.lo : W4_MAX_CONTEXT, any_hi = p.hi, all_lo = p.lo, all_hi = p.real ? p.hi : W4_MAX_CONTEXT;
@@ -741,7 +820,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void attend_wide_kernel(AttendArgs
         if (!FP8 && tiles < 2) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
     meet();
-    if (seen(0)) scores<D, 2, true>(s, kt[0], z);
+    if (seen(0)) scores<D>(s, kt[0], z);
     if (behind) meet();
     // One step, tile i in place S = i % kWideStages.
     auto step = [&](auto place, int i) {
@@ -749,7 +828,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void attend_wide_kernel(AttendArgs
         const int n = i + behind;
         look_up(n + kAhead + 1);
         if (seen(i))
-            weights<D, FP8, 2, false>(s, z, pw, sc_lane + 4 * S * kKeyTile, sc_lane + 4 * (kWideStages + S) * kKeyTile, a.scale_log2, k0 + i * kKeyTile, p.lo,
+            weights<D, FP8>(s, z, pw, sc_lane + 4 * S * kKeyTile, sc_lane + 4 * (kWideStages + S) * kKeyTile, a.scale_log2, k0 + i * kKeyTile, p.lo,
                                p.count, i < whole_lo || i > whole_hi);
         if (n >= 1 && n < tiles) {
             if constexpr (FP8) {
@@ -769,10 +848,10 @@ __global__ __launch_bounds__(kWideThreads, 2) void attend_wide_kernel(AttendArgs
         meet();
         __builtin_amdgcn_s_setprio(1);
         if (seen(i)) {
-            accumulate<D, 2, true, false>(s, vt[S], pw);
+            accumulate<D>(s, vt[S], pw);
         }
         if (seen(i + 1)) {
-            scores<D, 2, true>(s, kt[(S + 1) % kWideStages], z);
+            scores<D>(s, kt[(S + 1) % kWideStages], z);
         }
         __builtin_amdgcn_s_setprio(0);
         meet();
@@ -834,20 +913,20 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void attend_narrow_kernel(Attend
     // a wave's tiles; at the end its O (32 rows of D binary32) takes the same place
     __shared__ __attribute__((aligned(16))) uint8_t tiles_lds[kNarrowWaves][2 * kTileBytes];
     __shared__ __attribute__((aligned(16))) float scales[kNarrowWaves][2 * kKeys];
-    __shared__ float sm[kNarrowWaves][32], sl[kNarrowWaves][32];
-    static_assert(2 * kTileBytes == 32 * D * 4, "O fits the tiles' place");
+    __shared__ float sm[kNarrowWaves][kNarrowRows], sl[kNarrowWaves][kNarrowRows];
+    static_assert(2 * kTileBytes >= kNarrowRows * D * 4, "O fits the tiles' place");
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int part = blockIdx.y;
     int kv;
     const Tile t = find_tile<false>(a, blockIdx.x, part, kv);
     if (!t.run) return;
-    const Place p = row_place(a, t, kv, t.row0 + (lane & 31));
-    Rows<D> s;
-    load_q<D>(a, p, s);
-    clear_rows<D>(s);
+    const int i16 = lane & 15, quarter = lane >> 4;
+    const Place p = row_place(a, t, kv, t.row0 + i16);
+    Few<D> s;
+    load_q(a.q + p.row * D + 8 * quarter, s.q, 32);
     int all_lo = p.lo, all_hi = p.real ? p.hi : W4_MAX_CONTEXT;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
+    for (int off = 8; off > 0; off >>= 1) {
         all_lo = max(all_lo, __shfl_xor(all_lo, off));
         all_hi = min(all_hi, __shfl_xor(all_hi, off));
     }
@@ -885,13 +964,18 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void attend_narrow_kernel(Attend
             sc = (lane < 32 ? rows.ks : rows.vs)[at];
         }
     };
-    const uint32_t sc_lane = lds_address(scales[wave]) + 16 * (lane >> 5);
+    const uint32_t sc_lane = lds_address(scales[wave]) + 16 * quarter;
     const int tiles = (k1 - k0 + kKeys - 1) / kKeys;
     if (wave < tiles) {
         look_up(wave, entry);
         fetch(wave);
         look_up(wave + kNarrowWaves, entry);
     }
+    wait_q(s.q);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) s.o[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    s.m = kNegInf;
+    s.l = 0.0f;
     for (int i = wave; i < tiles; i += kNarrowWaves) {
         const int first = k0 + i * kKeys;
         int later[2];
@@ -909,32 +993,23 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void attend_narrow_kernel(Attend
             entry[1] = later[1];
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // rows staged by other lanes
-        f32x16_t z[1];
-        uint32_t pw[16];
-        scores<D, 1, false>(s, kt, z);
-        weights<D, FP8, 1, true>(s, z, pw, sc_lane, sc_lane + 4 * kKeys, a.scale_log2, first, p.lo, p.count,
-                           first < all_lo || first + kKeys - 1 > all_hi);
-        accumulate<D, 1, false, true>(s, vt, pw);
+        step_narrow<D, FP8>(s, kt, vt, sc_lane, lane, a.scale_log2, first, p.lo, p.count,
+                            first < all_lo || first + kKeys - 1 > all_hi);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // read before the next rows land
     }
 
     // Join the waves: O of wave w counts 2^(m_w - m).
-    const int half = lane >> 5;
-    const float l = s.l + __shfl_xor(s.l, 32);
-    if (lane < 32) {
+    float l = s.l + __shfl_xor(s.l, 16);
+    l += __shfl_xor(l, 32);
+    if (lane < 16) {
         sm[wave][lane] = s.m;
         sl[wave][lane] = l;
     }
     float* own = reinterpret_cast<float*>(tiles_lds[wave]);
-    // row r's groups of 4 columns are rotated by r, so that 8 rows do not share banks
+    // row r's groups of 4 columns are rotated by r, so that the rows do not share banks
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const f32x4_t v = {s.o[i][4 * g], s.o[i][4 * g + 1], s.o[i][4 * g + 2], s.o[i][4 * g + 3]};
-            const int group = (8 * i + 2 * g + half + (lane & 31)) & (D / 4 - 1);
-            *reinterpret_cast<f32x4_t*>(own + (lane & 31) * D + 4 * group) = v;
-        }
+    for (int i = 0; i < D / 16; ++i)
+        *reinterpret_cast<f32x4_t*>(own + i16 * D + 4 * ((4 * i + quarter + i16) & (D / 4 - 1))) = s.o[i];
     __syncthreads();
     constexpr int kGroups = D / 4;                           // a thread joins 4 columns of a row
     uint32_t bad_rows = 0;
@@ -1067,8 +1142,8 @@ int parts_for(int64_t tiles, int64_t target, int64_t longest, int64_t least) {
 void plan_attend(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int64_t capacity, AttendPlan* p) {
     const int64_t G = heads / kv_heads;
     // One token a sequence, or too few rows for the wide kernel: no sequence needs it.
-    p->both = T != B && T * G > kNarrowRows;
-    p->narrow_tiles = (p->both ? B : tile_bound(T, B, G, kNarrowRows)) * kv_heads;
+    p->both = T != B && T * G > kFewRows;
+    p->narrow_tiles = (p->both ? B * (kFewRows / kNarrowRows) : T * ceil_div(G, kNarrowRows)) * kv_heads;
     p->narrow_parts = parts_for(p->narrow_tiles, 256, capacity, kNarrowLeast);
     p->wide_tiles = p->both ? tile_bound(T, B, G, kWideRows) * kv_heads : 0;
     p->wide_parts = p->both ? parts_for(p->wide_tiles, 512, capacity, kWideLeast) : 1;

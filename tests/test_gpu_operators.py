@@ -516,6 +516,10 @@ ATTEND = [  # new, cached, heads, kv, d, page, fp8, window
     ([i % 3 for i in range(200)], [(11 * i) % 60 for i in range(200)], 4, 1, 64, 16, True, 0),
     ([40 * (i % 50 == 49) + (i % 2) for i in range(150)], [(5 * i) % 40 for i in range(150)], 8, 2, 64, 16, False, 0),
     ([1, 5], [5000, 4200], 4, 2, 64, 4096, False, 0),
+    ([1] * 3, [40, 3000, 1200], 24, 1, 128, 16, False, 0),    # more heads of a kv head than a tile has rows
+    ([1] * 2, [700, 9000], 40, 1, 64, 32, True, 100),
+    ([1, 3, 40], [6000, 5000, 9], 16, 2, 128, 16, False, 0),  # 8, 24 and 320 rows, the few split over the keys
+    ([2, 1, 50], [4000, 3, 9], 17, 1, 64, 16, True, 0),       # 34, 17 and 850 rows
 ]
 
 
