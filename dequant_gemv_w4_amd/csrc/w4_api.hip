@@ -746,7 +746,8 @@ w4_status w4_paged_attention(const void* q, int64_t T, int64_t heads, const w4_k
     a.cu = cu_q;
     a.lens = lens;
     a.status = d_status;
-    a.T = T;
+    a.T = (int)T;
+    a.capacity = (int)(max_pages << shift);
     a.pages = cache->pages;
     a.max_pages = max_pages;
     a.B = (int)B;

@@ -387,25 +387,24 @@ __device__ __forceinline__ void step_narrow(Few<D>& s, const uint8_t* kt, const 
 // The last sequence b with key(cu[b], b) <= x, by all lanes of a wave: 64 sequences at a time, so two
 // rounds of loads for up to 4096 sequences.  The sequence's own numbers are loaded in the same round.
 template <typename Key>
-__device__ __forceinline__ Seq find_seq(const AttendArgs& a, Key key, int64_t x, int& found, int64_t& cu_found) {
+__device__ __forceinline__ Seq find_seq(const AttendArgs& a, Key key, int x, int& found) {
     const int lane = threadIdx.x & 63;
+    auto below = [&](int cu, int b) { return b < a.B && key(min(max(cu, 0), a.T), b) <= x; };
     int base = 0;
     if (a.B > 64) {
         const int b = lane * 64;
-        const bool below = b < a.B && key(a.cu[b], b) <= x;
-        base = __builtin_amdgcn_readfirstlane(max(__popcll(__ballot(below)) - 1, 0) * 64);
+        base = __builtin_amdgcn_readfirstlane(max(__popcll(__ballot(below(a.cu[min(b, a.B - 1)], b))) - 1, 0) * 64);
     }
     const int b = min(base + lane, a.B - 1);
     const int cu0 = a.cu[b], cu1 = a.cu[b + 1], len = a.lens[b];
-    const int at = __builtin_amdgcn_readfirstlane(max(__popcll(__ballot(base + lane < a.B && key(cu0, b) <= x)) - 1, 0));
+    const int at = __builtin_amdgcn_readfirstlane(max(__popcll(__ballot(below(cu0, base + lane))) - 1, 0));
     found = base + at;
-    const int f0 = __builtin_amdgcn_readlane(cu0, at), f1 = __builtin_amdgcn_readlane(cu1, at);
-    cu_found = f0;
-    return clamp_seq(f0, f1, __builtin_amdgcn_readlane(len, at), a.T, a.max_pages << a.page_shift);
+    return clamp_seq(__builtin_amdgcn_readlane(cu0, at), __builtin_amdgcn_readlane(cu1, at),
+                     __builtin_amdgcn_readlane(len, at), a.T, a.capacity);
 }
 
 __device__ __forceinline__ Seq load_seq(const AttendArgs& a, int b) {
-    return clamp_seq(a.cu[b], a.cu[b + 1], a.lens[b], a.T, a.max_pages << a.page_shift);
+    return clamp_seq(a.cu[b], a.cu[b + 1], a.lens[b], a.T, a.capacity);
 }
 
 // Row of the cache that holds a key (times D elements), or -1 where the table names no page.
@@ -479,9 +478,9 @@ struct Tile {
     Span span;
     int b;
     int64_t part_row;  // the tile's first row in the workspace
-    int64_t row0;      // first row of the tile in its sequence
-    int64_t rows;      // rows of the sequence
-    int64_t k0, k1;    // keys of this workgroup's part
+    int row0;          // first row of the tile in its sequence
+    int rows;          // rows of the sequence
+    int k0, k1;        // keys of this workgroup's part
     bool run;
 };
 
@@ -501,38 +500,38 @@ __device__ __forceinline__ Tile find_tile(const AttendArgs& a, uint32_t index, i
         t.row0 = tile % (kFewRows / kNarrowRows) * kNarrowRows;
         t.seq = load_seq(a, t.b);
     } else {
-        const int64_t per = ceil_div(G, R);                  // tiles a token
-        auto first = [&](int64_t cu_b, int64_t b) { return WIDE ? first_tile(cu_b, b, G, R) : cu_b * per; };
-        int64_t cu;
-        t.seq = find_seq(a, first, tile, t.b, cu);
-        t.row0 = (tile - first(cu, t.b)) * R;
+        const int per = (G + R - 1) / R;                     // tiles a token
+        auto first = [&](int cu_b, int b) { return WIDE ? first_tile(cu_b, b, G, R) : cu_b * per; };
+        t.seq = find_seq(a, first, tile, t.b);
+        t.row0 = (tile - first(t.seq.start, t.b)) * R;
     }
     t.rows = t.seq.n * G;
     const bool few = t.rows <= kFewRows;
     t.run = t.row0 >= 0 && t.row0 < t.rows && (WIDE ? !few : few || !a.both);
     if (!t.run) return t;
-    t.span = key_span(t.seq, t.row0, imin(R, t.rows - t.row0), G, a.window,
+    t.span = key_span(t.seq, t.row0, min(R, t.rows - t.row0), G, a.window,
                       WIDE ? a.wide_parts : a.narrow_parts, WIDE ? kWideLeast : kNarrowLeast);
     t.run = part < t.span.parts;
+    if (!t.run) return t;
     t.k0 = t.span.begin + part * t.span.chunk;
-    t.k1 = imin(t.span.end, t.k0 + t.span.chunk);
+    t.k1 = min(t.span.end - t.k0, t.span.chunk) + t.k0;
     return t;
 }
 
 // The place of a row of the tile: its row in q and o, and the keys it sees.
 struct Place {
-    int64_t row;       // token * heads + head
+    int row;           // token * heads + head
     int lo, hi, count; // lo <= key <= hi
     bool real;
 };
-__device__ __forceinline__ Place row_place(const AttendArgs& a, const Tile& t, int kv, int64_t r) {
+__device__ __forceinline__ Place row_place(const AttendArgs& a, const Tile& t, int kv, int r) {
     Place p;
     p.real = r < t.rows;
-    const int64_t token = p.real ? r / a.group : 0;
-    p.row = (t.seq.start + token) * a.heads + (int64_t)kv * a.group + (p.real ? r - token * a.group : 0);
-    p.hi = p.real ? (int)(t.seq.ctx - t.seq.n + token) : -1;
-    p.lo = a.window > 0 ? (int)imax(0, p.hi - (int64_t)a.window + 1) : 0;
-    p.count = (int)imax(0, (int64_t)p.hi - p.lo + 1);
+    const int token = p.real ? quotient(r, a.group) : 0;
+    p.row = (t.seq.start + token) * a.heads + kv * a.group + (p.real ? r - token * a.group : 0);
+    p.hi = p.real ? t.seq.ctx - t.seq.n + token : -1;
+    p.lo = a.window > 0 ? max(0, p.hi - a.window + 1) : 0;
+    p.count = max(0, p.hi - p.lo + 1);
     return p;
 }
 
@@ -597,7 +596,7 @@ __device__ void redo_rows(const AttendArgs& a, const Tile& t, int part, int kv, 
             const bool sees = p.hi >= 0;
             for (int e = 0; e < E; ++e) {
                 const float v = l == 0.0f && sees ? __builtin_nanf("") : o[e];
-                a.o[p.row * D + lane * E + e] = (uint16_t)bf16_pair(v, v);
+                a.o[(int64_t)p.row * D + lane * E + e] = (uint16_t)bf16_pair(v, v);
             }
         } else {
             const Parts<WIDE> w(a);
@@ -683,7 +682,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void attend_wide_kernel(AttendArgs
     if (!t.run) return;
     Place p = row_place(a, t, kv, t.row0 + 32 * wave + (lane & 31));
     Rows<D> s;
-    load_q(a.q + p.row * D + 8 * (lane >> 5), s.q, 16);
+    load_q(a.q + (int64_t)p.row * D + 8 * (lane >> 5), s.q, 16);
     wait_q(s.q);
     clear_rows<D>(s);
     // keys that any row of this wave sees, and those that all of them see
@@ -923,7 +922,7 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void attend_narrow_kernel(Attend
     const int i16 = lane & 15, quarter = lane >> 4;
     const Place p = row_place(a, t, kv, t.row0 + i16);
     Few<D> s;
-    load_q(a.q + p.row * D + 8 * quarter, s.q, 32);
+    load_q(a.q + (int64_t)p.row * D + 8 * quarter, s.q, 32);
     int all_lo = p.lo, all_hi = p.real ? p.hi : W4_MAX_CONTEXT;
 #pragma unroll
     for (int off = 8; off > 0; off >>= 1) {
@@ -1014,7 +1013,7 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void attend_narrow_kernel(Attend
     constexpr int kGroups = D / 4;                           // a thread joins 4 columns of a row
     uint32_t bad_rows = 0;
     const bool whole = t.span.parts == 1;
-    const int rows_here = (int)imin(kNarrowRows, t.rows - t.row0);
+    const int rows_here = min(kNarrowRows, t.rows - t.row0);
     for (int i = tid; i < rows_here * kGroups; i += kNarrowThreads) {
         const int row = i / kGroups, g = i % kGroups;
         float m = kNegInf;
@@ -1114,9 +1113,9 @@ __device__ __forceinline__ void combine_rows(const AttendArgs& a, uint32_t set) 
     }
     const float inv = inverse(sum, place.hi >= 0);
     if constexpr (E == 2)
-        *reinterpret_cast<uint32_t*>(a.o + place.row * D + 2 * lane) = bf16_pair(o[0] * inv, o[1] * inv);
+        *reinterpret_cast<uint32_t*>(a.o + (int64_t)place.row * D + 2 * lane) = bf16_pair(o[0] * inv, o[1] * inv);
     else
-        a.o[place.row * D + lane] = (uint16_t)bf16_pair(o[0] * inv, o[0] * inv);
+        a.o[(int64_t)place.row * D + lane] = (uint16_t)bf16_pair(o[0] * inv, o[0] * inv);
 }
 
 template <int D>

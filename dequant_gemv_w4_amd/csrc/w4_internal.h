@@ -201,7 +201,8 @@ struct AttendArgs {
     // of tiles whose keys are split: per part and tile row O / l [head_dim], and m, l
     float *narrow_o, *wide_o, *narrow_ml, *wide_ml;
     int64_t narrow_rows, wide_rows;
-    int64_t T, pages, max_pages;
+    int64_t pages, max_pages;
+    int T, capacity;     // capacity: keys that a row of the table reaches
     int B, heads, kv_heads, group, page_shift, window;
     float scale_log2;    // softmax scale / ln 2
     int narrow_parts, wide_parts;

@@ -24,25 +24,31 @@ W4_HD int64_t imin(int64_t a, int64_t b) { return a < b ? a : b; }
 W4_HD int64_t imax(int64_t a, int64_t b) { return a > b ? a : b; }
 W4_HD int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// What a workgroup of the attention computes before its first load is in 32 bits: tokens times query
+// heads stay below 2^26 and keys at 2^30 or less, and a division in 64 bits is a hundred instructions.
+W4_HD int32_t lesser(int32_t a, int32_t b) { return a < b ? a : b; }
+W4_HD int32_t greater(int32_t a, int32_t b) { return a > b ? a : b; }
+W4_HD int32_t quotient(int32_t a, int32_t b) { return (int32_t)((uint32_t)a / (uint32_t)b); }   // a >= 0, b > 0
+
 // First tile of sequence b when the tiles of all sequences are numbered without knowing their
 // lengths: floor(cu[b] G / R) + b.  It grows by at least ceil(n G / R) and at least 1 from one
 // sequence to the next (floor(a + c) - floor(a) + 1 >= ceil(c)); numbers past a sequence's
 // tiles stay idle.  All tiles lie below floor(T G / R) + B.
-W4_HD int64_t first_tile(int64_t cu_b, int64_t b, int64_t G, int64_t R) { return cu_b * G / R + b; }
+W4_HD int32_t first_tile(int32_t cu_b, int32_t b, int32_t G, int32_t R) { return quotient(cu_b * G, R) + b; }
 W4_HD int64_t tile_bound(int64_t T, int64_t B, int64_t G, int64_t R) { return T * G / R + B; }
 
 // A sequence as the kernels read it, whatever the arrays hold: its rows lie in [0, T) and its
 // keys in the table.
 struct Seq {
-    int64_t start;   // first query row
-    int64_t n;       // query rows
-    int64_t ctx;     // keys
+    int32_t start;   // first query row
+    int32_t n;       // query rows
+    int32_t ctx;     // keys
 };
-W4_HD Seq clamp_seq(int64_t cu0, int64_t cu1, int64_t len, int64_t T, int64_t capacity) {
+W4_HD Seq clamp_seq(int32_t cu0, int32_t cu1, int32_t len, int32_t T, int32_t capacity) {
     Seq s;
-    s.start = imin(imax(cu0, 0), T);
-    s.n = imax(imin(cu1, T) - s.start, 0);
-    s.ctx = imin(imax(len, 0), capacity);
+    s.start = lesser(greater(cu0, 0), T);
+    s.n = greater(lesser(cu1, T) - s.start, 0);
+    s.ctx = lesser(greater(len, 0), capacity);
     return s;
 }
 
@@ -52,24 +58,27 @@ W4_HD Seq clamp_seq(int64_t cu0, int64_t cu1, int64_t len, int64_t T, int64_t ca
 // lengths, at least `least` keys each, whatever number the launch allows.
 constexpr int kKeyTile = 64;
 struct Span {
-    int64_t begin, end, chunk;
-    int parts;
+    int32_t begin, end, chunk, parts;
 };
-W4_HD Span key_span(const Seq& s, int64_t row0, int64_t rows, int64_t G, int64_t window,
-                    int64_t max_parts, int64_t least) {
+W4_HD Span key_span(const Seq& s, int32_t row0, int32_t rows, int32_t G, int32_t window,
+                    int32_t max_parts, int32_t least) {
     Span k;
-    const int64_t pos0 = s.ctx - s.n;                        // position of the first new token
-    k.end = imin(s.ctx, pos0 + (row0 + rows - 1) / G + 1);
-    k.begin = window > 0 ? imax(0, pos0 + row0 / G - window + 1) / kKeyTile * kKeyTile : 0;
+    const int32_t pos0 = s.ctx - s.n;                        // position of the first new token
+    k.end = lesser(s.ctx, pos0 + quotient(row0 + rows - 1, G) + 1);
+    k.begin = window > 0 ? greater(0, pos0 + quotient(row0, G) - window + 1) / kKeyTile * kKeyTile : 0;
+    k.chunk = least;
+    k.parts = 1;
     if (k.end <= k.begin) {
         k.end = k.begin;
-        k.chunk = least;
-        k.parts = 1;
         return k;
     }
-    const int64_t len = k.end - k.begin;
-    k.chunk = imax(least, ceil_div(ceil_div(len, max_parts), kKeyTile) * kKeyTile);
-    k.parts = (int)ceil_div(len, k.chunk);
+    const int32_t len = k.end - k.begin;
+    if (len > least && max_parts > 1) {
+        k.chunk = greater(least, (quotient(len + max_parts - 1, max_parts) + kKeyTile - 1) / kKeyTile * kKeyTile);
+        k.parts = quotient(len + k.chunk - 1, k.chunk);
+    } else {
+        k.chunk = greater(least, (len + kKeyTile - 1) / kKeyTile * kKeyTile);
+    }
     return k;
 }
 
