@@ -1132,7 +1132,7 @@ __global__ __launch_bounds__(256) void combine_kernel(AttendArgs a) {
 // 168 with 1024; two of 100,000 tokens 85, 92 and 110.  At least 512 keys a part: one request of 4000
 // tokens (8 kv heads) takes 16 us with parts of 512, 17.3 with 256, 18.5 with 1024.
 int parts_for(int64_t tiles, int64_t target, int64_t longest, int64_t least) {
-    const int64_t want = ceil_div(target, tiles);
+    const int64_t want = longest > 2 * least ? ceil_div(target, tiles) : 1;
     return (int)imax(1, imin(want, imin(ceil_div(longest, least), kMaxParts)));
 }
 

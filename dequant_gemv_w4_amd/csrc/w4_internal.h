@@ -185,7 +185,7 @@ hipError_t launch_block_tables(const TableArgs& a, hipStream_t s);
 
 // Attention: query rows of a tile in the two kernels, keys a part takes at least, parts at most.
 constexpr int kNarrowRows = 16, kFewRows = 32, kWideRows = 256;
-constexpr int kNarrowLeast = 512, kWideLeast = 512, kMaxParts = 64;
+constexpr int kNarrowLeast = 256, kWideLeast = 512, kMaxParts = 64;
 
 struct AttendArgs {
     const uint16_t* q;

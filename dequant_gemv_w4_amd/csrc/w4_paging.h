@@ -55,7 +55,7 @@ W4_HD Seq clamp_seq(int32_t cu0, int32_t cu1, int32_t len, int32_t T, int32_t ca
 // Keys of a tile of rows [row0, row0 + rows) of a sequence (rows >= 1), and their split:
 // [begin, end) is what any row sees, begin rounded down to a multiple of kKeyTile; part p of
 // `parts` takes [begin + p * chunk, begin + (p + 1) * chunk).  The parts are cut by the actual
-// lengths, at least `least` keys each, whatever number the launch allows.
+// lengths, at least `least` keys each and none below twice that, whatever number the launch allows.
 constexpr int kKeyTile = 64;
 struct Span {
     int32_t begin, end, chunk, parts;
@@ -66,18 +66,18 @@ W4_HD Span key_span(const Seq& s, int32_t row0, int32_t rows, int32_t G, int32_t
     const int32_t pos0 = s.ctx - s.n;                        // position of the first new token
     k.end = lesser(s.ctx, pos0 + quotient(row0 + rows - 1, G) + 1);
     k.begin = window > 0 ? greater(0, pos0 + quotient(row0, G) - window + 1) / kKeyTile * kKeyTile : 0;
-    k.chunk = least;
+    k.chunk = 2 * least;
     k.parts = 1;
     if (k.end <= k.begin) {
         k.end = k.begin;
         return k;
     }
     const int32_t len = k.end - k.begin;
-    if (len > least && max_parts > 1) {
+    if (len > 2 * least && max_parts > 1) {
         k.chunk = greater(least, (quotient(len + max_parts - 1, max_parts) + kKeyTile - 1) / kKeyTile * kKeyTile);
         k.parts = quotient(len + k.chunk - 1, k.chunk);
     } else {
-        k.chunk = greater(least, (len + kKeyTile - 1) / kKeyTile * kKeyTile);
+        k.chunk = greater(2 * least, (len + kKeyTile - 1) / kKeyTile * kKeyTile);
     }
     return k;
 }
