@@ -509,8 +509,9 @@ __device__ __forceinline__ Tile find_tile(const AttendArgs& a, uint32_t index, i
     const bool few = t.rows <= kFewRows;
     t.run = t.row0 >= 0 && t.row0 < t.rows && (WIDE ? !few : few || !a.both);
     if (!t.run) return t;
-    t.span = key_span(t.seq, t.row0, min(R, t.rows - t.row0), G, a.window,
-                      WIDE ? a.wide_parts : a.narrow_parts, WIDE ? kWideLeast : kNarrowLeast);
+    const int reach = a.window > 0 ? min(t.seq.ctx, a.window) : t.seq.ctx;
+    const int parts = !WIDE ? a.narrow_parts : reach < kWideEven ? a.wide_fill : a.wide_parts;
+    t.span = key_span(t.seq, t.row0, min(R, t.rows - t.row0), G, a.window, parts, WIDE ? kWideLeast : kNarrowLeast);
     t.run = part < t.span.parts;
     if (!t.run) return t;
     t.k0 = t.span.begin + part * t.span.chunk;
@@ -542,7 +543,7 @@ __device__ __forceinline__ void load_q(const uint16_t* q, u32x4_t (&out)[N], int
     for (int d = 0; d < N; ++d) out[d] = *reinterpret_cast<const u32x4_t*>(q + d * step);
 }
 // The wait for these loads: left to the first product, inside the loop, it would be a wait for the tile
-// loads in flight at every step.
+// loads in flight at every step.  attend_narrow has it behind the first tile's loads.
 template <int N>
 __device__ __forceinline__ void wait_q(u32x4_t (&q)[N]) {
 #pragma unroll
@@ -636,6 +637,8 @@ struct Rows16 {
         const auto t = (__attribute__((address_space(4))) const int32_t*)(uintptr_t)table;
         return t[(uint32_t)(min(__builtin_amdgcn_readfirstlane(key), end - 1) >> shift)];
     }
+    // The same with a key for each lane.
+    __device__ __forceinline__ int entry_by_lane(int key) const { return table[(uint32_t)(min(key, end - 1) >> shift)]; }
     // Byte offset of the row of `key` (a multiple of 16, the same for the wave) by its entry.  For a
     // page that the cache does not have it is that of a row of its last page: the kernel then computes
     // its rows again (attend_row).
@@ -660,30 +663,49 @@ __device__ __forceinline__ void load_lds16(const uint8_t* base, uint32_t lane_by
                  : "memory", "m0");
 }
 
-constexpr int kWideWaves = 8;
+constexpr int kThreads = 512;                                // of either kernel: 8 waves
 constexpr int kWideStages = 4;
-constexpr int kWideThreads = 64 * kWideWaves;
 
+// LDS of either kernel: the keys, the values and the rest.  Three arrays, not one: the offset in an LDS
+// instruction ends at 64 KB, and within one array every place of the values would take registers for
+// addresses of its own.
+template <int D>
+struct Lds {
+    uint8_t (&k)[kWideStages * kKeyTile * 2 * D];
+    uint8_t (&v)[kWideStages * kKeyTile * 2 * D];
+    union Rest {
+        struct {
+            float scales[2][kWideStages][kKeyTile];          // of keys, of values
+            int any_missing;
+        } wide;
+        struct {
+            float scales[kThreads / 64][2 * 32];
+            float m[kThreads / 64][kNarrowRows], l[kThreads / 64][kNarrowRows];
+            uint32_t redo;
+        } narrow;
+        __device__ Rest() {}
+    } &rest;
+};
+
+// Tile `index` of the wide ones, its part `part` of the keys.
 template <int D, bool FP8>
-__global__ __launch_bounds__(kWideThreads, 2) void attend_wide_kernel(AttendArgs a) {
+__device__ __forceinline__ void attend_wide(const AttendArgs& a, uint32_t index, int part, const Lds<D>& lds) {
     constexpr int kRowBytes = FP8 ? D : 2 * D;               // of a cached row
     constexpr int kChunks = kRowBytes / 16;
-    constexpr int kStepRows = kWideThreads / kChunks;        // rows that one load of all threads covers
+    constexpr int kStepRows = kThreads / kChunks;        // rows that one load of all threads covers
     constexpr int kLoads = kStepRows >= kKeyTile ? 1 : kKeyTile / kStepRows;
     constexpr int kTileBytes = kKeyTile * 2 * D;
-    __shared__ __attribute__((aligned(16))) uint8_t kt[kWideStages][kTileBytes], vt[kWideStages][kTileBytes];
-    __shared__ __attribute__((aligned(16))) float sc_lds[2][FP8 ? kWideStages : 1][kKeyTile];   // of keys, of values
-    __shared__ int any_missing;
+    auto& kt = reinterpret_cast<uint8_t(&)[kWideStages][kTileBytes]>(lds.k);
+    auto& vt = reinterpret_cast<uint8_t(&)[kWideStages][kTileBytes]>(lds.v);
+    auto& sc_lds = lds.rest.wide.scales;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-    const int part = blockIdx.y;
     int kv;
-    // the last tiles of a sequence see the most keys: they start first
-    const Tile t = find_tile<true>(a, gridDim.x - 1 - blockIdx.x, part, kv);
+    const Tile t = find_tile<true>(a, index, part, kv);
     if (!t.run) return;
     Place p = row_place(a, t, kv, t.row0 + 32 * wave + (lane & 31));
     Rows<D> s;
     load_q(a.q + (int64_t)p.row * D + 8 * (lane >> 5), s.q, 16);
-    wait_q(s.q);
+    wait_q(s.q);                                             // behind the first tile's loads: 1.6 % slower
     clear_rows<D>(s);
     // keys that any row of this wave sees, and those that all of them see
     int any_lo = p.real ? p.lo : W4_MAX_CONTEXT, any_hi = p.hi, all_lo = p.lo, all_hi = p.real ? p.hi : W4_MAX_CONTEXT;
@@ -761,7 +783,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void attend_wide_kernel(AttendArgs
             stage<D, true, true>(vt[at], crow, chunk, vw, left(i));
         } else {
             stage<D, true, false>(kt[at], crow, chunk, kw, left(i));
-            if (chunk < 2) sc_lds[chunk][FP8 ? at : 0][crow] = crow < left(i) ? sc : 1.0f;
+            if (chunk < 2) sc_lds[chunk][at][crow] = crow < left(i) ? sc : 1.0f;
         }
     };
     // Waits for this wave's LDS accesses and then for the other waves; loads of the cache stay in
@@ -799,11 +821,15 @@ __global__ __launch_bounds__(kWideThreads, 2) void attend_wide_kernel(AttendArgs
     asm volatile("" : "+v"(sc_lane));                        // one register for all places
     f32x16_t z[2];
     uint32_t pw[16];
-    if (tid == 0) any_missing = 0;
+    if (tid == 0) lds.rest.wide.any_missing = 0;
     if (tiles > 0) {
+        const int early = rows.entry_by_lane(k0 + 16 * lane);   // of the first 16 groups of 16 keys, in one load
         for (int i = 0; i <= kAhead + 1; ++i) {              // K(0), V(0), K(1), V(1) ...
             if (i >= tiles) break;
-            look_up(i);
+            static_assert((kAhead + 2) * kKeyTile <= 64 * 16, "a lane for each group");
+#pragma unroll
+            for (int c = 0; c < kLoads; ++c)
+                entry[c] = __builtin_amdgcn_readlane(early, (i * kKeyTile + granule + c * kStepRows) >> 4);
             locate(i);
             bring(i, false);
             if (FP8 && i <= 1) put(i, false);
@@ -863,9 +889,9 @@ __global__ __launch_bounds__(kWideThreads, 2) void attend_wide_kernel(AttendArgs
         if (i + 3 < tiles) step(std::integral_constant<int, 3>(), i + 3);
     }
     if (!behind) meet();
-    if (rows.missing()) any_missing = 1;
+    if (rows.missing()) lds.rest.wide.any_missing = 1;
     __syncthreads();
-    const bool missing = any_missing != 0;
+    const bool missing = lds.rest.wide.any_missing != 0;
     if (missing && tid == 0 && a.status) atomicOr(a.status, kStatusPage);
 
     // where the row goes is found again here: kept through the loop it would cost registers
@@ -898,26 +924,25 @@ __global__ __launch_bounds__(kWideThreads, 2) void attend_wide_kernel(AttendArgs
     }
 }
 
-constexpr int kNarrowWaves = 8;
-constexpr int kNarrowThreads = 64 * kNarrowWaves;
+constexpr int kNarrowWaves = kThreads / 64;
 
+// Tile `index` of the narrow ones, its part `part` of the keys.
 template <int D, bool FP8>
-__global__ __launch_bounds__(kNarrowThreads, 2) void attend_narrow_kernel(AttendArgs a) {
+__device__ __forceinline__ void attend_narrow(const AttendArgs& a, uint32_t index, int part, const Lds<D>& lds) {
     constexpr int kKeys = 32;                                // of a wave's tile
     constexpr int kRowBytes = FP8 ? D : 2 * D;
     constexpr int kChunks = kRowBytes / 16;
     constexpr int kStepRows = 64 / kChunks;                  // rows that one load of the wave covers
     constexpr int kLoads = kKeys / kStepRows;
     constexpr int kTileBytes = kKeys * 2 * D;
-    // a wave's tiles; at the end its O (32 rows of D binary32) takes the same place
-    __shared__ __attribute__((aligned(16))) uint8_t tiles_lds[kNarrowWaves][2 * kTileBytes];
-    __shared__ __attribute__((aligned(16))) float scales[kNarrowWaves][2 * kKeys];
-    __shared__ float sm[kNarrowWaves][kNarrowRows], sl[kNarrowWaves][kNarrowRows];
-    static_assert(2 * kTileBytes >= kNarrowRows * D * 4, "O fits the tiles' place");
+    static_assert(kNarrowWaves * kTileBytes <= sizeof(lds.k) && kTileBytes >= kNarrowRows * D * 4,
+                  "a tile a wave, and at the end its O in the keys' place");
+    auto& scales = lds.rest.narrow.scales;
+    auto& lds_m = lds.rest.narrow.m;
+    auto& lds_l = lds.rest.narrow.l;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-    const int part = blockIdx.y;
     int kv;
-    const Tile t = find_tile<false>(a, blockIdx.x, part, kv);
+    const Tile t = find_tile<false>(a, index, part, kv);
     if (!t.run) return;
     const int i16 = lane & 15, quarter = lane >> 4;
     const Place p = row_place(a, t, kv, t.row0 + i16);
@@ -934,8 +959,8 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void attend_narrow_kernel(Attend
 
     // the same for all, which the compiler has to know for what follows to stay in scalar registers
     const int k0 = __builtin_amdgcn_readfirstlane((int)t.k0), k1 = __builtin_amdgcn_readfirstlane((int)t.k1);
-    uint8_t* kt = tiles_lds[wave];
-    uint8_t* vt = kt + kTileBytes;
+    uint8_t* kt = lds.k + wave * kTileBytes;
+    uint8_t* vt = lds.v + wave * kTileBytes;
     const int crow = lane / kChunks, chunk = lane % kChunks;
     const uint32_t lane_byte = (crow & 15) * kRowBytes + 16 * chunk;
     // A page holds 16 keys at least and tiles begin at multiples of 32, so either half of a tile
@@ -1001,10 +1026,10 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void attend_narrow_kernel(Attend
     float l = s.l + __shfl_xor(s.l, 16);
     l += __shfl_xor(l, 32);
     if (lane < 16) {
-        sm[wave][lane] = s.m;
-        sl[wave][lane] = l;
+        lds_m[wave][lane] = s.m;
+        lds_l[wave][lane] = l;
     }
-    float* own = reinterpret_cast<float*>(tiles_lds[wave]);
+    float* own = reinterpret_cast<float*>(kt);
     // row r's groups of 4 columns are rotated by r, so that the rows do not share banks
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
@@ -1014,20 +1039,20 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void attend_narrow_kernel(Attend
     uint32_t bad_rows = 0;
     const bool whole = t.span.parts == 1;
     const int rows_here = min(kNarrowRows, t.rows - t.row0);
-    for (int i = tid; i < rows_here * kGroups; i += kNarrowThreads) {
+    for (int i = tid; i < rows_here * kGroups; i += kThreads) {
         const int row = i / kGroups, g = i % kGroups;
         float m = kNegInf;
 #pragma unroll
-        for (int w = 0; w < kNarrowWaves; ++w) m = fmaxf(m, sm[w][row]);
+        for (int w = 0; w < kNarrowWaves; ++w) m = fmaxf(m, lds_m[w][row]);
         float sum = 0.0f;
         f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int w = 0; w < kNarrowWaves; ++w) {
-            const float mw = sm[w][row];
+            const float mw = lds_m[w][row];
             const float f = mw == kNegInf ? 0.0f : exp2_fast(mw - m);
-            const f32x4_t ow = *reinterpret_cast<const f32x4_t*>(reinterpret_cast<const float*>(tiles_lds[w]) +
+            const f32x4_t ow = *reinterpret_cast<const f32x4_t*>(reinterpret_cast<const float*>(lds.k + w * kTileBytes) +
                                                                 row * D + 4 * ((g + row) & (kGroups - 1)));
-            sum += f * sl[w][row];
+            sum += f * lds_l[w][row];
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] += f * ow[j];
         }
@@ -1043,20 +1068,46 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void attend_narrow_kernel(Attend
         store4<false>(a, t, part, row, pr.row, D, 4 * g, v);
         if (g == 0 && !whole) store_ml<false>(a, t, part, row, m, sum);
     }
-    __shared__ uint32_t redo;
-    if (tid == 0) redo = 0;
+    if (tid == 0) lds.rest.narrow.redo = 0;
     __syncthreads();
     if (rows.missing()) {
         bad_rows = (uint32_t)(((uint64_t)1 << rows_here) - 1);
         if (lane == 0 && a.status) atomicOr(a.status, kStatusPage);
     }
-    if (bad_rows) atomicOr(&redo, bad_rows);
+    if (bad_rows) atomicOr(&lds.rest.narrow.redo, bad_rows);
     __syncthreads();
-    if (redo) {
+    if (lds.rest.narrow.redo) {
         __threadfence();                                     // the rows' first results have landed
         __syncthreads();
-        if (wave == 0) redo_rows<D, FP8, false>(a, t, part, kv, 0, redo);
+        if (wave == 0) redo_rows<D, FP8, false>(a, t, part, kv, 0, lds.rest.narrow.redo);
     }
+}
+
+#define W4_ATTEND_LDS(D)                                                                            \
+    __shared__ __attribute__((aligned(16))) uint8_t lds_k[kWideStages * kKeyTile * 2 * (D)];         \
+    __shared__ __attribute__((aligned(16))) uint8_t lds_v[kWideStages * kKeyTile * 2 * (D)];         \
+    __shared__ __attribute__((aligned(16))) typename Lds<(D)>::Rest lds_rest;                        \
+    const Lds<(D)> lds = {lds_k, lds_v, lds_rest}
+
+template <int D, bool FP8>
+__global__ __launch_bounds__(kThreads, 2) void attend_narrow_kernel(AttendArgs a) {
+    W4_ATTEND_LDS(D);
+    attend_narrow<D, FP8>(a, blockIdx.x, blockIdx.y, lds);
+}
+
+// Both kinds of tiles in one launch: the wide ones first, of them those last in their sequence, which
+// see the most keys.
+template <int D, bool FP8>
+__global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
+    W4_ATTEND_LDS(D);
+    const uint32_t wide = (uint32_t)a.wide_tiles * a.wide_parts;
+    const bool first = blockIdx.x < wide;
+    const uint32_t index = first ? blockIdx.x : blockIdx.x - wide, tiles = first ? a.wide_tiles : a.narrow_tiles;
+    const uint32_t part = __builtin_amdgcn_readfirstlane(index / tiles);   // the division leaves scalar registers
+    if (first)
+        attend_wide<D, FP8>(a, tiles - 1 - (index - part * tiles), part, lds);
+    else
+        attend_narrow<D, FP8>(a, index - part * tiles, part, lds);
 }
 
 // Joins the parts of the rows that were split: one wave a row, the tiles numbered as in the
@@ -1127,12 +1178,17 @@ __global__ __launch_bounds__(256) void combine_kernel(AttendArgs a) {
         combine_rows<D, true>(a, blockIdx.x - narrow);
 }
 
-// Parts that a launch allows per tile, to make `target` workgroups.  Narrow: 256, one a compute unit
-// (LDS holds no second): 32 requests of up to 8192 tokens take 155 us with 256 (unsplit), 165 with 512,
-// 168 with 1024; two of 100,000 tokens 85, 92 and 110.  At least 512 keys a part: one request of 4000
-// tokens (8 kv heads) takes 16 us with parts of 512, 17.3 with 256, 18.5 with 1024.
+// Parts that a launch allows per tile, to make up to `target` workgroups.  256 is one a compute unit (LDS
+// holds no second).  Single tokens, workgroups up to 256: 24 requests of up to 2000 tokens (192 tiles)
+// take 35 us unsplit, 42 in two parts each; 5 of up to 8000 over 32 kv heads 113 and 128; 32 of up to 8192
+// 155 with 256 workgroups, 165 with 512, 168 with 1024.  Wide tiles: up to 256 as well, since a part
+// costs a pass over its rows' results (1100 tokens over 500: 60 us unsplit, 86 in two parts; over 2000 136
+// and 160), but where the keys are many (kWideEven) about 512, so that the last round of workgroups is a
+// small one (over 8000: 448 and 400, over 30,000 1602 and 1284).  At least kNarrowLeast keys a part, and
+// none below twice that: one request over 1000 keys takes 11.2 us with parts of 256, 12.1 with 512, over
+// 500 8.5 unsplit and 10.2 split.  Wide: 16 tokens over 2000 16.0 with 128, 17.2 with 256, 22.8 with 512.
 int parts_for(int64_t tiles, int64_t target, int64_t longest, int64_t least) {
-    const int64_t want = longest > 2 * least ? ceil_div(target, tiles) : 1;
+    const int64_t want = longest > 2 * least ? target / tiles : 1;
     return (int)imax(1, imin(want, imin(ceil_div(longest, least), kMaxParts)));
 }
 
@@ -1145,7 +1201,9 @@ void plan_attend(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int64_t 
     p->narrow_tiles = (p->both ? B * (kFewRows / kNarrowRows) : T * ceil_div(G, kNarrowRows)) * kv_heads;
     p->narrow_parts = parts_for(p->narrow_tiles, 256, capacity, kNarrowLeast);
     p->wide_tiles = p->both ? tile_bound(T, B, G, kWideRows) * kv_heads : 0;
-    p->wide_parts = p->both ? parts_for(p->wide_tiles, 512, capacity, kWideLeast) : 1;
+    p->wide_fill = p->both ? parts_for(p->wide_tiles, 256, capacity, kWideLeast) : 1;
+    p->wide_parts = p->both && capacity >= kWideEven
+                        ? parts_for(p->wide_tiles, 511 + p->wide_tiles, capacity, kWideLeast) : p->wide_fill;
 }
 
 static int64_t split_rows(bool wide, const AttendPlan& p) {
@@ -1160,13 +1218,13 @@ size_t attend_workspace(int64_t D, const AttendPlan& p) {
 template <int D, bool FP8>
 static hipError_t launch_attend_d(const AttendArgs& a, const AttendPlan& p, hipStream_t s) {
     if (p.both)
-        hipLaunchKernelGGL((attend_wide_kernel<D, FP8>), dim3((unsigned)p.wide_tiles, (unsigned)p.wide_parts),
-                           dim3(kWideThreads), 0, s, a);
+        hipLaunchKernelGGL((attend_kernel<D, FP8>),
+                           dim3((unsigned)(p.wide_tiles * p.wide_parts + p.narrow_tiles * p.narrow_parts)),
+                           dim3(kThreads), 0, s, a);
+    else
+        hipLaunchKernelGGL((attend_narrow_kernel<D, FP8>), dim3((unsigned)p.narrow_tiles, (unsigned)p.narrow_parts),
+                           dim3(kThreads), 0, s, a);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((attend_narrow_kernel<D, FP8>), dim3((unsigned)p.narrow_tiles, (unsigned)p.narrow_parts),
-                       dim3(kNarrowThreads), 0, s, a);
-    e = hipGetLastError();
     if (e == hipSuccess && a.wide_rows + a.narrow_rows > 0) {
         hipLaunchKernelGGL(combine_kernel<D>, dim3((unsigned)((a.wide_rows + a.narrow_rows) / 4)), dim3(256), 0, s, a);
         e = hipGetLastError();
@@ -1176,8 +1234,11 @@ static hipError_t launch_attend_d(const AttendArgs& a, const AttendPlan& p, hipS
 
 hipError_t launch_attend(AttendArgs a, int head_dim, bool fp8, const AttendPlan& p, void* workspace, hipStream_t s) {
     a.both = p.both;
+    a.narrow_tiles = (int)p.narrow_tiles;
+    a.wide_tiles = (int)p.wide_tiles;
     a.narrow_parts = p.narrow_parts;
     a.wide_parts = p.wide_parts;
+    a.wide_fill = p.wide_fill;
     a.narrow_rows = split_rows(false, p);
     a.wide_rows = split_rows(true, p);
     a.narrow_o = static_cast<float*>(workspace);

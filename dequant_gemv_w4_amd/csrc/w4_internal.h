@@ -185,7 +185,7 @@ hipError_t launch_block_tables(const TableArgs& a, hipStream_t s);
 
 // Attention: query rows of a tile in the two kernels, keys a part takes at least, parts at most.
 constexpr int kNarrowRows = 16, kFewRows = 32, kWideRows = 256;
-constexpr int kNarrowLeast = 256, kWideLeast = 512, kMaxParts = 64;
+constexpr int kNarrowLeast = 256, kWideLeast = 128, kWideEven = 4096, kMaxParts = 64;
 
 struct AttendArgs {
     const uint16_t* q;
@@ -205,14 +205,14 @@ struct AttendArgs {
     int T, capacity;     // capacity: keys that a row of the table reaches
     int B, heads, kv_heads, group, page_shift, window;
     float scale_log2;    // softmax scale / ln 2
-    int narrow_parts, wide_parts;
-    bool both;           // both kernels are launched
+    int narrow_tiles, wide_tiles, narrow_parts, wide_parts, wide_fill;
+    bool both;           // both kinds of tiles are launched
 };
 // What the host knows of a call decides the launches; the parts that a tile really has follow
 // from the lengths on the device.
 struct AttendPlan {
     int64_t narrow_tiles, wide_tiles;   // workgroups of one part
-    int narrow_parts, wide_parts;
+    int narrow_parts, wide_parts, wide_fill;
     bool both;
 };
 void plan_attend(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int64_t capacity, AttendPlan* p);
