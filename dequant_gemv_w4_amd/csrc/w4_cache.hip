@@ -242,7 +242,7 @@ __global__ __launch_bounds__(kTableThreads) void block_tables_kernel(TableArgs a
         }
         const int64_t pos = (int64_t)sc.cached[lo] + (t - sc.cu[lo]);
         const int64_t at = pos >> a.page_shift;
-        const int64_t have = ceil_div(sc.cached[lo], page_size);
+        const int64_t have = (sc.cached[lo] + page_size - 1) >> a.page_shift;
         int32_t* entry = a.table + (int64_t)lo * a.max_pages + at;
         int64_t page;
         if (at >= have) {

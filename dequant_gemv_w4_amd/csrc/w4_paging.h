@@ -92,13 +92,14 @@ struct Need {
     int64_t take;    // pages more
     bool fits;       // lengths valid, table wide enough
 };
-W4_HD Need page_need(int64_t len, int64_t fresh, int64_t page, int64_t max_pages) {
+W4_HD Need page_need(int64_t len, int64_t fresh, int64_t page, int64_t max_pages) {   // page: a power of two
     Need d;
+    const int shift = __builtin_ctzll((unsigned long long)page);
     d.have = d.take = 0;
     d.fits = len >= 0 && fresh >= 0;
     if (!d.fits) return d;
-    d.have = ceil_div(len, page);
-    const int64_t want = ceil_div(len + fresh, page);
+    d.have = (len + page - 1) >> shift;
+    const int64_t want = (len + fresh + page - 1) >> shift;
     d.fits = want <= max_pages && len + fresh <= INT32_MAX;
     d.take = d.fits ? want - d.have : 0;
     return d;
