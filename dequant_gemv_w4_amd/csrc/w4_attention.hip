@@ -17,16 +17,25 @@
 // the bfloat16 output, and averaged over the keys: outputs are 1.4 times as far from 64 bits as an
 // unrounded P would leave them).  attend_narrow, which waits for memory, multiplies V by what that
 // rounding leaves as well (P = p + rest, both bfloat16, together within 2^-16): a decode step of 32
-// requests takes 156.5 us instead of 154.4.  E4M3 codes enter as exact bfloat16 values; the scale of a
+// requests takes 153.0 us instead of 152.3.  E4M3 codes enter as exact bfloat16 values; the scale of a
 // key's row multiplies its scores, that of a value's row its P, both in binary32.
 //
 // attend_wide: 256 rows a workgroup, 8 waves of 32 rows; tiles of 64 keys pass through LDS for
-// all of them, the next tile's loads in flight, and the two waves of a SIMD take turns on the
-// matrix unit.
+// all of them, the next tiles' loads in flight, and the two waves of a SIMD take turns on the matrix
+// unit.  Bound by the matrix unit and LDS together: two chunks of up to 2048 tokens over up to 6144
+// cached (64 heads, 8 kv heads, 0.79 Tflop) take 722 to 763 us on different cards, 1.03 to 1.09 PFLOP/s
+// where a large bfloat16 product of the vendor's library reaches 1.37; the matrix unit is busy for 51 % of
+// the cycles, and the products without their LDS reads take 0.55 of the time.  64 rows a wave would halve
+// those reads, with 512 registers and one wave a SIMD, which then has none to take turns with.
 // attend_narrow: 16 rows, for single tokens: the waves take 32-key tiles in turn, each with its own
 // piece of LDS, and join their sums at the end.  (Tiles of 32 rows, twice the registers and matrix
 // work: 157.0 us instead of 152.9 for single tokens of 32 requests over up to 8192 cached, 86.2
-// instead of 80.6 over 100,000 in E4M3, 13.8 instead of 12.8 for one request over 1000.)
+// instead of 80.6 over 100,000 in E4M3, 13.8 instead of 12.8 for one request over 1000.)  Bound by
+// memory: these 32 requests' 852 MB come at 5.6 TB/s, a plain read's rate being 5.9.  A short context is
+// bound by latency: one request over 1000 keys (16 MB) takes 11.2 us, 8.3 of them one chain of lengths,
+// table entries, rows, products and the waves' join, and 3 the launch that joins the parts.  Code that
+// the chain runs once is paid at the rate at which instructions arrive (600 more cost 1.5 us: two tiles
+// of loads in flight instead of one, in a loop unrolled by two, were dropped for that).
 // Either may split the keys of a tile over several workgroups, which then leave (m, l, O / l) in
 // the workspace for combine_kernel.
 //
