@@ -1109,9 +1109,10 @@ __global__ __launch_bounds__(kThreads, 2) void attend_narrow_kernel(AttendArgs a
 template <int D, bool FP8>
 __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
     W4_ATTEND_LDS(D);
-    const uint32_t wide = (uint32_t)a.wide_tiles * a.wide_parts;
-    const bool first = blockIdx.x < wide;
-    const uint32_t index = first ? blockIdx.x : blockIdx.x - wide, tiles = first ? a.wide_tiles : a.narrow_tiles;
+    const uint32_t wide = (uint32_t)a.wide_tiles * a.wide_parts, number = blockIdx.y * gridDim.x + blockIdx.x;
+    if (number >= wide + (uint32_t)a.narrow_tiles * a.narrow_parts) return;
+    const bool first = number < wide;
+    const uint32_t index = first ? number : number - wide, tiles = first ? a.wide_tiles : a.narrow_tiles;
     const uint32_t part = __builtin_amdgcn_readfirstlane(index / tiles);   // the division leaves scalar registers
     if (first)
         attend_wide<D, FP8>(a, tiles - 1 - (index - part * tiles), part, lds);
@@ -1226,11 +1227,11 @@ size_t attend_workspace(int64_t D, const AttendPlan& p) {
 
 template <int D, bool FP8>
 static hipError_t launch_attend_d(const AttendArgs& a, const AttendPlan& p, hipStream_t s) {
-    if (p.both)
-        hipLaunchKernelGGL((attend_kernel<D, FP8>),
-                           dim3((unsigned)(p.wide_tiles * p.wide_parts + p.narrow_tiles * p.narrow_parts)),
-                           dim3(kThreads), 0, s, a);
-    else
+    if (p.both) {
+        // a dimension of a grid holds less than 2^32 threads
+        const int64_t n = p.wide_tiles * p.wide_parts + p.narrow_tiles * p.narrow_parts, x = imin(n, 1 << 22);
+        hipLaunchKernelGGL((attend_kernel<D, FP8>), dim3((unsigned)x, (unsigned)ceil_div(n, x)), dim3(kThreads), 0, s, a);
+    } else
         hipLaunchKernelGGL((attend_narrow_kernel<D, FP8>), dim3((unsigned)p.narrow_tiles, (unsigned)p.narrow_parts),
                            dim3(kThreads), 0, s, a);
     hipError_t e = hipGetLastError();

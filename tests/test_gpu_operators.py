@@ -692,6 +692,25 @@ def test_attention_of_most_requests():
             assert np.all(np.abs(got[cu[b] + t] - ref) <= (UB + 2.0 ** -14) * ref), (b, t)
 
 
+def test_attention_of_most_tiles():
+    # as many requests and kv heads as there may be: more workgroups than one grid dimension holds
+    B, kv, d, pages = 4096, 1024, 64, 8
+    new = np.ones(B, np.int32)
+    new[7] = 2
+    ctx = (new + np.arange(B) % 13).astype(np.int32)
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    T = int(cu[-1])
+    v = torch.arange(pages * 16, device=DEV, dtype=F32).remainder(97).view(pages, 1, 16, 1).expand(pages, kv, 16, d).contiguous().to(BF)
+    cache = w4.W4KVCache(torch.zeros_like(v), v)
+    table = (torch.arange(B, dtype=torch.int32, device=DEV) % pages)[:, None].contiguous()
+    _say("attention of 4096 requests and 1024 kv heads")
+    o = w4.w4_paged_attention(torch.zeros(T, kv, d, dtype=BF, device=DEV), cache, table, _dev(cu), _dev(ctx), 1.0)
+    vals = to_np32(v)[:, 0, :, 0].astype(np.float64)
+    ref = np.concatenate([[vals[b % pages, : ctx[b] - new[b] + t + 1].mean() for t in range(new[b])] for b in range(B)])
+    ref = torch.from_numpy(ref).to(DEV, F32).view(T, 1, 1)     # off by 2^-24 of itself, inside the 2^-14 below
+    assert bool(((o.float() - ref).abs() <= (UB + 2.0 ** -14) * ref).all())
+
+
 def test_attention_far_offsets():
     # a cache past 2^32 bytes: pages at its end are reached with 64-bit offsets
     pages, page, kv, d = 300_000, 16, 8, 128
