@@ -520,6 +520,9 @@ ATTEND = [  # new, cached, heads, kv, d, page, fp8, window
     ([1] * 2, [700, 9000], 40, 1, 64, 32, True, 100),
     ([1, 3, 40], [6000, 5000, 9], 16, 2, 128, 16, False, 0),  # 8, 24 and 320 rows, the few split over the keys
     ([2, 1, 50], [4000, 3, 9], 17, 1, 64, 16, True, 0),       # 34, 17 and 850 rows
+    ([3], [700], 8, 1, 128, 16, False, 0),                    # few rows in all: 24, 16 and 32
+    ([2, 0, 2], [30, 4, 2000], 8, 2, 64, 16, True, 0),
+    ([31, 1], [3, 5000], 4, 4, 128, 32, False, 40),
     ([300, 1300], [4500, 100], 32, 8, 64, 64, False, 0),      # split and unsplit tiles in one call
     ([300, 1, 1300], [4500, 900, 100], 32, 8, 64, 64, False, 700),
 ]
