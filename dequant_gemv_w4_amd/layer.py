@@ -23,7 +23,7 @@ _F64, _U8, _I8 = (torch.float64,), (torch.uint8,), (torch.int8,)
 def _want(t, dtypes, shape, name, device):
     """A contiguous tensor of one of the types on ``device``, of that shape unless it is None."""
     try:
-        if t.dtype in dtypes and t.device == device and t.is_contiguous() and (shape is None or t.shape == shape):
+        if t.dtype in dtypes and t.get_device() == device.index and t.is_contiguous() and (shape is None or t.shape == shape):
             return
     except AttributeError:
         pass
@@ -70,11 +70,12 @@ def _rows_of(x, name):
     """x as [rows, values] on a GPU."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype not in _FLOATS or not x.is_contiguous():
         _require(x, _FLOATS, None, name)
-    if x.dim() == 1:
-        x = x.unsqueeze(0)
-    if x.dim() != 2:
+    dim = x.dim()
+    if dim == 2:
+        return x
+    if dim != 1:
         raise ValueError(f"{name} must be [rows, values]")
-    return x
+    return x.unsqueeze(0)
 
 
 def _value_rows(y, out_dtype, shape, device):
@@ -101,22 +102,24 @@ def _code_rows(codes, scales, dtypes, shape, device):
 def _norm_args(x, weight, eps, residual, residual_out):
     x = _rows_of(x, "x")
     shape, device = x.shape, x.device
-    _want(weight, _FLOATS, shape[1:], "weight", device)
+    rows, K = shape
+    _want(weight, _FLOATS, (K,), "weight", device)
+    r = r_out = None
     rt = W4_F32
     if residual is not None:
-        if residual_out is None:
-            residual_out = residual
         if residual.dim() == 1:
             residual = residual.unsqueeze(0)
-        if residual_out.dim() == 1:
-            residual_out = residual_out.unsqueeze(0)
         _want(residual, _FLOATS, shape, "residual", device)
-        _want(residual_out, (residual.dtype,), shape, "residual_out", device)
-        rt = _code(residual)
+        r, rt = residual.data_ptr(), _code(residual)
+        r_out = r
+        if residual_out is not None:
+            if residual_out.dim() == 1:
+                residual_out = residual_out.unsqueeze(0)
+            _want(residual_out, (residual.dtype,), shape, "residual_out", device)
+            r_out = residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out without residual")
-    return x, (x.data_ptr(), _code(x), _opt(residual), _opt(residual_out), rt, weight.data_ptr(), _code(weight), eps,
-               shape[0], shape[1])
+    return x, (x.data_ptr(), _code(x), r, r_out, rt, weight.data_ptr(), _code(weight), eps, rows, K)
 
 
 def w4_rmsnorm(x, weight, eps, residual=None, residual_out=None, y=None, out_dtype=None):
