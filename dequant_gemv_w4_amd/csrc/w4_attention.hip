@@ -26,7 +26,8 @@
 // cached (64 heads, 8 kv heads, 0.79 Tflop) take 722 to 763 us on different cards, 1.03 to 1.09 PFLOP/s
 // where a large bfloat16 product of the vendor's library reaches 1.37; the matrix unit is busy for 51 % of
 // the cycles, and the products without their LDS reads take 0.55 of the time.  64 rows a wave would halve
-// those reads, with 512 registers and one wave a SIMD, which then has none to take turns with.
+// those reads, with 512 registers and one wave a SIMD, which then has none to take turns with; half of
+// those registers are out of the vector unit's reach, and the compiler moves 256 values a step for that.
 // attend_narrow: 16 rows, for single tokens: the waves take 32-key tiles in turn, each with its own
 // piece of LDS, and join their sums at the end.  (Tiles of 32 rows, twice the registers and matrix
 // work: 157.0 us instead of 152.9 for single tokens of 32 requests over up to 8192 cached, 86.2
