@@ -28,9 +28,9 @@
 // the cycles, and the products without their LDS reads take 0.55 of the time.  64 rows a wave would halve
 // those reads, with 512 registers and one wave a SIMD, which then has none to take turns with; half of
 // those registers are out of the vector unit's reach, and the compiler moves 256 values a step for that.
-// attend_narrow: 16 rows, for single tokens: the waves take 32-key tiles in turn, each with its own
-// piece of LDS, and join their sums at the end.  (Tiles of 32 rows, twice the registers and matrix
-// work: 157.0 us instead of 152.9 for single tokens of 32 requests over up to 8192 cached, 86.2
+// attend_narrow: 16 rows or 32, for single tokens: the waves take 32-key tiles in turn, each with its own
+// piece of LDS, and join their sums at the end.  (Products of 32 rows for 8 rows, twice the registers and
+// matrix work: 157.0 us instead of 152.9 for single tokens of 32 requests over up to 8192 cached, 86.2
 // instead of 80.6 over 100,000 in E4M3, 13.8 instead of 12.8 for one request over 1000.)  Bound by
 // memory: these 32 requests' 852 MB come at 5.6 TB/s, a plain read's rate being 5.9.  A short context is
 // bound by latency: one request over 1000 keys (16 MB) takes 11.2 us, 8.3 of them one chain of lengths,
@@ -304,84 +304,111 @@ __device__ __forceinline__ void accumulate(Rows<D>& s, const uint8_t* vt, const 
     }
 }
 
-// The running state of attend_narrow's 16 query rows: lane % 16 is the row, lane / 16 picks a quarter
-// of the keys in the scores and of the columns in O (register r of block i: column 16 i +
+// The running state of attend_narrow's 16 N query rows: lane % 16 is the row of each 16, lane / 16 picks a
+// quarter of the keys in the scores and of the columns in O (register r of block i: column 16 i +
 // 4 (lane / 16) + r).  l is the lane's own part of the sum.
-template <int D>
+template <int D, int N>
 struct Few {
-    u32x4_t q[D / 32];
-    f32x4_t o[D / 16];
-    float m, l;
+    u32x4_t q[N][D / 32];
+    f32x4_t o[N][D / 16];
+    float m[N], l[N];
+    int lo[N], count[N];                                     // the rows see `count` keys from lo on
 };
 
-// A step of attend_narrow: the 32 staged keys from position `first` on; lane as the addresses in LDS
-// take it, sc: LDS address of the keys' row scales from row 4 (lane / 16) on, the values' 32 floats on.
-template <int D, bool FP8>
-__device__ __forceinline__ void step_narrow(Few<D>& s, const uint8_t* kt, const uint8_t* vt, uint32_t sc, int lane,
-                                            float scale, int first, int lo, int count, bool mask) {
-    const int i16 = lane & 15, quarter = lane >> 4;
-    f32x4_t z[2];
+// A step of attend_narrow: the 32 staged keys from position `first` on.  sc: LDS address of the keys' row
+// scales from row 4 (lane / 16) on, the values' 32 floats on; mask: whether the step reaches outside some
+// row's keys.
+template <int D, bool FP8, int N>
+__device__ __forceinline__ void step_narrow(Few<D, N>& s, const uint8_t* kt, const uint8_t* vt, uint32_t sc, float scale,
+                                            int first, bool mask) {
+    const int lane = threadIdx.x & 63, i16 = lane & 15, quarter = lane >> 4;
+    f32x4_t z[N][2];
 #pragma unroll
-    for (int b = 0; b < 2; ++b) z[b] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) z[n][b] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int d = 0; d < D / 32; ++d)
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             const u32x4_t k = *reinterpret_cast<const u32x4_t*>(kt + k_place<D>(16 * b + i16, 4 * d + quarter));
-            z[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, k),
-                                                           __builtin_bit_cast(bf16x8_t, s.q[d]), z[b], 0, 0, 0);
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+                z[n][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, k),
+                                                                  __builtin_bit_cast(bf16x8_t, s.q[n][d]), z[n][b], 0, 0, 0);
         }
     if constexpr (FP8) {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             const f32x4_t f = read_lds_f32x4(sc + 64 * b);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) z[b][r] *= f[r];
+            for (int n = 0; n < N; ++n)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) z[n][b][r] *= f[r];
         }
     }
     if (mask) {
-        const uint32_t from = (uint32_t)(first + 4 * quarter - lo);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const uint32_t from = (uint32_t)(first + 4 * quarter - s.lo[n]);
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (from + (16 * b + r) >= (uint32_t)s.count[n]) z[n][b][r] = kNegInf;
+        }
+    }
+    float mx[N];
+    bool grow = false;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        mx[n] = z[n][0][0];
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                if (from + (16 * b + r) >= (uint32_t)count) z[b][r] = kNegInf;
+            for (int r = 0; r < 4; ++r) mx[n] = fmaxf(mx[n], z[n][b][r]);
+        mx[n] = quarter_max(mx[n]) * scale;                  // scale > 0
+        grow |= mx[n] > s.m[n] + kSlack;
     }
-    float mx = z[0][0];
+    if (__any(grow)) {
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+        for (int n = 0; n < N; ++n) {
+            const float m = fmaxf(s.m[n], mx[n]);
+            const float f = m == s.m[n] ? 1.0f : exp2_fast(s.m[n] - m);
+            s.m[n] = m;
+            s.l[n] *= f;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) mx = fmaxf(mx, z[b][r]);
-    mx = quarter_max(mx) * scale;                            // scale > 0
-    if (__any(mx > s.m + kSlack)) {
-        const float m = fmaxf(s.m, mx);
-        const float f = m == s.m ? 1.0f : exp2_fast(s.m - m);
-        s.m = m;
-        s.l *= f;
+            for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) s.o[i][r] *= f;
+                for (int r = 0; r < 4; ++r) s.o[n][i][r] *= f;
+        }
     }
-    const float sub = s.m == kNegInf ? 0.0f : s.m;           // nothing seen yet: every weight is 0
-    u32x4_t p, rest;                                         // and what the rounding left, itself within 2^-8
-    float sum = 0.0f;
+    u32x4_t p[N], rest[N];                                   // and what the rounding left, itself within 2^-8
+    float sub[N], sum[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        sub[n] = s.m[n] == kNegInf ? 0.0f : s.m[n];          // nothing seen yet: every weight is 0
+        sum[n] = 0.0f;
+    }
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
         f32x4_t f = {1.0f, 1.0f, 1.0f, 1.0f};
         if constexpr (FP8) f = read_lds_f32x4(sc + 128 + 64 * b);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float e0 = exp2_fast(fmaf(z[b][2 * i], scale, -sub));
-            const float e1 = exp2_fast(fmaf(z[b][2 * i + 1], scale, -sub));
-            sum += e0 + e1;
-            const float w0 = FP8 ? e0 * f[2 * i] : e0, w1 = FP8 ? e1 * f[2 * i + 1] : e1;
-            const uint32_t w = bf16_pair(w0, w1);
-            p[2 * b + i] = w;
-            rest[2 * b + i] = bf16_pair(w0 - __uint_as_float(w << 16), w1 - __uint_as_float(w & 0xFFFF0000u));
-        }
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float e0 = exp2_fast(fmaf(z[n][b][2 * i], scale, -sub[n]));
+                const float e1 = exp2_fast(fmaf(z[n][b][2 * i + 1], scale, -sub[n]));
+                sum[n] += e0 + e1;
+                const float w0 = FP8 ? e0 * f[2 * i] : e0, w1 = FP8 ? e1 * f[2 * i + 1] : e1;
+                const uint32_t w = bf16_pair(w0, w1);
+                p[n][2 * b + i] = w;
+                rest[n][2 * b + i] = bf16_pair(w0 - __uint_as_float(w << 16), w1 - __uint_as_float(w & 0xFFFF0000u));
+            }
     }
-    s.l += sum;
+#pragma unroll
+    for (int n = 0; n < N; ++n) s.l[n] += sum[n];
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {                       // 16 columns, the 32 keys in the order of p
         const int chunk = 2 * i + ((i16 & 3) >> 1), off = 8 * (i16 & 1), r0 = 4 * quarter + (i16 >> 2);
@@ -389,8 +416,11 @@ __device__ __forceinline__ void step_narrow(Few<D>& s, const uint8_t* kt, const 
         const uint64_t a1 = read_tr(vt + v_place<D>(r0 + 16, chunk) + off);
         const bf16x8_t v = __builtin_bit_cast(
             bf16x8_t, u32x4_t{(uint32_t)a0, (uint32_t)(a0 >> 32), (uint32_t)a1, (uint32_t)(a1 >> 32)});
-        s.o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, __builtin_bit_cast(bf16x8_t, p), s.o[i], 0, 0, 0);
-        s.o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, __builtin_bit_cast(bf16x8_t, rest), s.o[i], 0, 0, 0);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            s.o[n][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, __builtin_bit_cast(bf16x8_t, p[n]), s.o[n][i], 0, 0, 0);
+            s.o[n][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, __builtin_bit_cast(bf16x8_t, rest[n]), s.o[n][i], 0, 0, 0);
+        }
     }
 }
 
@@ -494,24 +524,25 @@ struct Tile {
     bool run;
 };
 
-// Tile number `index` of attend_wide's or attend_narrow's launch.  Where both are launched, a
-// sequence of at most kFewRows rows is the narrow kernel's, and that launch has kFewRows /
-// kNarrowRows tiles a sequence; alone it has as many tiles a token as G rows fill.
-template <bool WIDE>
+// Tile number `index` of R rows: of attend_wide's (R = kWideRows) or attend_narrow's.  Where both are
+// launched, a sequence of at most kFewRows rows is the narrow kernel's, as its only tile; alone that has,
+// for as many tokens as sequences, the tiles that G rows fill for each token.
+template <int R>
 __device__ __forceinline__ Tile find_tile(const AttendArgs& a, uint32_t index, int part, int& kv) {
-    constexpr int R = WIDE ? kWideRows : kNarrowRows;
+    constexpr bool WIDE = R == kWideRows;
     Tile t;
     const int G = a.group;
     const int tile = __builtin_amdgcn_readfirstlane((int)(index / (uint32_t)a.kv_heads));
     kv = (int)index - tile * a.kv_heads;
     t.part_row = (int64_t)index * R;
     if (!WIDE && a.both) {
-        t.b = tile / (kFewRows / kNarrowRows);
-        t.row0 = tile % (kFewRows / kNarrowRows) * kNarrowRows;
+        t.b = tile;
+        t.row0 = 0;
         t.seq = load_seq(a, t.b);
     } else {
         const int per = (G + R - 1) / R;                     // tiles a token
-        auto first = [&](int cu_b, int b) { return WIDE ? first_tile(cu_b, b, G, R) : cu_b * per; };
+        const bool by_token = !WIDE && a.T == a.B;
+        auto first = [&](int cu_b, int b) { return by_token ? cu_b * per : first_tile(cu_b, b, G, R); };
         t.seq = find_seq(a, first, tile, t.b);
         t.row0 = (tile - first(t.seq.start, t.b)) * R;
     }
@@ -690,7 +721,7 @@ struct Lds {
         } wide;
         struct {
             float scales[kThreads / 64][2 * 32];
-            float m[kThreads / 64][kNarrowRows], l[kThreads / 64][kNarrowRows];
+            float m[kThreads / 64][kFewRows], l[kThreads / 64][kFewRows];
             uint32_t redo;
         } narrow;
         __device__ Rest() {}
@@ -710,7 +741,7 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, uint32_t index,
     auto& sc_lds = lds.rest.wide.scales;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     int kv;
-    const Tile t = find_tile<true>(a, index, part, kv);
+    const Tile t = find_tile<kWideRows>(a, index, part, kv);
     if (!t.run) return;
     Place p = row_place(a, t, kv, t.row0 + 32 * wave + (lane & 31));
     Rows<D> s;
@@ -937,28 +968,36 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, uint32_t index,
 constexpr int kNarrowWaves = kThreads / 64;
 
 // Tile `index` of the narrow ones, its part `part` of the keys.
-template <int D, bool FP8>
+template <int D, bool FP8, int N>
 __device__ __forceinline__ void attend_narrow(const AttendArgs& a, uint32_t index, int part, const Lds<D>& lds) {
+    constexpr int kRows = 16 * N;
     constexpr int kKeys = 32;                                // of a wave's tile
     constexpr int kRowBytes = FP8 ? D : 2 * D;
     constexpr int kChunks = kRowBytes / 16;
     constexpr int kStepRows = 64 / kChunks;                  // rows that one load of the wave covers
     constexpr int kLoads = kKeys / kStepRows;
     constexpr int kTileBytes = kKeys * 2 * D;
-    static_assert(kNarrowWaves * kTileBytes <= sizeof(lds.k) && kTileBytes >= kNarrowRows * D * 4,
-                  "a tile a wave, and at the end its O in the keys' place");
+    static_assert(kNarrowWaves * kTileBytes <= sizeof(lds.k) && kTileBytes >= 16 * D * 4 && N <= 2,
+                  "a tile a wave, and at the end its O in the place of the keys and, of rows past 16, the values");
     auto& scales = lds.rest.narrow.scales;
     auto& lds_m = lds.rest.narrow.m;
     auto& lds_l = lds.rest.narrow.l;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     int kv;
-    const Tile t = find_tile<false>(a, index, part, kv);
+    const Tile t = find_tile<kRows>(a, index, part, kv);
     if (!t.run) return;
     const int i16 = lane & 15, quarter = lane >> 4;
-    const Place p = row_place(a, t, kv, t.row0 + i16);
-    Few<D> s;
-    load_q(a.q + (int64_t)p.row * D + 8 * quarter, s.q, 32);
-    int all_lo = p.lo, all_hi = p.real ? p.hi : W4_MAX_CONTEXT;
+    Few<D, N> s;
+    int all_lo = 0, all_hi = W4_MAX_CONTEXT;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const Place p = row_place(a, t, kv, t.row0 + 16 * n + i16);
+        load_q(a.q + (int64_t)p.row * D + 8 * quarter, s.q[n], 32);
+        s.lo[n] = p.lo;
+        s.count[n] = p.count;
+        all_lo = max(all_lo, p.lo);
+        all_hi = min(all_hi, p.real ? p.hi : W4_MAX_CONTEXT);
+    }
 #pragma unroll
     for (int off = 8; off > 0; off >>= 1) {
         all_lo = max(all_lo, __shfl_xor(all_lo, off));
@@ -1005,11 +1044,14 @@ __device__ __forceinline__ void attend_narrow(const AttendArgs& a, uint32_t inde
         fetch(wave);
         look_up(wave + kNarrowWaves, entry);
     }
-    wait_q(s.q);
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) s.o[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    s.m = kNegInf;
-    s.l = 0.0f;
+    for (int n = 0; n < N; ++n) {
+        wait_q(s.q[n]);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) s.o[n][i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        s.m[n] = kNegInf;
+        s.l[n] = 0.0f;
+    }
     for (int i = wave; i < tiles; i += kNarrowWaves) {
         const int first = k0 + i * kKeys;
         int later[2];
@@ -1027,28 +1069,30 @@ __device__ __forceinline__ void attend_narrow(const AttendArgs& a, uint32_t inde
             entry[1] = later[1];
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // rows staged by other lanes
-        step_narrow<D, FP8>(s, kt, vt, sc_lane, lane, a.scale_log2, first, p.lo, p.count,
-                            first < all_lo || first + kKeys - 1 > all_hi);
+        step_narrow<D, FP8, N>(s, kt, vt, sc_lane, a.scale_log2, first, first < all_lo || first + kKeys - 1 > all_hi);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // read before the next rows land
     }
 
     // Join the waves: O of wave w counts 2^(m_w - m).
-    float l = s.l + __shfl_xor(s.l, 16);
-    l += __shfl_xor(l, 32);
-    if (lane < 16) {
-        lds_m[wave][lane] = s.m;
-        lds_l[wave][lane] = l;
-    }
-    float* own = reinterpret_cast<float*>(kt);
-    // row r's groups of 4 columns are rotated by r, so that the rows do not share banks
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i)
-        *reinterpret_cast<f32x4_t*>(own + i16 * D + 4 * ((4 * i + quarter + i16) & (D / 4 - 1))) = s.o[i];
+    for (int n = 0; n < N; ++n) {
+        float l = s.l[n] + __shfl_xor(s.l[n], 16);
+        l += __shfl_xor(l, 32);
+        if (lane < 16) {
+            lds_m[wave][16 * n + lane] = s.m[n];
+            lds_l[wave][16 * n + lane] = l;
+        }
+        float* own = reinterpret_cast<float*>(n == 0 ? kt : vt);
+        // row r's groups of 4 columns are rotated by r, so that the rows do not share banks
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+            *reinterpret_cast<f32x4_t*>(own + i16 * D + 4 * ((4 * i + quarter + i16) & (D / 4 - 1))) = s.o[n][i];
+    }
     __syncthreads();
     constexpr int kGroups = D / 4;                           // a thread joins 4 columns of a row
     uint32_t bad_rows = 0;
     const bool whole = t.span.parts == 1;
-    const int rows_here = min(kNarrowRows, t.rows - t.row0);
+    const int rows_here = min(kRows, t.rows - t.row0);
     for (int i = tid; i < rows_here * kGroups; i += kThreads) {
         const int row = i / kGroups, g = i % kGroups;
         float m = kNegInf;
@@ -1060,8 +1104,9 @@ __device__ __forceinline__ void attend_narrow(const AttendArgs& a, uint32_t inde
         for (int w = 0; w < kNarrowWaves; ++w) {
             const float mw = lds_m[w][row];
             const float f = mw == kNegInf ? 0.0f : exp2_fast(mw - m);
-            const f32x4_t ow = *reinterpret_cast<const f32x4_t*>(reinterpret_cast<const float*>(lds.k + w * kTileBytes) +
-                                                                row * D + 4 * ((g + row) & (kGroups - 1)));
+            const uint8_t* from = (N == 1 || row < 16 ? lds.k : lds.v) + w * kTileBytes;
+            const f32x4_t ow = *reinterpret_cast<const f32x4_t*>(reinterpret_cast<const float*>(from) + (row & 15) * D +
+                                                                4 * ((g + (row & 15)) & (kGroups - 1)));
             sum += f * lds_l[w][row];
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] += f * ow[j];
@@ -1099,10 +1144,10 @@ __device__ __forceinline__ void attend_narrow(const AttendArgs& a, uint32_t inde
     __shared__ __attribute__((aligned(16))) typename Lds<(D)>::Rest lds_rest;                        \
     const Lds<(D)> lds = {lds_k, lds_v, lds_rest}
 
-template <int D, bool FP8>
+template <int D, bool FP8, int N>
 __global__ __launch_bounds__(kThreads, 2) void attend_narrow_kernel(AttendArgs a) {
     W4_ATTEND_LDS(D);
-    attend_narrow<D, FP8>(a, blockIdx.x, blockIdx.y, lds);
+    attend_narrow<D, FP8, N>(a, blockIdx.x, blockIdx.y, lds);
 }
 
 // Both kinds of tiles in one launch: the wide ones first, of them those last in their sequence, which
@@ -1118,20 +1163,21 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
     if (first)
         attend_wide<D, FP8>(a, tiles - 1 - (index - part * tiles), part, lds);
     else
-        attend_narrow<D, FP8>(a, index - part * tiles, part, lds);
+        attend_narrow<D, FP8, kFewRows / 16>(a, index - part * tiles, part, lds);
 }
 
 // Joins the parts of the rows that were split: one wave a row, the tiles numbered as in the
 // launch that wrote them.  What the parts left is loaded before it is known how many there are (the
 // launch allows a.*_parts, at most 64), so that the sequence and the parts cost one wait.
-template <int D, bool WIDE>
+template <int D, int R>
 __device__ __forceinline__ void combine_rows(const AttendArgs& a, uint32_t set) {
-    constexpr int E = D / 64, kSets = (WIDE ? kWideRows : kNarrowRows) / 4;
+    constexpr bool WIDE = R == kWideRows;
+    constexpr int E = D / 64, kSets = R / 4;
     const int lane = threadIdx.x & 63;
     const int r = (int)(set % kSets) * 4 + (threadIdx.x >> 6);
     const int most = WIDE ? a.wide_parts : a.narrow_parts;
     const int64_t rows = WIDE ? a.wide_rows : a.narrow_rows;
-    const int64_t row = (int64_t)(set / kSets) * (WIDE ? kWideRows : kNarrowRows) + r;
+    const int64_t row = (int64_t)(set / kSets) * R + r;
     const float* ml = (WIDE ? a.wide_ml : a.narrow_ml) + 2 * row;
     const float* po = (WIDE ? a.wide_o : a.narrow_o) + row * D + lane * E;
     const int mine = min(lane, most - 1);
@@ -1145,7 +1191,7 @@ __device__ __forceinline__ void combine_rows(const AttendArgs& a, uint32_t set) 
     };
     load(0);
     int kv;
-    const Tile t = find_tile<WIDE>(a, set / kSets, 0, kv);
+    const Tile t = find_tile<R>(a, set / kSets, 0, kv);
     if (!t.run || t.span.parts == 1 || t.row0 + r >= t.rows) return;
     const Place place = row_place(a, t, kv, t.row0 + r);
     // lane p weighs part p: 2^(m_p - m) l_p, 0 where the part has nothing of weight
@@ -1183,10 +1229,12 @@ __device__ __forceinline__ void combine_rows(const AttendArgs& a, uint32_t set) 
 template <int D>
 __global__ __launch_bounds__(256) void combine_kernel(AttendArgs a) {
     const uint32_t narrow = (uint32_t)(a.narrow_rows / 4);
-    if (blockIdx.x < narrow)
-        combine_rows<D, false>(a, blockIdx.x);
+    if (blockIdx.x >= narrow)
+        combine_rows<D, kWideRows>(a, blockIdx.x - narrow);
+    else if (a.narrow_tile == 16)
+        combine_rows<D, 16>(a, blockIdx.x);
     else
-        combine_rows<D, true>(a, blockIdx.x - narrow);
+        combine_rows<D, kFewRows>(a, blockIdx.x);
 }
 
 // Parts that a launch allows per tile, to make up to `target` workgroups.  256 is one a compute unit (LDS
@@ -1209,7 +1257,14 @@ void plan_attend(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int64_t 
     const int64_t G = heads / kv_heads;
     // One token a sequence, or too few rows for the wide kernel: no sequence needs it.
     p->both = T != B && T * G > kFewRows;
-    p->narrow_tiles = (p->both ? B * (kFewRows / kNarrowRows) : T * ceil_div(G, kNarrowRows)) * kv_heads;
+    // 32 rows a narrow tile where 16 would read a sequence's keys twice: single tokens of 32 requests over up
+    // to 8192, 32 heads a kv head, take 51.6 us instead of 71.6, four tokens of 32 over 4000 (8 heads) 81.6
+    // instead of 97.0.  Not where the keys could not even give every compute unit a workgroup of 16 rows: one
+    // request over 8000, 2 kv heads, takes 14.8 us with 16 and 16.1 with 32.
+    const int64_t fine = T * ceil_div(G, 16) * kv_heads * ceil_div(capacity, kNarrowLeast);
+    p->narrow_tile = p->both || (G > 16 && fine > 256) ? kFewRows : 16;
+    const int64_t R = p->narrow_tile;
+    p->narrow_tiles = (p->both ? B : T == B ? T * ceil_div(G, R) : tile_bound(T, B, G, R)) * kv_heads;
     p->narrow_parts = parts_for(p->narrow_tiles, 256, capacity, kNarrowLeast);
     p->wide_tiles = p->both ? tile_bound(T, B, G, kWideRows) * kv_heads : 0;
     p->wide_fill = p->both ? parts_for(p->wide_tiles, 256, capacity, kWideLeast) : 1;
@@ -1219,7 +1274,7 @@ void plan_attend(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int64_t 
 
 static int64_t split_rows(bool wide, const AttendPlan& p) {
     const int64_t tiles = wide ? p.wide_tiles : p.narrow_tiles;
-    return (wide ? p.wide_parts : p.narrow_parts) > 1 ? tiles * (wide ? kWideRows : kNarrowRows) : 0;
+    return (wide ? p.wide_parts : p.narrow_parts) > 1 ? tiles * (wide ? kWideRows : p.narrow_tile) : 0;
 }
 
 size_t attend_workspace(int64_t D, const AttendPlan& p) {
@@ -1232,9 +1287,13 @@ static hipError_t launch_attend_d(const AttendArgs& a, const AttendPlan& p, hipS
         // a dimension of a grid holds less than 2^32 threads
         const int64_t n = p.wide_tiles * p.wide_parts + p.narrow_tiles * p.narrow_parts, x = imin(n, 1 << 22);
         hipLaunchKernelGGL((attend_kernel<D, FP8>), dim3((unsigned)x, (unsigned)ceil_div(n, x)), dim3(kThreads), 0, s, a);
-    } else
-        hipLaunchKernelGGL((attend_narrow_kernel<D, FP8>), dim3((unsigned)p.narrow_tiles, (unsigned)p.narrow_parts),
-                           dim3(kThreads), 0, s, a);
+    } else {
+        const dim3 grid((unsigned)p.narrow_tiles, (unsigned)p.narrow_parts), block(kThreads);
+        if (p.narrow_tile == 16)
+            hipLaunchKernelGGL((attend_narrow_kernel<D, FP8, 1>), grid, block, 0, s, a);
+        else
+            hipLaunchKernelGGL((attend_narrow_kernel<D, FP8, kFewRows / 16>), grid, block, 0, s, a);
+    }
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && a.wide_rows + a.narrow_rows > 0) {
         hipLaunchKernelGGL(combine_kernel<D>, dim3((unsigned)((a.wide_rows + a.narrow_rows) / 4)), dim3(256), 0, s, a);
@@ -1245,6 +1304,7 @@ static hipError_t launch_attend_d(const AttendArgs& a, const AttendPlan& p, hipS
 
 hipError_t launch_attend(AttendArgs a, int head_dim, bool fp8, const AttendPlan& p, void* workspace, hipStream_t s) {
     a.both = p.both;
+    a.narrow_tile = p.narrow_tile;
     a.narrow_tiles = (int)p.narrow_tiles;
     a.wide_tiles = (int)p.wide_tiles;
     a.narrow_parts = p.narrow_parts;

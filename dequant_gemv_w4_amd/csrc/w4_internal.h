@@ -184,7 +184,7 @@ struct TableArgs {
 hipError_t launch_block_tables(const TableArgs& a, hipStream_t s);
 
 // Attention: query rows of a tile in the two kernels, keys a part takes at least, parts at most.
-constexpr int kNarrowRows = 16, kFewRows = 32, kWideRows = 256;
+constexpr int kFewRows = 32, kWideRows = 256;   // narrow: 16 or kFewRows
 constexpr int kNarrowLeast = 256, kWideLeast = 128, kWideEven = 4096, kMaxParts = 64;
 
 struct AttendArgs {
@@ -205,13 +205,14 @@ struct AttendArgs {
     int T, capacity;     // capacity: keys that a row of the table reaches
     int B, heads, kv_heads, group, page_shift, window;
     float scale_log2;    // softmax scale / ln 2
-    int narrow_tiles, wide_tiles, narrow_parts, wide_parts, wide_fill;
+    int narrow_tile, narrow_tiles, wide_tiles, narrow_parts, wide_parts, wide_fill;
     bool both;           // both kinds of tiles are launched
 };
 // What the host knows of a call decides the launches; the parts that a tile really has follow
 // from the lengths on the device.
 struct AttendPlan {
     int64_t narrow_tiles, wide_tiles;   // workgroups of one part
+    int narrow_tile;                    // rows of a narrow tile: 16 or kFewRows
     int narrow_parts, wide_parts, wide_fill;
     bool both;
 };

@@ -521,6 +521,11 @@ ATTEND = [  # new, cached, heads, kv, d, page, fp8, window
     ([1, 3, 40], [6000, 5000, 9], 16, 2, 128, 16, False, 0),  # 8, 24 and 320 rows, the few split over the keys
     ([2, 1, 50], [4000, 3, 9], 17, 1, 64, 16, True, 0),       # 34, 17 and 850 rows
     ([3], [700], 8, 1, 128, 16, False, 0),                    # few rows in all: 24, 16 and 32
+    ([1] * 9, [7000, 1, 300, 0, 31, 5000, 63, 64, 90], 32, 1, 128, 16, False, 0),   # 32 rows a tile
+    ([1] * 6, [3000, 9, 4000, 77, 512, 513], 50, 2, 64, 16, True, 0),
+    ([2, 1, 0, 1], [2000, 700, 60, 31], 20, 1, 128, 16, True, 50),
+    ([1] * 4, [6000, 200, 0, 900], 33, 1, 128, 64, False, 0),
+    ([0, 1, 0], [5, 70000, 3], 20, 1, 64, 64, False, 0),      # one token of three requests
     ([2, 0, 2], [30, 4, 2000], 8, 2, 64, 16, True, 0),
     ([31, 1], [3, 5000], 4, 4, 128, 32, False, 40),
     ([300, 1300], [4500, 100], 32, 8, 64, 64, False, 0),      # split and unsplit tiles in one call
