@@ -645,6 +645,28 @@ def test_attention_bad_pages_read_as_zeros():
         b.d_table = _dev(keep)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_attention_of_32_row_tiles_redone(fp8):
+    # 24 rows of one request beside a chunk: a NaN that only its later tokens see, then pages that are not there
+    new, cached = [12, 40], [900, 10]
+    b = Batch(new, cached, 4, 2, 128, 16, fp8, seed=23)
+    clean = to_np32(b.run())
+    b.check(b.run(), 0, "clean")
+    c = Batch(new, cached, 4, 2, 128, 16, fp8, seed=23)
+    j = c.ctx[0] - 8
+    c.cache.v[int(c.table[0, j // 16]), :, j % 16, 5] = 0x7F if fp8 else float("nan")
+    got = to_np32(c.run())
+    assert np.all(np.abs(got[:4] - clean[:4]) <= 4 * UB * np.abs(clean[:4]) + 0.02)
+    assert np.isnan(got[4:12, :, 5]).all() and np.isfinite(got[4:12, :, :5]).all()
+    assert np.array_equal(got[12:], clean[12:])
+    for entry, value in ((3, -1), (40, b.cache.pages)):
+        b.table[0, entry] = value
+        for x in (b.keys[0], b.values[0]):
+            x[:, entry * 16: entry * 16 + 16] = 0.0
+    b.d_table = _dev(b.table)
+    b.check(b.run(), 0, "bad pages", status=8)
+
+
 @pytest.mark.parametrize("new,cached", [([1] * 3, [3000, 40, 900]), ([70, 1, 4], [2000, 300, 5])])
 def test_attention_graph_and_streams(new, cached):
     b = Batch(new, cached, 16, 2, 128, 16, False, seed=8)
