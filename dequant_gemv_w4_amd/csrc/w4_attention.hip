@@ -894,8 +894,8 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, uint32_t index,
         const int n = i + behind;
         look_up(n + kAhead + 1);
         if (seen(i))
-            weights<D, FP8>(s, z, pw, sc_lane + 4 * S * kKeyTile, sc_lane + 4 * (kWideStages + S) * kKeyTile, a.scale_log2, k0 + i * kKeyTile, p.lo,
-                               p.count, i < whole_lo || i > whole_hi);
+            weights<D, FP8>(s, z, pw, sc_lane + 4 * S * kKeyTile, sc_lane + 4 * (kWideStages + S) * kKeyTile, a.scale_log2,
+                            k0 + i * kKeyTile, p.lo, p.count, i < whole_lo || i > whole_hi);
         if (n >= 1 && n < tiles) {
             if constexpr (FP8) {
                 put(n, true);
@@ -913,12 +913,8 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, uint32_t index,
         }
         meet();
         __builtin_amdgcn_s_setprio(1);
-        if (seen(i)) {
-            accumulate<D>(s, vt[S], pw);
-        }
-        if (seen(i + 1)) {
-            scores<D>(s, kt[(S + 1) % kWideStages], z);
-        }
+        if (seen(i)) accumulate<D>(s, vt[S], pw);
+        if (seen(i + 1)) scores<D>(s, kt[(S + 1) % kWideStages], z);
         __builtin_amdgcn_s_setprio(0);
         meet();
     };
