@@ -709,7 +709,8 @@ size_t w4_paged_attention_workspace_bytes(int64_t T, int64_t heads, const w4_kv_
         check_batch(B, max_pages, cache->page_size) != W4_OK)
         return 0;
     w4::AttendPlan plan;
-    w4::plan_attend(T, B, heads, cache->kv_heads, max_pages << shift, &plan);
+    w4::plan_attend(T, B, heads, cache->kv_heads, max_pages << shift,
+                    cache->type == W4_CACHE_FP8, &plan);
     return w4::attend_workspace(cache->head_dim, plan);
 }
 
@@ -727,7 +728,8 @@ w4_status w4_paged_attention(const void* q, int64_t T, int64_t heads, const w4_k
     if (st != W4_OK) return st;
     if (!(scale > 0.0f) || !std::isfinite(scale) || window < 0) return W4_ERR_VALUE;
     w4::AttendPlan plan;
-    w4::plan_attend(T, B, heads, cache->kv_heads, max_pages << shift, &plan);
+    w4::plan_attend(T, B, heads, cache->kv_heads, max_pages << shift,
+                    cache->type == W4_CACHE_FP8, &plan);
     const size_t need = w4::attend_workspace(cache->head_dim, plan);
     if (need > 0 && (!workspace || workspace_bytes < need)) return W4_ERR_WORKSPACE;
     if (!aligned(q, 16) || !aligned(o, 16) || !aligned(block_table, 4) || !aligned(cu_q, 4) ||

@@ -525,8 +525,8 @@ struct Tile {
 };
 
 // Tile number `index` of R rows: of attend_wide's (R = kWideRows) or attend_narrow's.  Where both are
-// launched, a sequence of at most kFewRows rows is the narrow kernel's, as its only tile; alone that has,
-// for as many tokens as sequences, the tiles that G rows fill for each token.
+// launched, a sequence of at most few_tiles (1 or 2) * kFewRows rows is the narrow kernel's, as so many
+// tiles; alone that has, for as many tokens as sequences, the tiles that G rows fill for each token.
 template <int R>
 __device__ __forceinline__ Tile find_tile(const AttendArgs& a, uint32_t index, int part, int& kv) {
     constexpr bool WIDE = R == kWideRows;
@@ -536,8 +536,11 @@ __device__ __forceinline__ Tile find_tile(const AttendArgs& a, uint32_t index, i
     kv = (int)index - tile * a.kv_heads;
     t.part_row = (int64_t)index * R;
     if (!WIDE && a.both) {
-        t.b = tile;
-        t.row0 = 0;
+        // all first tiles, then all second ones, which mostly have no rows: taking turns, they would leave
+        // every other place that the workgroups go to in turn without work (31 single tokens over 4000
+        // beside a chunk: 143 us instead of 113)
+        t.b = tile < a.B ? tile : tile - a.B;
+        t.row0 = tile < a.B ? 0 : R;
         t.seq = load_seq(a, t.b);
     } else {
         const int per = (G + R - 1) / R;                     // tiles a token
@@ -547,11 +550,11 @@ __device__ __forceinline__ Tile find_tile(const AttendArgs& a, uint32_t index, i
         t.row0 = (tile - first(t.seq.start, t.b)) * R;
     }
     t.rows = t.seq.n * G;
-    const bool few = t.rows <= kFewRows;
+    const bool few = t.rows <= a.few_tiles * kFewRows;
     t.run = t.row0 >= 0 && t.row0 < t.rows && (WIDE ? !few : few || !a.both);
     if (!t.run) return t;
     const int reach = a.window > 0 ? min(t.seq.ctx, a.window) : t.seq.ctx;
-    const int parts = !WIDE ? a.narrow_parts : reach < kWideEven ? a.wide_fill : a.wide_parts;
+    const int parts = !WIDE ? (a.both && t.rows > R ? a.narrow_fill : a.narrow_parts) : reach < kWideEven ? a.wide_fill : a.wide_parts;
     t.span = key_span(t.seq, t.row0, min(R, t.rows - t.row0), G, a.window, parts, WIDE ? kWideLeast : kNarrowLeast);
     t.run = part < t.span.parts;
     if (!t.run) return t;
@@ -1249,10 +1252,15 @@ int parts_for(int64_t tiles, int64_t target, int64_t longest, int64_t least) {
 
 }  // namespace
 
-void plan_attend(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int64_t capacity, AttendPlan* p) {
+void plan_attend(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int64_t capacity, bool fp8, AttendPlan* p) {
     const int64_t G = heads / kv_heads;
     // One token a sequence, or too few rows for the wide kernel: no sequence needs it.
     p->both = T != B && T * G > kFewRows;
+    // Sequences of 33 to 64 rows as two narrow tiles: a wide one would have no rows for most of its waves.
+    // 16 requests of up to 8 tokens (8 heads a kv head) over up to 4000 take 69 us so, 91 with wide tiles, 8 over
+    // an E4M3 cache 38 and 55, 32 78 and 113.  Of a bfloat16 cache the keys come from memory twice where the
+    // second tiles have to wait for a compute unit: 32 requests 113 and 95.
+    p->few_tiles = fp8 || 2 * B * kv_heads <= 256 ? 2 : 1;
     // 32 rows a narrow tile where 16 would read a sequence's keys twice: single tokens of 32 requests over up
     // to 8192, 32 heads a kv head, take 51.6 us instead of 71.6, four tokens of 32 over 4000 (8 heads) 81.6
     // instead of 97.0.  Not where the keys could not even give every compute unit a workgroup of 16 rows: one
@@ -1260,8 +1268,10 @@ void plan_attend(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int64_t 
     const int64_t fine = T * ceil_div(G, 16) * kv_heads * ceil_div(capacity, kNarrowLeast);
     p->narrow_tile = p->both || (G > 16 && fine > 256) ? kFewRows : 16;
     const int64_t R = p->narrow_tile;
-    p->narrow_tiles = (p->both ? B : T == B ? T * ceil_div(G, R) : tile_bound(T, B, G, R)) * kv_heads;
-    p->narrow_parts = parts_for(p->narrow_tiles, 256, capacity, kNarrowLeast);
+    p->narrow_tiles = (p->both ? B * p->few_tiles : T == B ? T * ceil_div(G, R) : tile_bound(T, B, G, R)) * kv_heads;
+    // beside wide tiles most sequences have one narrow tile, which may then take the parts of the idle ones
+    p->narrow_fill = parts_for(p->narrow_tiles, 256, capacity, kNarrowLeast);
+    p->narrow_parts = p->both ? parts_for(B * kv_heads, 256, capacity, kNarrowLeast) : p->narrow_fill;
     p->wide_tiles = p->both ? tile_bound(T, B, G, kWideRows) * kv_heads : 0;
     p->wide_fill = p->both ? parts_for(p->wide_tiles, 256, capacity, kWideLeast) : 1;
     p->wide_parts = p->both && capacity >= kWideEven
@@ -1301,11 +1311,13 @@ static hipError_t launch_attend_d(const AttendArgs& a, const AttendPlan& p, hipS
 hipError_t launch_attend(AttendArgs a, int head_dim, bool fp8, const AttendPlan& p, void* workspace, hipStream_t s) {
     a.both = p.both;
     a.narrow_tile = p.narrow_tile;
+    a.few_tiles = p.few_tiles;
     a.narrow_tiles = (int)p.narrow_tiles;
     a.wide_tiles = (int)p.wide_tiles;
     a.narrow_parts = p.narrow_parts;
     a.wide_parts = p.wide_parts;
     a.wide_fill = p.wide_fill;
+    a.narrow_fill = p.narrow_fill;
     a.narrow_rows = split_rows(false, p);
     a.wide_rows = split_rows(true, p);
     a.narrow_o = static_cast<float*>(workspace);

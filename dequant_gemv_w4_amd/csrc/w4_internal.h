@@ -205,7 +205,7 @@ struct AttendArgs {
     int T, capacity;     // capacity: keys that a row of the table reaches
     int B, heads, kv_heads, group, page_shift, window;
     float scale_log2;    // softmax scale / ln 2
-    int narrow_tile, narrow_tiles, wide_tiles, narrow_parts, wide_parts, wide_fill;
+    int narrow_tile, few_tiles, narrow_tiles, wide_tiles, narrow_parts, narrow_fill, wide_parts, wide_fill;
     bool both;           // both kinds of tiles are launched
 };
 // What the host knows of a call decides the launches; the parts that a tile really has follow
@@ -213,10 +213,12 @@ struct AttendArgs {
 struct AttendPlan {
     int64_t narrow_tiles, wide_tiles;   // workgroups of one part
     int narrow_tile;                    // rows of a narrow tile: 16 or kFewRows
-    int narrow_parts, wide_parts, wide_fill;
+    int few_tiles;                      // narrow tiles of a sequence that has no wide ones, beside wide ones
+    int narrow_parts, narrow_fill, wide_parts, wide_fill;
     bool both;
 };
-void plan_attend(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int64_t capacity, AttendPlan* p);
+void plan_attend(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int64_t capacity, bool fp8,
+                 AttendPlan* p);
 size_t attend_workspace(int64_t D, const AttendPlan& p);
 hipError_t launch_attend(AttendArgs a, int head_dim, bool fp8, const AttendPlan& p, void* workspace,
                          hipStream_t s);

@@ -498,8 +498,9 @@ w4_status w4_block_tables(const int32_t* new_lens, const int32_t* lens_in, int64
  * in d_status (optional).  What lies in the cache behind a request's keys, and at keys that a
  * row does not see, does not reach the row, NaN and infinities included.
  * Scores, softmax sums and outputs are formed in binary32 and o is rounded once; requests with at
- * most 32 rows (tokens times query heads of a kv head), or all where T = B, multiply V by weights
- * held in two bfloat16 parts (2^-16), longer chunks by weights rounded to bfloat16.
+ * most 32 rows (tokens times query heads of a kv head), in small batches 64, or all where T = B,
+ * multiply V by weights held in two bfloat16 parts (2^-16), longer chunks by weights rounded to
+ * bfloat16.
  * Deterministic; the split of the work depends on the arguments and lengths only.
  * Requires 1 <= T <= W4_MAX_TOKENS, 1 <= B <= W4_MAX_SEQUENCES, heads a multiple of kv_heads, at
  * most 65536, T * heads < 2^26, 1 <= max_pages, max_pages * page_size <= W4_MAX_CONTEXT.

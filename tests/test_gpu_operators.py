@@ -526,6 +526,8 @@ ATTEND = [  # new, cached, heads, kv, d, page, fp8, window
     ([2, 1, 0, 1], [2000, 700, 60, 31], 20, 1, 128, 16, True, 50),
     ([1] * 4, [6000, 200, 0, 900], 33, 1, 128, 64, False, 0),
     ([0, 1, 0], [5, 70000, 3], 20, 1, 64, 64, False, 0),      # one token of three requests
+    ([6, 1, 8, 30, 5], [3000, 900, 40, 7, 1000], 16, 2, 128, 16, False, 0),   # 48, 8, 64, 240 and 40 rows
+    ([9, 0, 1, 60, 7], [2500, 9, 4000, 300, 31], 7, 1, 64, 32, True, 200),    # 63, 0, 7, 420 and 49 rows
     ([2, 0, 2], [30, 4, 2000], 8, 2, 64, 16, True, 0),
     ([31, 1], [3, 5000], 4, 4, 128, 32, False, 40),
     ([300, 1300], [4500, 100], 32, 8, 64, 64, False, 0),      # split and unsplit tiles in one call
