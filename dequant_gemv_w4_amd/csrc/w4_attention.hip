@@ -555,7 +555,7 @@ __device__ __forceinline__ Tile find_tile(const AttendArgs& a, uint32_t index, i
     if (!t.run) return t;
     const int reach = a.window > 0 ? min(t.seq.ctx, a.window) : t.seq.ctx;
     const int parts = !WIDE ? (a.both && t.rows > R ? a.narrow_fill : a.narrow_parts) : reach < kWideEven ? a.wide_fill : a.wide_parts;
-    t.span = key_span(t.seq, t.row0, min(R, t.rows - t.row0), G, a.window, parts, WIDE ? kWideLeast : kNarrowLeast);
+    t.span = seen_span(key_span(t.seq, t.row0, min(R, t.rows - t.row0), G, a.window, parts, WIDE ? kWideLeast : kNarrowLeast));
     t.run = part < t.span.parts;
     if (!t.run) return t;
     t.k0 = t.span.begin + part * t.span.chunk;
@@ -1011,7 +1011,7 @@ __device__ __forceinline__ void attend_narrow(const AttendArgs& a, uint32_t inde
     uint8_t* vt = lds.v + wave * kTileBytes;
     const int crow = lane / kChunks, chunk = lane % kChunks;
     const uint32_t lane_byte = (crow & 15) * kRowBytes + 16 * chunk;
-    // A page holds 16 keys at least and tiles begin at multiples of 32, so either half of a tile
+    // A page holds 16 keys at least and tiles begin at multiples of 16, so either half of a tile
     // lies in one page: two lookups a tile, the same for all lanes.
     Rows16<kRowBytes> rows(a, __builtin_amdgcn_readfirstlane(t.b), __builtin_amdgcn_readfirstlane(kv), k1);
     int entry[2];                                            // table entries of the next tile

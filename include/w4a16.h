@@ -494,9 +494,11 @@ w4_status w4_block_tables(const int32_t* new_lens, const int32_t* lens_in, int64
  *   workspace    w4_paged_attention_workspace_bytes(...) bytes of device scratch (may be 0),
  *                16-B aligned; contents need no initialisation.  Calls (and captured graphs)
  *                sharing a workspace must be ordered.
- * A key in a page that the cache does not have reads as zeros (K and V) and sets W4_STATUS_PAGE
- * in d_status (optional).  What lies in the cache behind a request's keys, and at keys that a
- * row does not see, does not reach the row, NaN and infinities included.
+ * A key that a row sees in a page that the cache does not have reads as zeros (K and V) and sets
+ * W4_STATUS_PAGE in d_status (optional).  Table entries of pages that lie wholly before every row's
+ * window, or behind a request's keys, are not looked at: such pages may have been given back.
+ * What lies in the cache behind a request's keys, and at keys that a row does not see, does not
+ * reach the row, NaN and infinities included.
  * Scores, softmax sums and outputs are formed in binary32 and o is rounded once; requests with at
  * most 32 rows (tokens times query heads of a kv head), in small batches 64, or all where T = B,
  * multiply V by weights held in two bfloat16 parts (2^-16), longer chunks by weights rounded to
