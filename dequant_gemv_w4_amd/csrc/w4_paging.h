@@ -100,8 +100,8 @@ W4_HD Span seen_span(Span k) {
 // Number of a page if the cache has it, else -1.
 W4_HD int64_t checked_page(int64_t page, int64_t pages) { return page >= 0 && page < pages ? page : -1; }
 
-// Pages that a request takes for its new tokens: the list has `count` pages left, `before` of
-// them are taken by the requests ahead of it (those that were served or would have been).
+// Pages that a request with `len` cached tokens takes for `fresh` new ones, if its lengths are valid
+// and its table of max_pages entries is wide enough.
 struct Need {
     int64_t have;    // pages of the cached tokens
     int64_t take;    // pages more

@@ -465,7 +465,7 @@ w4_status w4_rope_cache(const void* qkv, w4_dtype xt, int64_t T, int64_t heads,
  * A request whose length is negative or whose tokens do not end within T (W4_STATUS_LENGTH), or
  * whose pages do not fit its table row, or are not there once the requests ahead of it are
  * served (W4_STATUS_PAGES_SHORT), is left as it is: it takes no page, its length stays and its
- * tokens get position 0 and slot -1; cu_q still counts them.  A negative new length counts as
+ * tokens get position 0 and slot -1; cu_q still counts them, the requests behind it are served.  A negative new length counts as
  * none, a taken page with a negative number gives slot -1.
  * Requires 1 <= B <= W4_MAX_SEQUENCES, 1 <= T <= W4_MAX_TOKENS, page_size as in w4_kv_cache,
  * max_pages * page_size <= W4_MAX_CONTEXT, free_capacity >= 0; int32 arrays 4-B aligned, slots

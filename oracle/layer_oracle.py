@@ -82,7 +82,7 @@ def block_tables_ref(new_lens, lens, free_pages, free_count, table, page, tokens
     table = [list(map(int, row)) for row in table]
     count = min(max(int(free_count), 0), len(free_pages))
     positions, slots = [0] * tokens, [-1] * tokens
-    cu, out, status, asked, taken = [0], [], 0, 0, 0
+    cu, out, status, taken = [0], [], 0, 0
     for b, (n, have) in enumerate(zip(map(int, new_lens), map(int, lens))):
         start = cu[-1]
         cu.append(start + max(n, 0))
@@ -95,17 +95,15 @@ def block_tables_ref(new_lens, lens, free_pages, free_count, table, page, tokens
         if own + need > len(table[b]):
             status |= 16 if start + n > tokens else 32
             continue
-        asked += need
         if start + n > tokens:
             status |= 16
             continue
-        if need and asked > count:
+        if need and taken + need > count:
             status |= 32
             continue
         for i in range(need):
-            table[b][own + i] = int(free_pages[count - 1 - (asked - need) - i])
-        if need:
-            taken = asked
+            table[b][own + i] = int(free_pages[count - 1 - taken - i])
+        taken += need
         for i in range(n):
             p = have + i
             positions[start + i] = p
