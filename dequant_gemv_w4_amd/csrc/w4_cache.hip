@@ -112,7 +112,8 @@ __global__ __launch_bounds__(kRopeThreads) void rope_cache_kernel(RopeArgs a) {
         for (int d = lanes >> 1; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor(amax, d));
         const double s = amax == 0.0f ? 1.0 : (double)amax / kFp8Max;
         const float rs = (float)(1.0 / s);
-        const bool ok = s >= 0x1p-100 && s <= 0x1p100;
+        // values that are not finite take the quotients, so that their bytes are the row quantizers' too
+        const bool ok = s >= 0x1p-100 && s <= 0x1p100 && off == 0.0f;
         if (u == 0) (is_v ? a.v_scales : a.k_scales)[row] = (float)s;
         uint8_t* dst = static_cast<uint8_t*>(is_v ? a.v : a.k) + row * D;
         *reinterpret_cast<uint2*>(dst + c0) = w8_codes8_of<false>(v, s, rs, ok);

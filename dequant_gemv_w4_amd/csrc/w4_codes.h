@@ -121,7 +121,7 @@ __device__ __forceinline__ uint2 w8_codes8(const float* v, double s, float rs, b
 }
 
 // The same codes for the kernels that have 8 values of a row in registers, with one branch for
-// all of them.  E4M3: t = v * r32 is within 2^-23 relative of v / s, and rounding is monotonic,
+// all of them; rcp_ok has to be false where one of them is not finite.  E4M3: t = v * r32 is within 2^-23 relative of v / s, and rounding is monotonic,
 // so where t (1 - 2^-21) and t (1 + 2^-21) have the same byte it is the byte of v / s; about one
 // value in 10^5 differs and sends the 8 to the binary64 quotients.  The conversion instruction
 // rounds halves to even, subnormals included, and keeps the sign of a value that rounds to zero;

@@ -123,7 +123,8 @@ __device__ __forceinline__ void write_row(const RowOut& o, int64_t row, int64_t 
     const double s = amax == 0.0f ? 1.0 : (double)amax / (int8 ? 127.0 : kFp8Max);
     if (threadIdx.x == 0) o.scales[row] = (float)s;
     const float rs = (float)(1.0 / s);
-    const bool ok = s >= 0x1p-100 && s <= 0x1p100;
+    // values that are not finite take the quotients, so that their bytes are the row quantizers' too
+    const bool ok = s >= 0x1p-100 && s <= 0x1p100 && off == 0.0f;
     uint8_t* dst = static_cast<uint8_t*>(o.y) + row * K + first;
 #pragma unroll
     for (int c = 0; c < C; ++c) {

@@ -344,7 +344,8 @@ w4_status w4_int8_gemm(const int8_t* xq, const float* sx, int64_t M, const int8_
  *   y             [rows, K] binary32 or bfloat16.
  * w4_rmsnorm_fp8, w4_rmsnorm_int8 -- the same y, quantized per row without being stored: codes
  *   [rows, K] and scales [rows] as w4_fp8_quantize_rows / w4_int8_quantize_rows write them for
- *   the binary32 y, bit for bit; d_status (optional) receives W4_STATUS_NONFINITE.
+ *   the binary32 y, bit for bit; d_status (optional) receives W4_STATUS_NONFINITE where a row
+ *   holds a value that is not finite (the row's codes say nothing then; 0x7F is not among them).
  * Requires rows >= 1, K a multiple of 128, 128 <= K <= W4_ROWS_MAX_K, eps finite and > 0
  * (W4_ERR_VALUE).  All arrays 16-B aligned (scales, d_status 4-B); outputs must not overlap
  * inputs except residual_out as stated.  Deterministic.
