@@ -589,8 +589,13 @@ w4_status w4_rope_frequencies(const w4_rope* rope, double* freqs, double* amplit
             return half * std::log((double)rope->original_positions / (two_pi * turns)) /
                    std::log(rope->base);
         };
-        first = std::fmax(0.0, std::floor(pair_of(rope->high)));
-        last = std::fmin(2.0 * half - 1.0, std::ceil(pair_of(rope->low)));
+        first = std::floor(pair_of(rope->high));
+        last = std::ceil(pair_of(rope->low));
+        // a ramp that ends ahead of the first pair or begins behind the last place stays there
+        if (last >= 0.0 && first <= 2.0 * half - 1.0) {
+            first = std::fmax(0.0, first);
+            last = std::fmin(2.0 * half - 1.0, last);
+        }
         if (first == last) last += 0.001;
     }
     for (int i = 0; i < half; ++i) {

@@ -410,8 +410,9 @@ typedef struct {
  *   W4_ROPE_RAMP    f * (1 - r + r / factor), r rising from 0 to 1 between the pairs
  *                   floor(c(high)) (at least 0) and ceil(c(low)) (at most rotary_dim - 1;
  *                   0.001 more if both are the same), c(t) = rotary_dim *
- *                   ln(original_positions / (2 pi t)) / (2 ln base); cosines and sines are
- *                   multiplied by the amplitude 1 + 0.1 ln(factor).
+ *                   ln(original_positions / (2 pi t)) / (2 ln base); r is 1 for all pairs where
+ *                   ceil(c(low)) < 0 and 0 where floor(c(high)) > rotary_dim - 1; cosines and
+ *                   sines are multiplied by the amplitude 1 + 0.1 ln(factor).
  *   rotary_dim   elements of a head that turn: a multiple of 16 (the rest stays as it is).
  *   interleaved  0: pairs (i, i + rotary_dim / 2); 1: pairs (2i, 2i + 1).
  * Requires base > 1, factor >= 1 (but for NONE), and for BANDS and RAMP 0 < low < high and

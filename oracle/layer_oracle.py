@@ -56,10 +56,14 @@ def rope_frequencies_ref(rotary_dim, base, scaling="none", factor=1.0, low=1.0, 
         elif scaling == "ramp":
             def dim(turns):
                 return rotary_dim * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))
-            a, b = max(math.floor(dim(high)), 0), min(math.ceil(dim(low)), rotary_dim - 1)
-            if a == b:
-                b += 0.001
-            r = min(max((i - a) / (b - a), 0.0), 1.0)
+            a, b = math.floor(dim(high)), math.ceil(dim(low))
+            if b < 0:
+                r = 1.0                                      # the ramp ends ahead of every pair
+            elif a > rotary_dim - 1:
+                r = 0.0                                      # begins behind every pair
+            else:
+                a, b = max(a, 0), min(b, rotary_dim - 1)
+                r = min(max((i - a) / (b - a if b > a else 0.001), 0.0), 1.0)
             f = f / factor * r + f * (1 - r)
         out.append(f)
     return np.array(out), 1.0 + 0.1 * math.log(factor) if scaling == "ramp" else 1.0
