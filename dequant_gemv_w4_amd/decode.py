@@ -127,8 +127,10 @@ class DecoderStep:
     ``residual`` [tokens, hidden] and their number per request into ``new_lens`` [seqs]; the step places
     them in pages (``lens``, ``free_pages``, ``free_count`` and ``block_table`` go on from step to step,
     problems are reported in ``status``) and leaves the normed last hidden states in ``hidden``.
-    Rows past the new tokens are padding.  4-bit products run on w4_gemv up to 16 tokens and on
-    w4_gemm beyond; rows for 8-bit products are quantized by the operator that computes them.
+    Rows past the new tokens are padding; like the rows of requests that could not be served they are
+    zeroed first (three small launches a step), so that nothing an earlier step left in them reaches the
+    status.  4-bit products run on w4_gemv up to 16 tokens and on w4_gemm beyond; rows for 8-bit
+    products are quantized by the operator that computes them.
     A step of another size over the same requests (a captured one for single tokens beside one for
     prompts) is made with ``state``, the step whose lengths, pages, table and status it shares.
     """
@@ -170,7 +172,9 @@ class DecoderStep:
         self.slots = torch.zeros(tokens, dtype=torch.int64, device=dev)
         self._x, self._y = torch.zeros(tokens, hidden, **bf16), torch.zeros(tokens, hidden, **bf16)
         self._qkv = torch.zeros(tokens, width, **bf16)
-        self._q, self._o = (torch.zeros(tokens, heads, c.head_dim, **bf16) for _ in range(2))
+        self._qo = torch.zeros(2, tokens, heads, c.head_dim, **bf16)
+        self._q, self._o = self._qo
+        self._idle = torch.zeros(tokens, 1, dtype=torch.bool, device=dev)
         self._gate_up = {f: torch.zeros(tokens, 2 * f, **bf16) for f in {a.down.k for a in layers}}
         self._act = {f: torch.zeros(tokens, f, **bf16) for f in self._gate_up}
         products = [p for a in layers for p in (a.qkv, a.o, a.gate_up, a.down)]
@@ -220,9 +224,14 @@ class DecoderStep:
         return call(x, codes=codes, scales=scales, status=self.status)
 
     def run_eager(self) -> None:
+        import torch
         from . import w4_block_tables, w4_paged_attention, w4_rmsnorm, w4_rope_cache
         w4_block_tables(self.new_lens, self.lens, self.free_pages, self.free_count, self.block_table, self.page_size,
                         cu_q=self.cu_q, positions=self.positions, slots=self.slots, status=self.status)
+        # Rows without a slot: the cache write and the attention leave them out, the products and norms do not.
+        torch.lt(self.slots.view(-1, 1), 0, out=self._idle)
+        self.residual.masked_fill_(self._idle, 0)
+        self._qo.masked_fill_(self._idle.view(-1, 1, 1), 0)
         for i, (a, cache) in enumerate(zip(self.layers, self.caches)):
             if i == 0:
                 x = self._norm(a.qkv, self.residual, a.attn_norm, None)

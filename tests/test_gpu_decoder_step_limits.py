@@ -1,0 +1,45 @@
+"""DecoderStep at its edges: rows that become padding after they held a value that is not finite, and
+requests that are refused."""
+
+import pytest
+import torch
+
+import dequant_gemv_w4_amd as w4
+from dequant_gemv_w4_amd.decode import DecoderStep
+from test_gpu_decoder_step import D, DEV, EPS, HEADS, HIDDEN, KV, Model
+
+pytestmark = pytest.mark.gpu
+
+
+def _put(s, new, rows):
+    s.new_lens.copy_(torch.tensor(new, dtype=torch.int32))
+    s.residual[: len(rows)] = rows
+
+
+@pytest.mark.parametrize("kind", ["fp8", "int8", "w4"])
+@pytest.mark.parametrize("fp8_cache", [False, True])
+@pytest.mark.parametrize("capture", [False, True])
+def test_rows_that_become_padding(kind, fp8_cache, capture):
+    m = Model((kind,) * 4, fp8_cache, 16, False, seed=12)
+    caches = [w4.W4KVCache.empty(12, 16, KV, D, fp8=fp8_cache, device=DEV) for _ in m.layers]
+    s = DecoderStep(m.layers, caches, HEADS, m.spec, m.final_dev, 6, 4, 4, EPS)
+    rows = torch.randn(6, HIDDEN, generator=torch.Generator().manual_seed(2)).to(DEV).to(torch.bfloat16)
+    if capture:
+        s.capture()
+    bad = rows.clone()
+    bad[3:] = float("nan")                                    # request 3's three tokens
+    _put(s, [1, 1, 1, 3], bad)
+    s.run()
+    torch.cuda.synchronize()
+    assert bool(torch.isfinite(s.hidden[:3].float()).all()) and not bool(torch.isfinite(s.hidden[3:].float()).any())
+    assert int(s.status) == (0 if kind == "w4" and not fp8_cache else 1)
+    s.status.zero_()
+    _put(s, [1, 1, 1, 0], rows[:3])                           # the rows behind are padding now
+    s.run()
+    torch.cuda.synchronize()
+    assert int(s.status) == 0 and bool(torch.isfinite(s.hidden[:3].float()).all())
+    _put(s, [1, 9, 0, 0], rows)                               # and here those of a request that has too many tokens
+    s.run()
+    torch.cuda.synchronize()
+    assert int(s.status) == 16 and bool(torch.isfinite(s.hidden[:1].float()).all())
+    assert s.lens.cpu().tolist() == [3, 2, 2, 3]
