@@ -132,7 +132,7 @@ class DecoderStep:
     status.  4-bit products run on w4_gemv up to 16 tokens and on w4_gemm beyond; rows for 8-bit
     products are quantized by the operator that computes them.
     A step of another size over the same requests (a captured one for single tokens beside one for
-    prompts) is made with ``state``, the step whose lengths, pages, table and status it shares.
+    prompts) is made with ``state``, the step whose caches, lengths, pages, table and status it shares.
     """
 
     def __init__(self, layers, caches, heads, rope, final_norm, tokens, seqs, max_pages, eps=1e-5, free_pages=None,
@@ -158,7 +158,8 @@ class DecoderStep:
         self.residual, self.hidden = torch.zeros(tokens, hidden, **bf16), torch.zeros(tokens, hidden, **bf16)
         self.new_lens = torch.zeros(seqs, **i32)
         if state is not None:
-            if state.block_table.shape != (seqs, max_pages) or state.caches[0] is not c:
+            if (state.block_table.shape != (seqs, max_pages) or len(state.caches) != len(caches)
+                    or any(x is not y for x, y in zip(state.caches, caches))):
                 raise ValueError("state is of other requests")
             self.lens, self.free_pages, self.free_count = state.lens, state.free_pages, state.free_count
             self.block_table, self.status = state.block_table, state.status

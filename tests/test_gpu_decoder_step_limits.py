@@ -1,5 +1,5 @@
 """DecoderStep at its edges: rows that become padding after they held a value that is not finite, and
-requests that are refused."""
+requests that are refused; a state whose caches are others."""
 
 import pytest
 import torch
@@ -43,3 +43,13 @@ def test_rows_that_become_padding(kind, fp8_cache, capture):
     torch.cuda.synchronize()
     assert int(s.status) == 16 and bool(torch.isfinite(s.hidden[:1].float()).all())
     assert s.lens.cpu().tolist() == [3, 2, 2, 3]
+
+
+def test_state_of_other_caches_is_refused():
+    m = Model(("w4",) * 4, False, 16, False, seed=8)
+    caches = [w4.W4KVCache.empty(2, 16, KV, D, device=DEV) for _ in m.layers]
+    s = DecoderStep(m.layers, caches, HEADS, m.spec, m.final_dev, 4, 1, 2)
+    DecoderStep(m.layers, list(caches), HEADS, m.spec, m.final_dev, 2, 1, 2, state=s)
+    others = [caches[0]] + [w4.W4KVCache.empty(2, 16, KV, D, device=DEV) for _ in m.layers[1:]]
+    with pytest.raises(ValueError):
+        DecoderStep(m.layers, others, HEADS, m.spec, m.final_dev, 2, 1, 2, state=s)
