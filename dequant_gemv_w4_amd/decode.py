@@ -146,6 +146,7 @@ class DecoderStep:
         self.layers, self.caches, self.heads, self.rope, self.eps = layers, caches, heads, rope, eps
         self.final_norm, self.tokens, self.page_size = final_norm, tokens, c.page_size
         dev, hidden = c.device, layers[0].qkv.k
+        self._device = dev
         width = (heads + 2 * c.kv_heads) * c.head_dim
         for a in layers:
             ffn = a.down.k
@@ -226,6 +227,11 @@ class DecoderStep:
 
     def run_eager(self) -> None:
         import torch
+        with torch.cuda.device(self._device):                # some products launch on the current device
+            self._step()
+
+    def _step(self) -> None:
+        import torch
         from . import w4_block_tables, w4_paged_attention, w4_rmsnorm, w4_rope_cache
         w4_block_tables(self.new_lens, self.lens, self.free_pages, self.free_count, self.block_table, self.page_size,
                         cu_q=self.cu_q, positions=self.positions, slots=self.slots, status=self.status)
@@ -252,15 +258,17 @@ class DecoderStep:
         """Record a step once into a graph (replayed by run()); what goes on from step to step, and
         ``residual``, is left as it was."""
         import torch
-        kept = [t.clone() for t in self._state()]
-        self.run_eager()                      # warm caches and the device check outside capture
-        torch.cuda.synchronize()
-        g = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(g):
-            self.run_eager()
-        for t, k in zip(self._state(), kept):
-            t.copy_(k)
-        torch.cuda.synchronize()
+        with torch.cuda.device(self._device):
+            kept = [t.clone() for t in self._state()]
+            self.run_eager()                  # warm caches and the device check outside capture
+            torch.cuda.synchronize()
+            g = torch.cuda.CUDAGraph()
+            # a stream of this device: the one that torch captures on by default stays on the first device used
+            with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+                self.run_eager()
+            for t, k in zip(self._state(), kept):
+                t.copy_(k)
+            torch.cuda.synchronize()
         self._graph = g
 
     def _state(self):

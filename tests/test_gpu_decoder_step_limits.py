@@ -1,5 +1,6 @@
 """DecoderStep at its edges: rows that become padding after they held a value that is not finite, and
-requests that are refused; a state whose caches are others."""
+requests that are refused; a state whose caches are others; a device that is not
+the current one."""
 
 import pytest
 import torch
@@ -53,3 +54,35 @@ def test_state_of_other_caches_is_refused():
     others = [caches[0]] + [w4.W4KVCache.empty(2, 16, KV, D, device=DEV) for _ in m.layers[1:]]
     with pytest.raises(ValueError):
         DecoderStep(m.layers, others, HEADS, m.spec, m.final_dev, 2, 1, 2, state=s)
+
+
+def test_capture_on_the_step_s_own_device(monkeypatch):
+    # A graph records what goes to the capturing stream of one device: the step has to make its device the
+    # current one and capture on a stream of it.  One GPU is here, so the calls that do it are watched.
+    m = Model(("w4",) * 4, False, 16, False, seed=8)
+    caches = [w4.W4KVCache.empty(2, 16, KV, D, device=DEV) for _ in m.layers]
+    s = DecoderStep(m.layers, caches, HEADS, m.spec, m.final_dev, 4, 1, 2)
+    inside, real_device, real_graph = [], torch.cuda.device, torch.cuda.graph
+    graphs = []
+
+    class Device(real_device):
+        def __enter__(self):
+            inside.append(self.idx)
+            return super().__enter__()
+
+        def __exit__(self, *a):
+            inside.pop()
+            return super().__exit__(*a)
+
+    def graph(g, **kw):
+        graphs.append((list(inside), kw["stream"].device.index if kw.get("stream") is not None else None))
+        return real_graph(g, **kw)
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch.cuda, "graph", graph)
+    s.capture()
+    assert graphs == [([0], 0)]
+    s.new_lens.fill_(2)
+    s.run()
+    torch.cuda.synchronize()
+    assert s.lens.cpu().tolist() == [2] and int(s.status) == 0
