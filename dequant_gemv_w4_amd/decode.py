@@ -131,6 +131,9 @@ class DecoderStep:
     zeroed first (three small launches a step), so that nothing an earlier step left in them reaches the
     status.  4-bit products run on w4_gemv up to 16 tokens and on w4_gemm beyond; rows for 8-bit
     products are quantized by the operator that computes them.
+    A request ends when the caller takes it out between two steps: with n the pages that its ``lens[b]``
+    tokens fill, ``block_table[b, :n]`` goes to ``free_pages[free_count : free_count + n]``, ``free_count``
+    grows by n and ``lens[b]`` becomes 0; the next request may then use its place.
     A step of another size over the same requests (a captured one for single tokens beside one for
     prompts) is made with ``state``, the step whose caches, lengths, pages, table and status it shares.
     """

@@ -1,13 +1,15 @@
 """DecoderStep at its edges: rows that become padding after they held a value that is not finite, and
-requests that are refused; a state whose caches are others; a device that is not
-the current one."""
+requests that are refused; requests that end and give their pages back; a state whose caches are
+others; a device that is not the current one."""
 
+import numpy as np
 import pytest
 import torch
 
 import dequant_gemv_w4_amd as w4
+import oracle
 from dequant_gemv_w4_amd.decode import DecoderStep
-from test_gpu_decoder_step import D, DEV, EPS, HEADS, HIDDEN, KV, Model
+from test_gpu_decoder_step import D, DEV, EPS, HEADS, HIDDEN, KV, MORE, TOL, Model, _check
 
 pytestmark = pytest.mark.gpu
 
@@ -44,6 +46,35 @@ def test_rows_that_become_padding(kind, fp8_cache, capture):
     torch.cuda.synchronize()
     assert int(s.status) == 16 and bool(torch.isfinite(s.hidden[:1].float()).all())
     assert s.lens.cpu().tolist() == [3, 2, 2, 3]
+
+
+@pytest.mark.parametrize("kind,fp8_cache", [("w4", False), ("fp8", True)])
+def test_requests_end_and_others_take_their_pages(kind, fp8_cache):
+    # the pages of the request that ends go back to the list behind the free ones; the next takes them
+    page, pages, wide = 16, 6, 4
+    m = Model((kind,) * 4, fp8_cache, page, False, seed=14)
+    g = np.random.default_rng(3)
+    caches = [w4.W4KVCache.empty(pages, page, KV, D, fp8=fp8_cache, device=DEV) for _ in m.layers]
+    s = DecoderStep(m.layers, caches, HEADS, m.spec, m.final_dev, 64, 2, wide, EPS)
+    tol = TOL + MORE[kind]
+    other = oracle.bf16_round(g.standard_normal((4, HIDDEN)).astype(np.float32))
+    other_ref = m.forward(other)
+    done = 0
+    for n in (50, 37, 60, 33):                                # 4 or 3 of 5 pages: none fits beside its predecessor
+        emb = oracle.bf16_round(g.standard_normal((n, HIDDEN)).astype(np.float32))
+        _put(s, [n, 1], torch.from_numpy(np.concatenate([emb, other[done: done + 1]])).to(DEV).to(torch.bfloat16))
+        s.run()
+        torch.cuda.synchronize()
+        assert int(s.status) == 0 and s.lens.cpu().tolist() == [n, done + 1]
+        _check(s.hidden[:n], m.forward(emb), f"request of {n} tokens", tol)
+        _check(s.hidden[n: n + 1], other_ref[done: done + 1], f"token {done} beside it", tol)
+        done += 1
+        held, count = -(-n // page), int(s.free_count)
+        s.free_pages[count: count + held] = s.block_table[0, :held]
+        s.free_count += held
+        s.block_table[0] = -1
+        s.lens[0] = 0
+        assert sorted(s.free_pages[: count + held].tolist() + s.block_table[1, :1].tolist()) == list(range(pages))
 
 
 def test_state_of_other_caches_is_refused():
