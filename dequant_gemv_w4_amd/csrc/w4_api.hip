@@ -10,6 +10,7 @@
 
 #include "w4a16.h"
 #include "w4_internal.h"
+#include "w4_paging.h"
 
 namespace {
 

@@ -524,9 +524,7 @@ struct Tile {
     bool run;
 };
 
-// Tile number `index` of R rows: of attend_wide's (R = kWideRows) or attend_narrow's.  Where both are
-// launched, a sequence of at most few_tiles (1 or 2) * kFewRows rows is the narrow kernel's, as so many
-// tiles; alone that has, for as many tokens as sequences, the tiles that G rows fill for each token.
+// Tile number `index` of R rows: of attend_wide's (R = kWideRows) or attend_narrow's.
 template <int R>
 __device__ __forceinline__ Tile find_tile(const AttendArgs& a, uint32_t index, int part, int& kv) {
     constexpr bool WIDE = R == kWideRows;
@@ -536,22 +534,17 @@ __device__ __forceinline__ Tile find_tile(const AttendArgs& a, uint32_t index, i
     kv = (int)index - tile * a.kv_heads;
     t.part_row = (int64_t)index * R;
     if (!WIDE && a.both) {
-        // all first tiles, then all second ones, which mostly have no rows: taking turns, they would leave
-        // every other place that the workgroups go to in turn without work (31 single tokens over 4000
-        // beside a chunk: 143 us instead of 113)
-        t.b = tile < a.B ? tile : tile - a.B;
-        t.row0 = tile < a.B ? 0 : R;
+        t.b = few_sequence(tile, a.B);
+        t.row0 = few_row0(tile, a.B, R);
         t.seq = load_seq(a, t.b);
     } else {
-        const int per = (G + R - 1) / R;                     // tiles a token
         const bool by_token = !WIDE && a.T == a.B;
-        auto first = [&](int cu_b, int b) { return by_token ? cu_b * per : first_tile(cu_b, b, G, R); };
+        auto first = [&](int cu_b, int b) { return by_token ? token_tile(cu_b, G, R) : first_tile(cu_b, b, G, R); };
         t.seq = find_seq(a, first, tile, t.b);
         t.row0 = (tile - first(t.seq.start, t.b)) * R;
     }
     t.rows = t.seq.n * G;
-    const bool few = t.rows <= a.few_tiles * kFewRows;
-    t.run = t.row0 >= 0 && t.row0 < t.rows && (WIDE ? !few : few || !a.both);
+    t.run = tile_runs(WIDE, a.both, t.row0, t.rows, a.few_tiles);
     if (!t.run) return t;
     const int reach = a.window > 0 ? min(t.seq.ctx, a.window) : t.seq.ctx;
     const int parts = !WIDE ? (a.both && t.rows > R ? a.narrow_fill : a.narrow_parts) : reach < kWideEven ? a.wide_fill : a.wide_parts;
@@ -1236,47 +1229,7 @@ __global__ __launch_bounds__(256) void combine_kernel(AttendArgs a) {
         combine_rows<D, kFewRows>(a, blockIdx.x);
 }
 
-// Parts that a launch allows per tile, to make up to `target` workgroups.  256 is one a compute unit (LDS
-// holds no second).  Single tokens, workgroups up to 256: 24 requests of up to 2000 tokens (192 tiles)
-// take 35 us unsplit, 42 in two parts each; 5 of up to 8000 over 32 kv heads 113 and 128; 32 of up to 8192
-// 155 with 256 workgroups, 165 with 512, 168 with 1024.  Wide tiles: up to 256 as well, since a part
-// costs a pass over its rows' results (1100 tokens over 500: 60 us unsplit, 86 in two parts; over 2000 136
-// and 160), but where the keys are many (kWideEven) about 512, so that the last round of workgroups is a
-// small one (over 8000: 448 and 400, over 30,000 1602 and 1284).  At least kNarrowLeast keys a part, and
-// none below twice that: one request over 1000 keys takes 11.2 us with parts of 256, 12.1 with 512, over
-// 500 8.5 unsplit and 10.2 split.  Wide: 16 tokens over 2000 16.0 with 128, 17.2 with 256, 22.8 with 512.
-int parts_for(int64_t tiles, int64_t target, int64_t longest, int64_t least) {
-    const int64_t want = longest > 2 * least ? target / tiles : 1;
-    return (int)imax(1, imin(want, imin(ceil_div(longest, least), kMaxParts)));
-}
-
 }  // namespace
-
-void plan_attend(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int64_t capacity, bool fp8, AttendPlan* p) {
-    const int64_t G = heads / kv_heads;
-    // One token a sequence, or too few rows for the wide kernel: no sequence needs it.
-    p->both = T != B && T * G > kFewRows;
-    // Sequences of 33 to 64 rows as two narrow tiles: a wide one would have no rows for most of its waves.
-    // 16 requests of up to 8 tokens (8 heads a kv head) over up to 4000 take 69 us so, 91 with wide tiles, 8 over
-    // an E4M3 cache 38 and 55, 32 78 and 113.  Of a bfloat16 cache the keys come from memory twice where the
-    // second tiles have to wait for a compute unit: 32 requests 113 and 95.
-    p->few_tiles = fp8 || 2 * B * kv_heads <= 256 ? 2 : 1;
-    // 32 rows a narrow tile where 16 would read a sequence's keys twice: single tokens of 32 requests over up
-    // to 8192, 32 heads a kv head, take 51.6 us instead of 71.6, four tokens of 32 over 4000 (8 heads) 81.6
-    // instead of 97.0.  Not where the keys could not even give every compute unit a workgroup of 16 rows: one
-    // request over 8000, 2 kv heads, takes 14.8 us with 16 and 16.1 with 32.
-    const int64_t fine = T * ceil_div(G, 16) * kv_heads * ceil_div(capacity, kNarrowLeast);
-    p->narrow_tile = p->both || (G > 16 && fine > 256) ? kFewRows : 16;
-    const int64_t R = p->narrow_tile;
-    p->narrow_tiles = (p->both ? B * p->few_tiles : T == B ? T * ceil_div(G, R) : tile_bound(T, B, G, R)) * kv_heads;
-    // beside wide tiles most sequences have one narrow tile, which may then take the parts of the idle ones
-    p->narrow_fill = parts_for(p->narrow_tiles, 256, capacity, kNarrowLeast);
-    p->narrow_parts = p->both ? parts_for(B * kv_heads, 256, capacity, kNarrowLeast) : p->narrow_fill;
-    p->wide_tiles = p->both ? tile_bound(T, B, G, kWideRows) * kv_heads : 0;
-    p->wide_fill = p->both ? parts_for(p->wide_tiles, 256, capacity, kWideLeast) : 1;
-    p->wide_parts = p->both && capacity >= kWideEven
-                        ? parts_for(p->wide_tiles, 511 + p->wide_tiles, capacity, kWideLeast) : p->wide_fill;
-}
 
 static int64_t split_rows(bool wide, const AttendPlan& p) {
     const int64_t tiles = wide ? p.wide_tiles : p.narrow_tiles;

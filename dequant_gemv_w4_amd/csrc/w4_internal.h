@@ -183,10 +183,6 @@ struct TableArgs {
 };
 hipError_t launch_block_tables(const TableArgs& a, hipStream_t s);
 
-// Attention: query rows of a tile in the two kernels, keys a part takes at least, parts at most.
-constexpr int kFewRows = 32, kWideRows = 256;   // narrow: 16 or kFewRows
-constexpr int kNarrowLeast = 256, kWideLeast = 128, kWideEven = 4096, kMaxParts = 64;
-
 struct AttendArgs {
     const uint16_t* q;
     uint16_t* o;
@@ -208,17 +204,7 @@ struct AttendArgs {
     int narrow_tile, few_tiles, narrow_tiles, wide_tiles, narrow_parts, narrow_fill, wide_parts, wide_fill;
     bool both;           // both kinds of tiles are launched
 };
-// What the host knows of a call decides the launches; the parts that a tile really has follow
-// from the lengths on the device.
-struct AttendPlan {
-    int64_t narrow_tiles, wide_tiles;   // workgroups of one part
-    int narrow_tile;                    // rows of a narrow tile: 16 or kFewRows
-    int few_tiles;                      // narrow tiles of a sequence that has no wide ones, beside wide ones
-    int narrow_parts, narrow_fill, wide_parts, wide_fill;
-    bool both;
-};
-void plan_attend(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int64_t capacity, bool fp8,
-                 AttendPlan* p);
+struct AttendPlan;
 size_t attend_workspace(int64_t D, const AttendPlan& p);
 hipError_t launch_attend(AttendArgs a, int head_dim, bool fp8, const AttendPlan& p, void* workspace,
                          hipStream_t s);

@@ -37,6 +37,26 @@ W4_HD int32_t quotient(int32_t a, int32_t b) { return (int32_t)((uint32_t)a / (u
 W4_HD int32_t first_tile(int32_t cu_b, int32_t b, int32_t G, int32_t R) { return quotient(cu_b * G, R) + b; }
 W4_HD int64_t tile_bound(int64_t T, int64_t B, int64_t G, int64_t R) { return T * G / R + B; }
 
+// The other two ways to number tiles.  By token, where there are as many tokens as sequences: each token has
+// the tiles that its G rows fill, so a sequence's first follows from its first token.
+W4_HD int32_t token_tile(int32_t cu_b, int32_t G, int32_t R) { return cu_b * quotient(G + R - 1, R); }
+// Of sequences with few rows beside wide tiles: all first tiles, then all second ones, which mostly have no
+// rows: taking turns, they would leave every other place that the workgroups go to in turn without work
+// (31 single tokens over 4000 beside a chunk: 143 us instead of 113).
+W4_HD int32_t few_sequence(int32_t tile, int32_t B) { return tile < B ? tile : tile - B; }
+W4_HD int32_t few_row0(int32_t tile, int32_t B, int32_t R) { return tile < B ? 0 : R; }
+
+// Attention: query rows of a tile in the two kernels, keys a part takes at least, parts at most.
+constexpr int kFewRows = 32, kWideRows = 256;   // narrow: 16 or kFewRows
+constexpr int kNarrowLeast = 256, kWideLeast = 128, kWideEven = 4096, kMaxParts = 64;
+
+// Whether a tile has rows: where both kinds are launched, a sequence of at most few_tiles (1 or 2) * kFewRows
+// rows has narrow tiles, as many, and the others have wide ones.
+W4_HD bool tile_runs(bool wide, bool both, int32_t row0, int32_t rows, int32_t few_tiles) {
+    const bool few = rows <= few_tiles * kFewRows;
+    return row0 >= 0 && row0 < rows && (wide ? !few : few || !both);
+}
+
 // A sequence as the kernels read it, whatever the arrays hold: its rows lie in [0, T) and its
 // keys in the table.
 struct Seq {
@@ -95,6 +115,56 @@ W4_HD Span seen_span(Span k) {
         k.parts = quotient(k.end - begin + k.chunk - 1, k.chunk);
     }
     return k;
+}
+
+// What the host knows of a call decides the launches; the parts that a tile really has follow
+// from the lengths on the device.
+struct AttendPlan {
+    int64_t narrow_tiles, wide_tiles;   // workgroups of one part
+    int narrow_tile;                    // rows of a narrow tile: 16 or kFewRows
+    int few_tiles;                      // narrow tiles of a sequence that has no wide ones, beside wide ones
+    int narrow_parts, narrow_fill, wide_parts, wide_fill;
+    bool both;
+};
+
+// Parts that a launch allows per tile, to make up to `target` workgroups.  256 is one a compute unit (LDS
+// holds no second).  Single tokens, workgroups up to 256: 24 requests of up to 2000 tokens (192 tiles)
+// take 35 us unsplit, 42 in two parts each; 5 of up to 8000 over 32 kv heads 113 and 128; 32 of up to 8192
+// 155 with 256 workgroups, 165 with 512, 168 with 1024.  Wide tiles: up to 256 as well, since a part
+// costs a pass over its rows' results (1100 tokens over 500: 60 us unsplit, 86 in two parts; over 2000 136
+// and 160), but where the keys are many (kWideEven) about 512, so that the last round of workgroups is a
+// small one (over 8000: 448 and 400, over 30,000 1602 and 1284).  At least kNarrowLeast keys a part, and
+// none below twice that: one request over 1000 keys takes 11.2 us with parts of 256, 12.1 with 512, over
+// 500 8.5 unsplit and 10.2 split.  Wide: 16 tokens over 2000 16.0 with 128, 17.2 with 256, 22.8 with 512.
+inline int parts_for(int64_t tiles, int64_t target, int64_t longest, int64_t least) {
+    const int64_t want = longest > 2 * least ? target / tiles : 1;
+    return (int)imax(1, imin(want, imin(ceil_div(longest, least), kMaxParts)));
+}
+
+inline void plan_attend(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int64_t capacity, bool fp8, AttendPlan* p) {
+    const int64_t G = heads / kv_heads;
+    // One token a sequence, or too few rows for the wide kernel: no sequence needs it.
+    p->both = T != B && T * G > kFewRows;
+    // Sequences of 33 to 64 rows as two narrow tiles: a wide one would have no rows for most of its waves.
+    // 16 requests of up to 8 tokens (8 heads a kv head) over up to 4000 take 69 us so, 91 with wide tiles, 8 over
+    // an E4M3 cache 38 and 55, 32 78 and 113.  Of a bfloat16 cache the keys come from memory twice where the
+    // second tiles have to wait for a compute unit: 32 requests 113 and 95.
+    p->few_tiles = fp8 || 2 * B * kv_heads <= 256 ? 2 : 1;
+    // 32 rows a narrow tile where 16 would read a sequence's keys twice: single tokens of 32 requests over up
+    // to 8192, 32 heads a kv head, take 51.6 us instead of 71.6, four tokens of 32 over 4000 (8 heads) 81.6
+    // instead of 97.0.  Not where the keys could not even give every compute unit a workgroup of 16 rows: one
+    // request over 8000, 2 kv heads, takes 14.8 us with 16 and 16.1 with 32.
+    const int64_t fine = T * ceil_div(G, 16) * kv_heads * ceil_div(capacity, kNarrowLeast);
+    p->narrow_tile = p->both || (G > 16 && fine > 256) ? kFewRows : 16;
+    const int64_t R = p->narrow_tile;
+    p->narrow_tiles = (p->both ? B * p->few_tiles : T == B ? T * ceil_div(G, R) : tile_bound(T, B, G, R)) * kv_heads;
+    // beside wide tiles most sequences have one narrow tile, which may then take the parts of the idle ones
+    p->narrow_fill = parts_for(p->narrow_tiles, 256, capacity, kNarrowLeast);
+    p->narrow_parts = p->both ? parts_for(B * kv_heads, 256, capacity, kNarrowLeast) : p->narrow_fill;
+    p->wide_tiles = p->both ? tile_bound(T, B, G, kWideRows) * kv_heads : 0;
+    p->wide_fill = p->both ? parts_for(p->wide_tiles, 256, capacity, kWideLeast) : 1;
+    p->wide_parts = p->both && capacity >= kWideEven
+                        ? parts_for(p->wide_tiles, 511 + p->wide_tiles, capacity, kWideLeast) : p->wide_fill;
 }
 
 // Number of a page if the cache has it, else -1.
