@@ -143,7 +143,12 @@ inline int parts_for(int64_t tiles, int64_t target, int64_t longest, int64_t lea
 
 inline void plan_attend(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int64_t capacity, bool fp8, AttendPlan* p) {
     const int64_t G = heads / kv_heads;
-    // One token a sequence, or too few rows for the wide kernel: no sequence needs it.
+    // As many tokens as sequences are taken for one each, and then as for too few rows in all the wide
+    // kernel is left out.  The lengths are on the device: a prompt among idle sequences has narrow tiles for
+    // every 16 rows there (a prompt of 500 in 512 places 55 us, 36 with one row more; 200 tokens and 56
+    // single ones over 2000 in 256 places 145 and 106; 4000 over 4000 in 4096 places 2490 and 910).  Single
+    // tokens are what such a batch mostly holds, and both kernels would cost them more: 32 over up to 8192
+    // 156 us, 178 with one row more; 256 over 2000 336 and 346.
     p->both = T != B && T * G > kFewRows;
     // Sequences of 33 to 64 rows as two narrow tiles: a wide one would have no rows for most of its waves.
     // 16 requests of up to 8 tokens (8 heads a kv head) over up to 4000 take 69 us so, 91 with wide tiles, 8 over

@@ -275,7 +275,9 @@ __global__ __launch_bounds__(1024) void silu_mul_kernel(const void* gu, int64_t 
 // chunks (512 threads), 57 with four, 63 with one.  `wide` raises that to eight for rows past 16384
 // values where the registers allow it (bfloat16 gate rows): 4096 x 28672 to E4M3 takes 125 us
 // with 448 threads, of which two workgroups fit, 174 with 896, of which one does; binary32 rows
-// spill there (1024 x 28672: 75 us with eight, 65 with four).
+// spill there (1024 x 28672: 75 us with eight, 65 with four).  Past 32768 values a row needs eight with
+// any type, and a binary32 norm with a binary32 residual then spills 89 registers: 1024 x 65536 to E4M3 takes
+// 276 us, where a copy of its bytes takes 182.
 struct RowShape {
     int threads;
     int chunks;

@@ -136,6 +136,8 @@ class DecoderStep:
     grows by n and ``lens[b]`` becomes 0; the next request may then use its place.
     A step of another size over the same requests (a captured one for single tokens beside one for
     prompts) is made with ``state``, the step whose caches, lengths, pages, table and status it shares.
+    ``tokens`` = ``seqs`` suits single tokens; a step that takes prompts should have another number of
+    tokens, since the attention takes T = B for one token a request and is slower where it is not.
     """
 
     def __init__(self, layers, caches, heads, rope, final_norm, tokens, seqs, max_pages, eps=1e-5, free_pages=None,

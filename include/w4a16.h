@@ -75,9 +75,9 @@ typedef enum {
 
 typedef enum { W4_F32 = 0, W4_BF16 = 1 } w4_dtype;
 
-/* Device status word bits (OR-ed, never cleared), written by w4_quantize and, the last three,
- * by the paged-cache calls. */
-#define W4_STATUS_NONFINITE      1u  /* a weight was NaN or +-inf (outputs undefined) */
+/* Device status word bits (OR-ed, never cleared): the first three written by w4_quantize, the first also
+ * by the calls that quantize rows to 8 bits, the last three by the paged-cache calls. */
+#define W4_STATUS_NONFINITE      1u  /* a weight or a value of a row was NaN or +-inf (outputs undefined) */
 #define W4_STATUS_SCALE_OVERFLOW 2u  /* a binary32 scale rounded to binary16 infinity */
 #define W4_STATUS_SCALE_ZERO     4u  /* a non-empty group's scale rounded to binary16 zero */
 #define W4_STATUS_PAGE           8u  /* a page or slot number outside the cache */
@@ -489,7 +489,7 @@ w4_status w4_block_tables(const int32_t* new_lens, const int32_t* lens_in, int64
  * lens[b] - (cu_q[b+1] - cu_q[b]) + t.  Query head h reads kv head h / (heads / kv_heads).
  *   q            [T, heads, head_dim] bfloat16; 16-B aligned.
  *   block_table  [B, max_pages] device; cu_q [B + 1], lens [B] device (as w4_block_tables
- *                writes them: lens counts the new tokens).
+ *                writes them: lens counts the new tokens; one past the table counts as its end).
  *   scale        finite, > 0.   window  0 (none) or >= 1.   (else W4_ERR_VALUE)
  *   o            out [T, heads, head_dim] bfloat16; 16-B aligned; must not overlap q.  Rows that
  *                belong to no request stay as they are; a row that sees no key gets zeros.
@@ -501,10 +501,14 @@ w4_status w4_block_tables(const int32_t* new_lens, const int32_t* lens_in, int64
  * window, or behind a request's keys, are not looked at: such pages may have been given back.
  * What lies in the cache behind a request's keys, and at keys that a row does not see, does not
  * reach the row, NaN and infinities included.
- * Scores, softmax sums and outputs are formed in binary32 and o is rounded once; requests with at
- * most 32 rows (tokens times query heads of a kv head), in small batches 64, or all where T = B,
- * multiply V by weights held in two bfloat16 parts (2^-16), longer chunks by weights rounded to
- * bfloat16.
+ * Scores, softmax sums and outputs are formed in binary32 and o is rounded once.  V is multiplied by
+ * weights held in two bfloat16 parts (2^-16) for every request where T = B or all rows together
+ * (T times heads / kv_heads) are at most 32, else for requests of at most 32 rows, 64 with an E4M3
+ * cache or where 2 * B * kv_heads <= 256; for the others by weights rounded to bfloat16 (2^-8).  A
+ * request's last bits may so depend on the batch that it is in.
+ * T = B is taken for one token a request: any lengths give right results, but a long prompt there
+ * reads its keys once for every 16 rows.  Where prompts and idle places may add up to T = B, one
+ * padding row more (T = B + 1) avoids that.
  * Deterministic; the split of the work depends on the arguments and lengths only.
  * Requires 1 <= T <= W4_MAX_TOKENS, 1 <= B <= W4_MAX_SEQUENCES, heads a multiple of kv_heads, at
  * most 65536, T * heads < 2^26, 1 <= max_pages, max_pages * page_size <= W4_MAX_CONTEXT.
