@@ -25,6 +25,7 @@ __all__ = [
     "w4_rmsnorm", "w4_rmsnorm_fp8", "w4_rmsnorm_int8", "w4_silu_mul", "w4_silu_mul_fp8", "w4_silu_mul_int8",
     "W4KVCache", "W4Rope", "w4_rope_frequencies", "w4_rope_cache", "w4_block_tables",
     "w4_paged_attention", "w4_paged_attention_workspace_bytes",
+    "w4_cache_write", "w4_cache_read", "W4Scores", "w4_paged_attention_scores",
     "W4_OK", "W4_F32", "W4_BF16", "GROUP",
 ]
 
@@ -62,6 +63,11 @@ class _KVCacheStruct(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
                 ("v_scales", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
                 ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("type", ctypes.c_int32)]
+
+
+class _ScoresStruct(ctypes.Structure):
+    _fields_ = [("cap", ctypes.c_float), ("reserved", ctypes.c_int32), ("slopes", ctypes.c_void_p),
+                ("first_keys", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p)]
 
 
 class W4Rope(ctypes.Structure):
@@ -165,6 +171,10 @@ def lib() -> ctypes.CDLL:
     L.w4_paged_attention_workspace_bytes.argtypes = [i64, i64, cp, i64, i64]
     L.w4_paged_attention_workspace_bytes.restype = sz
     L.w4_paged_attention.argtypes = [vp, i64, i64, cp, vp, i64, vp, vp, i64, f32, i64, vp, vp, sz, vp, vp]
+    L.w4_cache_write.argtypes = [vp, i32, i64, i64, cp, vp, vp, vp, vp]
+    L.w4_cache_read.argtypes = [cp, vp, i64, vp, i32, vp, vp]
+    L.w4_paged_attention_scores.argtypes = [vp, i64, i64, cp, vp, i64, vp, vp, i64, f32, i64,
+                                            ctypes.POINTER(_ScoresStruct), vp, vp, sz, vp, vp]
     del u32
     _lib = L
     return L
@@ -588,7 +598,8 @@ def w4_int8_gemm(xq, sx, wq, sw, Y=None, out_dtype=None):
 # --------------------------------------------------------------------------
 
 _LAYER = ("w4_rmsnorm", "w4_rmsnorm_fp8", "w4_rmsnorm_int8", "w4_silu_mul", "w4_silu_mul_fp8", "w4_silu_mul_int8",
-          "W4KVCache", "w4_rope_cache", "w4_block_tables", "w4_paged_attention", "w4_paged_attention_workspace_bytes")
+          "W4KVCache", "w4_rope_cache", "w4_block_tables", "w4_paged_attention", "w4_paged_attention_workspace_bytes",
+          "w4_cache_write", "w4_cache_read", "W4Scores", "w4_paged_attention_scores")
 
 
 def __getattr__(name):

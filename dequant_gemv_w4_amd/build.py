@@ -20,7 +20,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["w4_api.hip", "w4_quantize.hip", "w4_gemv.hip", "w4_gemv_mfma.hip", "w4_gemm.hip",
            "w4_probe.hip", "w4_w8a8.hip", "w4_rows.hip", "w4_cache.hip",
-           "w4_attention.hip"]
+           "w4_attention.hip", "w4_attention_int8.hip", "w4_attention_scores.hip", "w4_attention_scores_fp8.hip",
+           "w4_blocks.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

@@ -80,7 +80,7 @@ w4_status check_page_size(int32_t page_size, int* shift) {
 
 w4_status check_cache(const w4_kv_cache* c, int* shift) {
     if (!c) return W4_ERR_NULL;
-    if (c->type != W4_CACHE_BF16 && c->type != W4_CACHE_FP8) return W4_ERR_UNSUPPORTED;
+    if (c->type != W4_CACHE_BF16 && c->type != W4_CACHE_FP8 && c->type != W4_CACHE_INT8) return W4_ERR_UNSUPPORTED;
     if (c->head_dim != 64 && c->head_dim != 128) return W4_ERR_UNSUPPORTED;
     const w4_status st = check_page_size(c->page_size, shift);
     if (st != W4_OK) return st;
@@ -92,7 +92,7 @@ w4_status check_cache(const w4_kv_cache* c, int* shift) {
 
 w4_status check_cache_pointers(const w4_kv_cache* c) {
     if (!c->k || !c->v) return W4_ERR_NULL;
-    if (c->type == W4_CACHE_FP8 && (!c->k_scales || !c->v_scales)) return W4_ERR_NULL;
+    if (c->type != W4_CACHE_BF16 && (!c->k_scales || !c->v_scales)) return W4_ERR_NULL;
     if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scales, 4) ||
         !aligned(c->v_scales, 4))
         return W4_ERR_ALIGN;
@@ -105,6 +105,9 @@ w4_status check_heads(int64_t T, int64_t heads, const w4_kv_cache* c) {
         return W4_ERR_SHAPE;
     return W4_OK;
 }
+
+// The kernels' number of a cache type.
+int cache_kind(const w4_kv_cache* c) { return c->type == W4_CACHE_INT8 ? 2 : c->type == W4_CACHE_FP8 ? 1 : 0; }
 
 w4_status check_batch(int64_t B, int64_t max_pages, int64_t page_size) {
     if (B < 1 || B > W4_MAX_SEQUENCES || max_pages < 1 || max_pages > W4_MAX_CONTEXT / page_size)
@@ -622,6 +625,33 @@ w4_status w4_rope_frequencies(const w4_rope* rope, double* freqs, double* amplit
     return W4_OK;
 }
 
+// What a write into a cache takes, without rotation.
+static w4::RopeArgs rope_args(const w4_kv_cache* cache, int shift, const void* qkv, int64_t T, int64_t heads,
+                              const int64_t* slots, void* q, uint32_t* d_status) {
+    w4::RopeArgs a = {};
+    a.qkv = qkv;
+    a.slots = slots;
+    a.q = static_cast<uint16_t*>(q);
+    a.k = cache->k;
+    a.v = cache->v;
+    a.k_scales = cache->k_scales;
+    a.v_scales = cache->v_scales;
+    a.status = d_status;
+    a.T = T;
+    a.pages = cache->pages;
+    a.heads = (int)heads;
+    a.kv_heads = cache->kv_heads;
+    a.head_dim = cache->head_dim;
+    a.page_shift = shift;
+    a.amplitude = 1.0f;
+    return a;
+}
+
+static hipError_t launch_cache_write(const w4::RopeArgs& a, w4_dtype xt, int type, hipStream_t stream) {
+    if (type == W4_CACHE_INT8) return w4::launch_write_blocks(a, xt == W4_F32, stream);
+    return w4::launch_rope_cache(a, xt == W4_F32, type == W4_CACHE_FP8, stream);
+}
+
 w4_status w4_rope_cache(const void* qkv, w4_dtype xt, int64_t T, int64_t heads,
                         const w4_kv_cache* cache, const int32_t* positions, const int64_t* slots,
                         const w4_rope* rope, const double* d_freqs, void* q, uint32_t* d_status,
@@ -640,27 +670,59 @@ w4_status w4_rope_cache(const void* qkv, w4_dtype xt, int64_t T, int64_t heads,
         return W4_ERR_ALIGN;
     st = check_arch();
     if (st != W4_OK) return st;
-    w4::RopeArgs a;
-    a.qkv = qkv;
+    w4::RopeArgs a = rope_args(cache, shift, qkv, T, heads, slots, q, d_status);
     a.positions = positions;
-    a.slots = slots;
     a.freqs = d_freqs;
-    a.q = static_cast<uint16_t*>(q);
+    a.rotary = rope->rotary_dim;
+    a.interleaved = rope->interleaved;
+    a.amplitude = (float)rope_amplitude(rope);
+    const hipError_t e = launch_cache_write(a, xt, cache->type, stream);
+    return e == hipSuccess ? W4_OK : hip_fail(e);
+}
+
+w4_status w4_cache_write(const void* qkv, w4_dtype xt, int64_t T, int64_t heads, const w4_kv_cache* cache,
+                         const int64_t* slots, void* q, uint32_t* d_status, hipStream_t stream) {
+    if (!qkv || !cache || !slots || (heads != 0 && !q)) return W4_ERR_NULL;
+    if (!is_dtype(xt)) return W4_ERR_DTYPE;
+    int shift = 0;
+    w4_status st = check_cache(cache, &shift);
+    if (st == W4_OK) st = check_cache_pointers(cache);
+    if (st == W4_OK) st = check_heads(T, heads == 0 ? cache->kv_heads : heads, cache);
+    if (st != W4_OK) return st;
+    if (!aligned(qkv, 16) || !aligned(q, 16) || !aligned(slots, 8) || !aligned(d_status, 4)) return W4_ERR_ALIGN;
+    st = check_arch();
+    if (st != W4_OK) return st;
+    w4::RopeArgs a = rope_args(cache, shift, qkv, T, heads, slots, q, d_status);
+    const hipError_t e = launch_cache_write(a, xt, cache->type, stream);
+    return e == hipSuccess ? W4_OK : hip_fail(e);
+}
+
+w4_status w4_cache_read(const w4_kv_cache* cache, const int64_t* slots, int64_t n, void* kv, w4_dtype yt,
+                        uint32_t* d_status, hipStream_t stream) {
+    if (!cache || !slots || !kv) return W4_ERR_NULL;
+    if (!is_dtype(yt)) return W4_ERR_DTYPE;
+    int shift = 0;
+    w4_status st = check_cache(cache, &shift);
+    if (st == W4_OK) st = check_cache_pointers(cache);
+    if (st != W4_OK) return st;
+    if (n < 1 || n > W4_MAX_TOKENS) return W4_ERR_SHAPE;
+    if (!aligned(slots, 8) || !aligned(kv, 16) || !aligned(d_status, 4)) return W4_ERR_ALIGN;
+    st = check_arch();
+    if (st != W4_OK) return st;
+    w4::ReadArgs a;
     a.k = cache->k;
     a.v = cache->v;
     a.k_scales = cache->k_scales;
     a.v_scales = cache->v_scales;
+    a.slots = slots;
+    a.out = kv;
     a.status = d_status;
-    a.T = T;
+    a.n = n;
     a.pages = cache->pages;
-    a.heads = (int)heads;
     a.kv_heads = cache->kv_heads;
     a.head_dim = cache->head_dim;
     a.page_shift = shift;
-    a.rotary = rope->rotary_dim;
-    a.interleaved = rope->interleaved;
-    a.amplitude = (float)rope_amplitude(rope);
-    const hipError_t e = w4::launch_rope_cache(a, xt == W4_F32, cache->type == W4_CACHE_FP8, stream);
+    const hipError_t e = w4::launch_cache_read(a, cache_kind(cache), yt == W4_F32, stream);
     return e == hipSuccess ? W4_OK : hip_fail(e);
 }
 
@@ -716,15 +778,15 @@ size_t w4_paged_attention_workspace_bytes(int64_t T, int64_t heads, const w4_kv_
         return 0;
     w4::AttendPlan plan;
     w4::plan_attend(T, B, heads, cache->kv_heads, max_pages << shift,
-                    cache->type == W4_CACHE_FP8, &plan);
+                    cache->type != W4_CACHE_BF16, &plan);
     return w4::attend_workspace(cache->head_dim, plan);
 }
 
-w4_status w4_paged_attention(const void* q, int64_t T, int64_t heads, const w4_kv_cache* cache,
-                             const int32_t* block_table, int64_t max_pages, const int32_t* cu_q,
-                             const int32_t* lens, int64_t B, float scale, int64_t window, void* o,
-                             void* workspace, size_t workspace_bytes, uint32_t* d_status,
-                             hipStream_t stream) {
+static w4_status attend_common(const void* q, int64_t T, int64_t heads, const w4_kv_cache* cache,
+                               const int32_t* block_table, int64_t max_pages, const int32_t* cu_q,
+                               const int32_t* lens, int64_t B, float scale, int64_t window, const w4_scores& scores,
+                               void* o, void* workspace, size_t workspace_bytes, uint32_t* d_status,
+                               hipStream_t stream) {
     if (!q || !cache || !block_table || !cu_q || !lens || !o) return W4_ERR_NULL;
     int shift = 0;
     w4_status st = check_cache(cache, &shift);
@@ -732,14 +794,18 @@ w4_status w4_paged_attention(const void* q, int64_t T, int64_t heads, const w4_k
     if (st == W4_OK) st = check_heads(T, heads, cache);
     if (st == W4_OK) st = check_batch(B, max_pages, cache->page_size);
     if (st != W4_OK) return st;
+    if (scores.reserved != 0) return W4_ERR_UNSUPPORTED;
     if (!(scale > 0.0f) || !std::isfinite(scale) || window < 0) return W4_ERR_VALUE;
+    if (scores.cap != 0.0f && !(scale <= 256.0f && scores.cap >= 0x1p-20f * scale && scores.cap <= 0x1p20f * scale))
+        return W4_ERR_VALUE;
     w4::AttendPlan plan;
     w4::plan_attend(T, B, heads, cache->kv_heads, max_pages << shift,
-                    cache->type == W4_CACHE_FP8, &plan);
+                    cache->type != W4_CACHE_BF16, &plan);
     const size_t need = w4::attend_workspace(cache->head_dim, plan);
     if (need > 0 && (!workspace || workspace_bytes < need)) return W4_ERR_WORKSPACE;
     if (!aligned(q, 16) || !aligned(o, 16) || !aligned(block_table, 4) || !aligned(cu_q, 4) ||
-        !aligned(lens, 4) || !aligned(workspace, 16) || !aligned(d_status, 4))
+        !aligned(lens, 4) || !aligned(scores.slopes, 4) || !aligned(scores.first_keys, 4) ||
+        !aligned(scores.prefix_lens, 4) || !aligned(workspace, 16) || !aligned(d_status, 4))
         return W4_ERR_ALIGN;
     st = check_arch();
     if (st != W4_OK) return st;
@@ -765,9 +831,40 @@ w4_status w4_paged_attention(const void* q, int64_t T, int64_t heads, const w4_k
     a.page_shift = shift;
     a.window = (int)(window < W4_MAX_CONTEXT ? window : 0);   // wider than any context: none
     a.scale_log2 = (float)((double)scale * 1.4426950408889634074);
-    const hipError_t e = w4::launch_attend(a, cache->head_dim, cache->type == W4_CACHE_FP8, plan,
-                                           workspace, stream);
+    a.slopes = scores.slopes;
+    a.first = scores.first_keys;
+    a.prefix = scores.prefix_lens;
+    a.ranges = a.first || a.prefix;
+    if (scores.cap != 0.0f) {                                // tanh(y) = y - y^3 / 3 + 2 y^5 / 15 - 17 y^7 / 315 + ...
+        const double log2e = 1.4426950408889634074, y = (double)scale / scores.cap, s = scale * log2e;
+        a.cap_log2 = (float)(scores.cap * log2e);
+        a.cap_exp = (float)(2.0 * y * log2e);
+        a.cap_small = (float)(0.25 / y);
+        a.cap_c3 = (float)(-s * y * y / 3.0);
+        a.cap_c5 = (float)(s * y * y * y * y * 2.0 / 15.0);
+        a.cap_c7 = (float)(-s * y * y * y * y * y * y * 17.0 / 315.0);
+    }
+    const hipError_t e = w4::launch_attend(a, cache->head_dim, cache_kind(cache), plan, workspace, stream);
     return e == hipSuccess ? W4_OK : hip_fail(e);
+}
+
+w4_status w4_paged_attention(const void* q, int64_t T, int64_t heads, const w4_kv_cache* cache,
+                             const int32_t* block_table, int64_t max_pages, const int32_t* cu_q,
+                             const int32_t* lens, int64_t B, float scale, int64_t window, void* o,
+                             void* workspace, size_t workspace_bytes, uint32_t* d_status,
+                             hipStream_t stream) {
+    return attend_common(q, T, heads, cache, block_table, max_pages, cu_q, lens, B, scale, window, w4_scores{}, o,
+                         workspace, workspace_bytes, d_status, stream);
+}
+
+w4_status w4_paged_attention_scores(const void* q, int64_t T, int64_t heads, const w4_kv_cache* cache,
+                                    const int32_t* block_table, int64_t max_pages, const int32_t* cu_q,
+                                    const int32_t* lens, int64_t B, float scale, int64_t window,
+                                    const w4_scores* scores, void* o, void* workspace, size_t workspace_bytes,
+                                    uint32_t* d_status, hipStream_t stream) {
+    if (!scores) return W4_ERR_NULL;
+    return attend_common(q, T, heads, cache, block_table, max_pages, cu_q, lens, B, scale, window, *scores, o,
+                         workspace, workspace_bytes, d_status, stream);
 }
 
 w4_status w4_stream_read(const void* buf, size_t bytes, uint32_t* sink, hipStream_t stream) {

@@ -1,0 +1,317 @@
+// The INT8 cache: rows written as codes with one scale for each block of 16 rows (of a page and kv head),
+// and the rows of any cache read back as values.
+//
+// Write: with m the largest magnitude that a call writes into a block, old the block's scale (0 where its
+// first row is written, for the block then begins anew) and S = m / 127 in binary64 if that is larger than old,
+// else old:   scale = S, code = round(y / S), and of the block's other rows, where the scale has grown,
+// code = round(code / (S / old)).  All quotients are those of binary64 (a new block's codes are the row
+// quantizer's for its 16 rows as one); w4_codes.h has them from a binary32 reciprocal where no half is near.
+//
+// One wave takes a block of one kv head, K or V: D / 16 lanes a row, so that all 16 rows are in registers, the
+// largest value is found by shuffles and a row is either written from its token or, where the scale grows,
+// rescaled.  The tokens of a block stand next to each other in the batch, so the workgroup of token t serves
+// the block that begins with it and ends at once where the token before it lies in the same block.  The query
+// heads of a token are other workgroups of the same launch.
+#include "w4_codes.h"
+#include "w4_internal.h"
+#include "w4_paging.h"
+
+namespace w4 {
+namespace {
+
+constexpr int kBlockRows = 16;
+constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr int kMaxPairs = 64;   // head_dim 128
+constexpr float kLeastMax = 0x1p-93f;                        // a block below it counts as zeros
+constexpr float kLeastScale = 0x1p-100f;                     // below kLeastMax / 127
+
+__device__ __forceinline__ uint32_t bf16_pair2(float a, float b) {
+    typedef float f2_t __attribute__((ext_vector_type(2)));
+    typedef __bf16 b2_t __attribute__((ext_vector_type(2)));
+    const f2_t f = {a, b};
+    const b2_t h = __builtin_convertvector(f, b2_t);
+    return __builtin_bit_cast(uint32_t, h);
+}
+
+__device__ __forceinline__ u32x4_t bf16_of8(const float* v) {
+    u32x4_t a;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) a[q] = bf16_pair2(v[2 * q], v[2 * q + 1]);
+    return a;
+}
+
+__device__ __forceinline__ void values_of8(uint2 c, float* v) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        v[q] = (float)(int8_t)(c.x >> (8 * q));
+        v[4 + q] = (float)(int8_t)(c.y >> (8 * q));
+    }
+}
+
+// The 16 elements of a head that a lane holds: pairs of a rotation are within it.
+struct Chunks {
+    int c0, c1;   // two runs of 8
+    bool turns;
+};
+__device__ __forceinline__ Chunks chunks_of(const RopeArgs& a, int u) {
+    Chunks c;
+    c.turns = u < (a.rotary >> 4);
+    const bool split = c.turns && !a.interleaved;
+    c.c0 = split ? 8 * u : 16 * u;
+    c.c1 = split ? 8 * u + (a.rotary >> 1) : 16 * u + 8;
+    return c;
+}
+
+__device__ __forceinline__ void turn(const RopeArgs& a, const float* cs, const float* sn, int u, float* v) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float c = cs[8 * u + j], s = sn[8 * u + j];
+        if (a.interleaved) {
+            const float x0 = v[2 * j], x1 = v[2 * j + 1];
+            v[2 * j] = x0 * c - x1 * s;
+            v[2 * j + 1] = x0 * s + x1 * c;
+        } else {
+            const float x0 = v[j], x1 = v[8 + j];
+            v[j] = x0 * c - x1 * s;
+            v[8 + j] = x0 * s + x1 * c;
+        }
+    }
+}
+
+// Cosines and sines of the pairs of n tokens from t on.
+__device__ __forceinline__ void angles(const RopeArgs& a, int64_t t, int n, float (*cs)[kMaxPairs], float (*sn)[kMaxPairs]) {
+    const int pair = threadIdx.x & (kMaxPairs - 1);
+    if (pair >= a.rotary >> 1) return;
+    for (int i = threadIdx.x / kMaxPairs; i < n; i += kThreads / kMaxPairs) {
+        const double turns = (double)a.positions[t + i] * a.freqs[pair] * 0.15915494309189533577;
+        const float part = (float)(turns - rint(turns));     // [-1/2, 1/2]
+        float s, c;
+        sincospif(2.0f * part, &s, &c);
+        cs[i][pair] = c * a.amplitude;
+        sn[i][pair] = s * a.amplitude;
+    }
+}
+
+// Query heads of token t.
+template <bool XF32>
+__device__ __forceinline__ void write_q(const RopeArgs& a, int64_t t, int part, float (*cs)[kMaxPairs], float (*sn)[kMaxPairs]) {
+    const int lanes = a.head_dim >> 4;
+    const int item = part * kThreads + threadIdx.x, head = item / lanes, u = item & (lanes - 1);
+    const int64_t slot = a.slots[t];
+    const Chunks c = chunks_of(a, u);
+    float v[16];
+    const bool active = head < a.heads;
+    if (active) {
+        const int64_t from = (t * (a.heads + 2 * a.kv_heads) + head) * a.head_dim;
+        load8<!XF32>(a.qkv, from + c.c0, v);
+        load8<!XF32>(a.qkv, from + c.c1, v + 8);
+    }
+    angles(a, t, 1, cs, sn);
+    __syncthreads();
+    if (slot < 0 || slot >= a.pages << a.page_shift || !active) return;
+    if (c.turns) turn(a, cs[0], sn[0], u, v);
+    uint16_t* q = a.q + (t * a.heads + head) * a.head_dim;
+    *reinterpret_cast<u32x4_t*>(q + c.c0) = bf16_of8(v);
+    *reinterpret_cast<u32x4_t*>(q + c.c1) = bf16_of8(v + 8);
+}
+
+// The block that begins with token t: heads of K and V, wave by wave.
+template <bool XF32, int D>
+__device__ __forceinline__ void write_block(const RopeArgs& a, int64_t t, int part, int parts, float (*cs)[kMaxPairs],
+                                            float (*sn)[kMaxPairs]) {
+    constexpr int kLanes = D / 16, kGroups = 64 / kLanes, kRows = kBlockRows / kGroups;   // rows of a lane
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t slot = a.slots[t], block = slot >> 4;
+    if (slot < 0 || (t > 0 && a.slots[t - 1] >> 4 == block)) return;
+    if (slot >= a.pages << a.page_shift) {
+        if (part == 0 && threadIdx.x == 0 && a.status) atomicOr(a.status, kStatusPage);
+        return;
+    }
+    // the tokens that follow in the same block, and their rows
+    const int64_t near = t + (lane & 15);
+    const int64_t theirs = near < a.T ? a.slots[near] : -1;
+    const uint64_t others = ~__ballot(theirs >> 4 == block) & 0xFFFF;
+    const int n = others ? __builtin_ctzll(others) : kBlockRows;
+    const int row_of = (int)theirs & 15;
+    const bool anew = __any(lane < n && row_of == 0);
+    const int group = lane / kLanes, u = lane % kLanes;
+    int token[kRows];                                        // of my rows; -1: not written
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) token[i] = -1;
+    for (int j = 0; j < n; ++j) {
+        const int r = __builtin_amdgcn_readlane(row_of, j);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+            if (r == i * kGroups + group) token[i] = j;
+    }
+    if (a.rotary > 0) {
+        angles(a, t, n, cs, sn);
+        __syncthreads();
+    }
+    const Chunks ck = chunks_of(a, u);
+    const int page_rows = 1 << a.page_shift;
+    for (int item = part * kWaves + wave; item < 2 * a.kv_heads; item += parts * kWaves) {
+        const bool is_v = item >= a.kv_heads;
+        const int kvh = item - (is_v ? a.kv_heads : 0);
+        const Chunks c = is_v ? Chunks{16 * u, 16 * u + 8, false} : ck;
+        const int64_t row0 = (((slot >> a.page_shift) * a.kv_heads + kvh) << a.page_shift) + (slot & (page_rows - 1) & ~15);
+        float* scale = (is_v ? a.v_scales : a.k_scales) + (row0 >> 4);
+        uint8_t* codes = static_cast<uint8_t*>(is_v ? a.v : a.k) + row0 * D;
+        float v[kRows][16];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            if (token[i] >= 0) {
+                const int64_t from = ((t + token[i]) * (a.heads + 2 * a.kv_heads) + a.heads + item) * D;
+                load8<!XF32>(a.qkv, from + c.c0, v[i]);
+                load8<!XF32>(a.qkv, from + c.c1, v[i] + 8);
+            }
+        }
+        float old = anew ? 0.0f : *scale;
+        old = old >= kLeastScale && old < __builtin_huge_valf() ? old : 0.0f;
+        float most = 0.0f;
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            if (token[i] < 0) continue;
+            if (c.turns) turn(a, cs[token[i]], sn[token[i]], u, v[i]);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                if (!(fabsf(v[i][j]) < __builtin_huge_valf())) {
+                    bad = true;
+                    v[i][j] = 0.0f;
+                }
+                most = fmaxf(most, fabsf(v[i][j]));
+            }
+        }
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor(most, off));
+        const double need = most < kLeastMax ? 0.0 : (double)most / 127.0;
+        const bool more = (float)need > old;
+        const double S = more ? need : old > 0.0f ? (double)old : 1.0;
+        const float r = (float)(1.0 / S);
+        const bool in_range = S <= 0x1p100;                  // and at least 2^-100
+        if (__any(bad) && lane == 0 && a.status) atomicOr(a.status, kStatusNonfinite);
+        if (lane == 0) *scale = more ? (float)need : old;
+        const bool grown = more && !anew;                    // the same for the wave
+        const double by = grown && old > 0.0f ? S / old : 0x1p60;   // a scale of 0: all codes become 0
+        const float r_by = (float)(1.0 / by);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            uint8_t* row = codes + (i * kGroups + group) * D;
+            if (token[i] >= 0) {
+                *reinterpret_cast<uint2*>(row + c.c0) = w8_codes8_of<true>(v[i], S, r, in_range);
+                *reinterpret_cast<uint2*>(row + c.c1) = w8_codes8_of<true>(v[i] + 8, S, r, in_range);
+            } else if (grown) {
+                const u32x4_t w = *reinterpret_cast<const u32x4_t*>(row + 16 * u);
+                float x[16];
+                values_of8(make_uint2(w[0], w[1]), x);
+                values_of8(make_uint2(w[2], w[3]), x + 8);
+                const uint2 lo = w8_codes8_of<true>(x, by, r_by, by <= 0x1p100);
+                const uint2 hi = w8_codes8_of<true>(x + 8, by, r_by, by <= 0x1p100);
+                *reinterpret_cast<u32x4_t*>(row + 16 * u) = u32x4_t{lo.x, lo.y, hi.x, hi.y};
+            }
+        }
+    }
+}
+
+template <bool XF32, int D>
+__global__ __launch_bounds__(kThreads) void write_blocks_kernel(RopeArgs a, int q_parts, int kv_parts) {
+    __shared__ float cs[kBlockRows][kMaxPairs], sn[kBlockRows][kMaxPairs];
+    const int64_t t = blockIdx.x;
+    if ((int)blockIdx.y < kv_parts)
+        write_block<XF32, D>(a, t, blockIdx.y, kv_parts, cs, sn);
+    else
+        write_q<XF32>(a, t, blockIdx.y - kv_parts, cs, sn);
+}
+
+// --------------------------------------------------------------------------
+// Rows read back
+// --------------------------------------------------------------------------
+//
+// Bound by memory: a lane reads 8 elements and writes 8, four of them in flight.
+
+template <int TYPE, bool F32>
+__global__ __launch_bounds__(kThreads) void cache_read_kernel(ReadArgs a) {
+    const int chunks = 2 * a.kv_heads * (a.head_dim >> 3);   // of a token
+    const int64_t total = a.n * chunks;
+    const int64_t end = a.pages << a.page_shift;
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
+        const int64_t t = i / chunks;
+        const int c = (int)(i - t * chunks);
+        const int64_t slot = a.slots[t];
+        if (slot < 0) continue;                              // padding
+        if (slot >= end) {
+            if (c == 0 && a.status) atomicOr(a.status, kStatusPage);
+            continue;
+        }
+        const int head = c / (a.head_dim >> 3), at = 8 * (c - head * (a.head_dim >> 3));
+        const bool is_v = head >= a.kv_heads;
+        const int64_t row = (((slot >> a.page_shift) * a.kv_heads + head - (is_v ? a.kv_heads : 0)) << a.page_shift) +
+                            (slot & ((1 << a.page_shift) - 1));
+        const void* from = is_v ? a.v : a.k;
+        const float* scales = is_v ? a.v_scales : a.k_scales;
+        float v[8];
+        if constexpr (TYPE == 0) {
+            load8<true>(from, row * a.head_dim + at, v);
+        } else {
+            const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(from) + row * a.head_dim + at);
+            const float s = scales[TYPE == 2 ? row >> 4 : row];
+            if constexpr (TYPE == 2) {
+                values_of8(w, v);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    v[q] = __builtin_amdgcn_cvt_f32_fp8(w.x >> (8 * q), 0);
+                    v[4 + q] = __builtin_amdgcn_cvt_f32_fp8(w.y >> (8 * q), 0);
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] *= s;
+        }
+        if constexpr (F32) {
+            float* to = static_cast<float*>(a.out) + i * 8;
+            *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4*>(to + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(a.out) + i * 8) = bf16_of8(v);
+        }
+    }
+}
+
+}  // namespace
+
+hipError_t launch_write_blocks(const RopeArgs& a, bool x_f32, hipStream_t s) {
+    const int q_parts = (int)ceil_div((int64_t)a.heads * (a.head_dim / 16), kThreads);
+    const int kv_parts = (int)ceil_div(2 * a.kv_heads, kWaves);
+    const dim3 grid((unsigned)a.T, (unsigned)(q_parts + kv_parts)), block(kThreads);
+    if (a.head_dim == 128) {
+        if (x_f32)
+            hipLaunchKernelGGL((write_blocks_kernel<true, 128>), grid, block, 0, s, a, q_parts, kv_parts);
+        else
+            hipLaunchKernelGGL((write_blocks_kernel<false, 128>), grid, block, 0, s, a, q_parts, kv_parts);
+    } else {
+        if (x_f32)
+            hipLaunchKernelGGL((write_blocks_kernel<true, 64>), grid, block, 0, s, a, q_parts, kv_parts);
+        else
+            hipLaunchKernelGGL((write_blocks_kernel<false, 64>), grid, block, 0, s, a, q_parts, kv_parts);
+    }
+    return hipGetLastError();
+}
+
+template <int TYPE>
+static hipError_t launch_read_type(const ReadArgs& a, bool out_f32, hipStream_t s) {
+    const int64_t chunks = a.n * 2 * a.kv_heads * (a.head_dim / 8);
+    const dim3 grid((unsigned)imin(ceil_div(chunks, kThreads), 1 << 20)), block(kThreads);
+    if (out_f32)
+        hipLaunchKernelGGL((cache_read_kernel<TYPE, true>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((cache_read_kernel<TYPE, false>), grid, block, 0, s, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_cache_read(const ReadArgs& a, int type, bool out_f32, hipStream_t s) {
+    if (type == 0) return launch_read_type<0>(a, out_f32, s);
+    return type == 1 ? launch_read_type<1>(a, out_f32, s) : launch_read_type<2>(a, out_f32, s);
+}
+
+}  // namespace w4

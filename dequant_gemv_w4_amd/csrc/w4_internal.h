@@ -203,10 +203,39 @@ struct AttendArgs {
     float scale_log2;    // softmax scale / ln 2
     int narrow_tile, few_tiles, narrow_tiles, wide_tiles, narrow_parts, narrow_fill, wide_parts, wide_fill;
     bool both;           // both kinds of tiles are launched
+    // scores and keys other than the plain causal ones
+    bool ranges;
+    const float* slopes;      // [heads], or none
+    const int32_t* first;     // [T], or none
+    const int32_t* prefix;    // [B], or none
+    // a capped score of a product z, times log2 e: up to |z| = cap_small the series
+    // z (scale_log2 + cap_c3 z^2 + cap_c5 z^4 + cap_c7 z^6), beyond cap_log2 (1 - 2 / (1 + 2^(cap_exp z)));
+    // cap_log2 = 0: no cap
+    float cap_log2, cap_exp, cap_small, cap_c3, cap_c5, cap_c7;
 };
 struct AttendPlan;
 size_t attend_workspace(int64_t D, const AttendPlan& p);
-hipError_t launch_attend(AttendArgs a, int head_dim, bool fp8, const AttendPlan& p, void* workspace,
+// type: W4_CACHE_BF16 0, W4_CACHE_FP8 1, W4_CACHE_INT8 2 (as the kernels number them)
+hipError_t launch_attend(AttendArgs a, int head_dim, int type, const AttendPlan& p, void* workspace,
                          hipStream_t s);
+// of one type of cache; mod: which of the kernels' forms (w4_attention.h)
+hipError_t launch_attend_int8(const AttendArgs& a, int head_dim, int mod, const AttendPlan& p, hipStream_t s);
+hipError_t launch_attend_scores_bf16(const AttendArgs& a, int head_dim, int mod, const AttendPlan& p, hipStream_t s);
+hipError_t launch_attend_scores_fp8(const AttendArgs& a, int head_dim, int mod, const AttendPlan& p, hipStream_t s);
+
+// The write of K and V into an INT8 cache, and the rows of any cache read back.
+hipError_t launch_write_blocks(const RopeArgs& a, bool x_f32, hipStream_t s);
+struct ReadArgs {
+    const void* k;
+    const void* v;
+    const float* k_scales;
+    const float* v_scales;
+    const int64_t* slots;
+    void* out;
+    uint32_t* status;
+    int64_t n, pages;
+    int kv_heads, head_dim, page_shift;
+};
+hipError_t launch_cache_read(const ReadArgs& a, int type, bool out_f32, hipStream_t s);
 
 }  // namespace w4

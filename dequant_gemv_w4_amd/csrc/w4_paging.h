@@ -72,6 +72,19 @@ W4_HD Seq clamp_seq(int32_t cu0, int32_t cu1, int32_t len, int32_t T, int32_t ca
     return s;
 }
 
+// Keys lo .. hi that the row at position pos sees of ctx: those up to itself, with a prefix the first `prefix`
+// ones too; none ahead of `first` (the first of its document) or of its window.  None where hi < lo.
+struct KeyRange {
+    int32_t lo, hi;
+};
+W4_HD KeyRange key_range(int32_t pos, int32_t ctx, int32_t window, int32_t first, int32_t prefix) {
+    KeyRange k;
+    k.hi = greater(pos, lesser(greater(prefix, 0), ctx) - 1);
+    k.lo = greater(0, lesser(first, ctx));                   // ctx: behind every key
+    if (window > 0) k.lo = greater(k.lo, pos - window + 1);
+    return k;
+}
+
 // Keys of a tile of rows [row0, row0 + rows) of a sequence (rows >= 1), and their split:
 // [first, end) is what any row sees, begin is first rounded down to a multiple of kKeyTile; part p of
 // `parts` takes [begin + p * chunk, begin + (p + 1) * chunk).  The parts are cut by the actual
@@ -80,12 +93,10 @@ constexpr int kKeyTile = 64;
 struct Span {
     int32_t first, begin, end, chunk, parts;
 };
-W4_HD Span key_span(const Seq& s, int32_t row0, int32_t rows, int32_t G, int32_t window,
-                    int32_t max_parts, int32_t least) {
+W4_HD Span cut_span(int32_t first, int32_t end, int32_t max_parts, int32_t least) {
     Span k;
-    const int32_t pos0 = s.ctx - s.n;                        // position of the first new token
-    k.end = lesser(s.ctx, pos0 + quotient(row0 + rows - 1, G) + 1);
-    k.first = window > 0 ? greater(0, pos0 + quotient(row0, G) - window + 1) : 0;
+    k.first = first;
+    k.end = end;
     k.begin = k.first / kKeyTile * kKeyTile;
     k.chunk = 2 * least;
     k.parts = 1;
@@ -101,6 +112,12 @@ W4_HD Span key_span(const Seq& s, int32_t row0, int32_t rows, int32_t G, int32_t
         k.chunk = greater(2 * least, (len + kKeyTile - 1) / kKeyTile * kKeyTile);
     }
     return k;
+}
+W4_HD Span key_span(const Seq& s, int32_t row0, int32_t rows, int32_t G, int32_t window,
+                    int32_t max_parts, int32_t least) {
+    const int32_t pos0 = s.ctx - s.n;                        // position of the first new token
+    const int32_t end = lesser(s.ctx, pos0 + quotient(row0 + rows - 1, G) + 1);
+    return cut_span(window > 0 ? greater(0, pos0 + quotient(row0, G) - window + 1) : 0, end, max_parts, least);
 }
 
 // The span without the keys ahead of the 16 that hold the first one seen.  Pages hold a multiple of 16

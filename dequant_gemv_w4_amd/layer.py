@@ -1,5 +1,6 @@
 """Binding of the operators between the products of a decoder layer: the root-mean-square norm, the
-gate, rotary positions with the write into a paged cache, block tables, and paged attention.
+gate, rotary positions with the write into a paged cache, its rows read back, block tables, and paged
+attention.
 
 Argument marshalling only, like the rest of the package; tensors have to be contiguous and on one
 GPU, and a call runs on that GPU's current stream.  A decode step makes hundreds of these calls,
@@ -13,7 +14,7 @@ import ctypes
 
 import torch
 
-from . import W4_BF16, W4_F32, W4Rope, _check, _KVCacheStruct, _require, lib
+from . import W4_BF16, W4_F32, W4Rope, _check, _KVCacheStruct, _require, _ScoresStruct, lib
 
 _FLOATS = (torch.float32, torch.bfloat16)
 _F32, _BF16, _I32, _I64 = (torch.float32,), (torch.bfloat16,), (torch.int32,), (torch.int64,)
@@ -184,35 +185,50 @@ def w4_silu_mul_int8(gate_up, codes=None, scales=None, status=None):
 
 
 class W4KVCache:
-    """A paged cache: k and v [pages, kv_heads, page_size, head_dim], bfloat16, or uint8 (E4M3
-    codes) with float32 scales [pages, kv_heads, page_size].  Keeps its tensors alive."""
+    """A paged cache: k and v [pages, kv_heads, page_size, head_dim], bfloat16; uint8 (E4M3 codes)
+    with float32 scales [pages, kv_heads, page_size]; or int8 with float32 scales [pages, kv_heads,
+    page_size / 16].  Keeps its tensors alive."""
+
+    BLOCK = 16                                                # rows of an int8 cache that share a scale
+    _TYPES = {torch.bfloat16: 0, torch.uint8: 1, torch.int8: 3}
 
     def __init__(self, k, v, k_scales=None, v_scales=None):
-        _require(k, (torch.bfloat16, torch.uint8), None, "k")
+        _require(k, (torch.bfloat16, torch.uint8, torch.int8), None, "k")
         if k.dim() != 4:
             raise ValueError("k must be [pages, kv_heads, page_size, head_dim]")
         index = k.get_device()
         _want(v, (k.dtype,), k.shape, "v", index)
-        fp8 = k.dtype == torch.uint8
-        if fp8:
-            _want(k_scales, _F32, k.shape[:3], "k_scales", index)
-            _want(v_scales, _F32, k.shape[:3], "v_scales", index)
+        if k.dtype != torch.bfloat16:
+            if k.dtype == torch.int8 and k.shape[2] % self.BLOCK:
+                raise ValueError("page_size must be a multiple of 16")
+            shape = self._scales_shape(k.shape, k.dtype)
+            _want(k_scales, _F32, shape, "k_scales", index)
+            _want(v_scales, _F32, shape, "v_scales", index)
         elif k_scales is not None or v_scales is not None:
             raise ValueError("a bfloat16 cache has no scales")
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
         self.pages, self.kv_heads, self.page_size, self.head_dim = k.shape
         self.device, self._index = k.device, index
         self._c = _KVCacheStruct(k.data_ptr(), v.data_ptr(), _opt(k_scales), _opt(v_scales), self.pages,
-                                 self.page_size, self.kv_heads, self.head_dim, int(fp8))
+                                 self.page_size, self.kv_heads, self.head_dim, self._TYPES[k.dtype])
         self._ref = ctypes.byref(self._c)
 
     @classmethod
-    def empty(cls, pages, page_size, kv_heads, head_dim, fp8=False, device="cuda"):
+    def _scales_shape(cls, shape, dtype):
+        return (*shape[:2], shape[2] // cls.BLOCK if dtype == torch.int8 else shape[2])
+
+    @classmethod
+    def empty(cls, pages, page_size, kv_heads, head_dim, fp8=False, device="cuda", int8=False):
         """A cache of that shape (zeros)."""
+        if fp8 and int8:
+            raise ValueError("a cache holds one type")
         shape = (pages, kv_heads, page_size, head_dim)
-        kv = [torch.zeros(shape, dtype=torch.uint8 if fp8 else torch.bfloat16, device=device) for _ in range(2)]
-        scales = [torch.ones(shape[:3], dtype=torch.float32, device=device) if fp8 else None for _ in range(2)]
-        return cls(*kv, *scales)
+        dtype = torch.uint8 if fp8 else torch.int8 if int8 else torch.bfloat16
+        kv = [torch.zeros(shape, dtype=dtype, device=device) for _ in range(2)]
+        if dtype == torch.bfloat16:
+            return cls(*kv)
+        scale = torch.ones if fp8 else torch.zeros
+        return cls(*kv, *[scale(cls._scales_shape(shape, dtype), dtype=torch.float32, device=device) for _ in range(2)])
 
 
 def w4_rope_cache(qkv, cache: W4KVCache, positions, slots, rope: W4Rope, freqs, q=None, status=None):
@@ -238,6 +254,50 @@ def w4_rope_cache(qkv, cache: W4KVCache, positions, slots, rope: W4Rope, freqs, 
     _call("w4_rope_cache", index, x.data_ptr(), _code(x), T, heads, cache._ref, positions.data_ptr(),
           slots.data_ptr(), ctypes.byref(rope), freqs.data_ptr(), q.data_ptr(), _status_ptr(status, index))
     return q
+
+
+def w4_cache_write(qkv, cache: W4KVCache, slots, q=None, status=None):
+    """w4_rope_cache without rotation: store K and V of qkv [T, (heads + 2 kv_heads) * head_dim] at
+    ``slots``; returns q [T, heads, head_dim] bfloat16, or None where qkv holds no query heads."""
+    x = _rows_of(qkv, "qkv")
+    index = cache._index
+    T, width = x.shape
+    d = cache.head_dim
+    heads = width // d - 2 * cache.kv_heads
+    if width % d or heads < 0:
+        raise ValueError("qkv must be [T, (heads + 2 kv_heads) * head_dim]")
+    if x.get_device() != index:
+        raise ValueError(f"cache is on {cache.device}, expected {x.device}")
+    _want(slots, _I64, (T,), "slots", index)
+    if heads == 0:
+        if q is not None:
+            raise ValueError("q without query heads in qkv")
+    elif q is None:
+        q = torch.empty((T, heads, d), dtype=torch.bfloat16, device=x.device)
+    else:
+        _want(q, _BF16, (T, heads, d), "q", index)
+    _call("w4_cache_write", index, x.data_ptr(), _code(x), T, heads, cache._ref, slots.data_ptr(), _opt(q),
+          _status_ptr(status, index))
+    return q
+
+
+def w4_cache_read(cache: W4KVCache, slots, out=None, out_dtype=None, status=None):
+    """Rows of the cache at ``slots`` [n] as values [n, 2 kv_heads * head_dim] (key heads, value heads; what
+    w4_cache_write takes), bfloat16 by default.  Rows of slots that are negative or past the cache are left."""
+    index = cache._index
+    _want(slots, _I64, None, "slots", index)
+    if slots.dim() != 1:
+        raise ValueError("slots must be [n]")
+    shape = (slots.numel(), 2 * cache.kv_heads * cache.head_dim)
+    if out is None:
+        if (out_dtype or torch.bfloat16) not in _FLOATS:
+            raise TypeError(f"out_dtype is {out_dtype}")
+        out = torch.empty(shape, dtype=out_dtype or torch.bfloat16, device=cache.device)
+    else:
+        _want(out, _FLOATS, shape, "out", index)
+    _call("w4_cache_read", index, cache._ref, slots.data_ptr(), shape[0], out.data_ptr(), _code(out),
+          _status_ptr(status, index))
+    return out
 
 
 def w4_block_tables(new_lens, lens, free_pages, free_count, block_table, page_size, tokens=None, lens_out=None,
@@ -301,6 +361,40 @@ def w4_paged_attention(q, cache: W4KVCache, block_table, cu_q, lens, scale, wind
 
     ``cu_q`` [B + 1] and ``lens`` [B] as w4_block_tables gives them (lens counts the new tokens);
     rows of q behind cu_q[B] are left out of o.  The workspace is allocated where it is not given."""
+    return _attend("w4_paged_attention", (), q, cache, block_table, cu_q, lens, scale, window, o, workspace, status)
+
+
+class W4Scores:
+    """Scores and keys other than the plain causal ones: scores capped at ``cap``; ``slopes`` [heads] float32 of
+    a bias by distance; ``first_keys`` [T] int32, the first key that each row of the batch sees (of its
+    document); ``prefix_lens`` [B] int32, tokens at the start of each request that all its rows see.  Keeps its
+    tensors alive."""
+
+    def __init__(self, cap=0.0, slopes=None, first_keys=None, prefix_lens=None):
+        for t, dtypes, name in ((slopes, _F32, "slopes"), (first_keys, _I32, "first_keys"), (prefix_lens, _I32, "prefix_lens")):
+            if t is not None:
+                _require(t, dtypes, None, name)
+        self.cap, self.slopes, self.first_keys, self.prefix_lens = cap, slopes, first_keys, prefix_lens
+        self._c = _ScoresStruct(cap, 0, _opt(slopes), _opt(first_keys), _opt(prefix_lens))
+        self._ref = ctypes.byref(self._c)
+
+
+def w4_paged_attention_scores(q, cache: W4KVCache, block_table, cu_q, lens, scale, scores: W4Scores, window=0, o=None,
+                              workspace=None, status=None):
+    """w4_paged_attention with the scores and keys that ``scores`` asks for; the workspace is of the same size."""
+    index = cache._index
+    _want(q, _BF16, None, "q", index)
+    if scores.slopes is not None:
+        _want(scores.slopes, _F32, tuple(q.shape[1:2]), "slopes", index)
+    if scores.first_keys is not None:
+        _want(scores.first_keys, _I32, tuple(q.shape[:1]), "first_keys", index)
+    if scores.prefix_lens is not None:
+        _want(scores.prefix_lens, _I32, tuple(lens.shape), "prefix_lens", index)
+    return _attend("w4_paged_attention_scores", (scores._ref,), q, cache, block_table, cu_q, lens, scale, window, o, workspace,
+                   status)
+
+
+def _attend(name, scores, q, cache, block_table, cu_q, lens, scale, window, o, workspace, status):
     index = cache._index
     _want(q, _BF16, None, "q", index)
     shape = q.shape
@@ -322,7 +416,7 @@ def w4_paged_attention(q, cache: W4KVCache, block_table, cu_q, lens, scale, wind
         workspace = torch.empty(need, dtype=torch.uint8, device=cache.device) if need else None
     else:
         _want(workspace, _U8, None, "workspace", index)
-    _call("w4_paged_attention", index, q.data_ptr(), T, heads, cache._ref, block_table.data_ptr(),
-          max_pages, cu_q.data_ptr(), lens.data_ptr(), B, scale, window, o.data_ptr(), _opt(workspace),
+    _call(name, index, q.data_ptr(), T, heads, cache._ref, block_table.data_ptr(),
+          max_pages, cu_q.data_ptr(), lens.data_ptr(), B, scale, window, *scores, o.data_ptr(), _opt(workspace),
           0 if workspace is None else workspace.numel(), _status_ptr(status, index))
     return o

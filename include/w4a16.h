@@ -381,12 +381,31 @@ w4_status w4_silu_mul_int8(const void* gate_up, w4_dtype gt, int64_t rows, int64
  * (p * kv_heads + h) * page_size + j of k and v, head_dim elements; a slot is
  * p * page_size + j.
  *   type       W4_CACHE_BF16: bfloat16 rows; W4_CACHE_FP8: E4M3 codes, one binary32 scale per
- *              row in k_scales and v_scales [pages, kv_heads, page_size] (NULL otherwise).
+ *              row in k_scales and v_scales [pages, kv_heads, page_size]; W4_CACHE_INT8: int8
+ *              codes, one binary32 scale per block of W4_CACHE_BLOCK rows in k_scales and v_scales
+ *              [pages, kv_heads, page_size / W4_CACHE_BLOCK] (NULL for bfloat16).  A value is
+ *              code * scale.
  *   page_size  a power of two, 16 to 4096.   head_dim  64 or 128.   kv_heads  1 to 1024.
  * k and v 16-B aligned, scales 4-B.  W4_ERR_UNSUPPORTED for another type, page size or head
  * dimension.  pages >= 1; kv_heads * page_size * pages < 2^40.
+ *
+ * The codes of an INT8 cache, for K and V and each kv head apart.  A call that writes rows of a block
+ * (rows 16 i .. 16 i + 15 of a page) forms, with m the largest magnitude of the values that it writes
+ * there (0 below 2^-93),
+ *   old = 0 where the block's first row is among those written (the block begins anew, whatever it
+ *         held), else the block's scale (0 where that is no finite number of at least 2^-100);
+ *   S = m / 127 in binary64 where that, rounded to binary32, is larger than old, else old;
+ *   scale = S in binary32;   code = y / S in binary64, to the nearest whole number, halves to even;
+ * where the scale has grown and the block goes on, the codes c of its other rows become c / (S / old),
+ * rounded alike (0 for an old of 0); else they are not touched.  So rows written as a whole block get the
+ * codes that w4_int8_quantize_rows gives the 16 of them as one row, and a value is within half a step
+ * (scale / 2) of y; one that its block outgrows g times is within (g + 1) / 2 of the last step.  Values that
+ * are not finite get the code 0 and set W4_STATUS_NONFINITE.  The rows of a block that one call writes
+ * have to stand next to each other in the batch (as w4_block_tables places them; in any order): apart, or
+ * written by two calls at once, they leave the block's codes and scale undefined.
  */
-typedef enum { W4_CACHE_BF16 = 0, W4_CACHE_FP8 = 1 } w4_cache_type;
+#define W4_CACHE_BLOCK 16
+typedef enum { W4_CACHE_BF16 = 0, W4_CACHE_FP8 = 1, W4_CACHE_INT8 = 3 } w4_cache_type;   /* 2: none */
 typedef struct {
     void* k;
     void* v;
@@ -432,7 +451,7 @@ typedef struct {
  *   q          out [T, heads, head_dim] bfloat16; 16-B aligned; must not overlap qkv.
  * Angles are formed in binary64, rotations in binary32, results rounded once: q and a bfloat16
  * cache to nearest even, rows of an E4M3 cache as w4_fp8_quantize_rows with K = head_dim would
- * the binary32 row (d_status: W4_STATUS_NONFINITE).  Requires 1 <= T <= W4_MAX_TOKENS,
+ * the binary32 row (d_status: W4_STATUS_NONFINITE), blocks of an INT8 cache as stated there.  Requires 1 <= T <= W4_MAX_TOKENS,
  * heads a multiple of kv_heads, at most 65536, T * heads < 2^26, rotary_dim <= head_dim.
  */
 typedef enum { W4_ROPE_NONE = 0, W4_ROPE_LINEAR = 1, W4_ROPE_BANDS = 2, W4_ROPE_RAMP = 3 } w4_rope_scaling;
@@ -452,6 +471,25 @@ w4_status w4_rope_cache(const void* qkv, w4_dtype xt, int64_t T, int64_t heads,
                         const w4_kv_cache* cache, const int32_t* positions, const int64_t* slots,
                         const w4_rope* rope, const double* d_freqs, void* q, uint32_t* d_status,
                         hipStream_t stream);
+
+/*
+ * w4_cache_write -- w4_rope_cache without rotation, for models that know positions by a bias of the
+ * scores (w4_paged_attention_scores) or not at all, and to put rows back that w4_cache_read gave.
+ *   heads  as in w4_rope_cache, or 0: qkv is [T, 2 kv_heads * head_dim], there is no q (NULL).
+ * Other arguments, types, rounding and limits as w4_rope_cache.
+ *
+ * w4_cache_read -- the rows of a cache of any type at n slots, as values.
+ *   slots  [n] device; 8-B aligned; a slot may be named more than once.  The row of a negative slot is
+ *          left as it is, and so is that of a slot past the cache, which sets W4_STATUS_PAGE.
+ *   kv     out [n, 2 kv_heads * head_dim] binary32 or bfloat16: the key heads, the value heads, as
+ *          w4_cache_write with heads = 0 takes them; 16-B aligned; must not overlap the cache.
+ * code * scale in binary32, rounded once to a bfloat16 kv; bfloat16 rows exactly.  Requires
+ * 1 <= n <= W4_MAX_TOKENS.  Deterministic.
+ */
+w4_status w4_cache_write(const void* qkv, w4_dtype xt, int64_t T, int64_t heads, const w4_kv_cache* cache,
+                         const int64_t* slots, void* q, uint32_t* d_status, hipStream_t stream);
+w4_status w4_cache_read(const w4_kv_cache* cache, const int64_t* slots, int64_t n, void* kv, w4_dtype yt,
+                        uint32_t* d_status, hipStream_t stream);
 
 /*
  * w4_block_tables -- places the new tokens of a batch of requests in pages, on the device.
@@ -520,6 +558,39 @@ w4_status w4_paged_attention(const void* q, int64_t T, int64_t heads, const w4_k
                              const int32_t* lens, int64_t B, float scale, int64_t window, void* o,
                              void* workspace, size_t workspace_bytes, uint32_t* d_status,
                              hipStream_t stream);
+
+/*
+ * w4_paged_attention_scores -- w4_paged_attention of models whose scores, or the keys that a row sees, are
+ * not the plain causal ones:
+ *   z = scale * q . k_j;   with a cap   z = cap * tanh(z / cap);
+ *   with slopes   z -= slopes[head] * |position - j|;   p_j = exp(z), over the keys lo <= j <= hi with
+ *   hi = position, with prefix_lens at least min(prefix_lens[b], lens[b]) - 1 (the first tokens of request
+ *        b are seen by all of its rows, those ahead of them included);
+ *   lo = 0, with first_keys at least first_keys[t] (t a row of the batch: the first key of its
+ *        document), with a window at least position - window + 1.
+ * A row for which hi < lo gets zeros.  Each of the four may be left out (0 or NULL); a record of zeros asks
+ * for w4_paged_attention.
+ *   cap          0, or scale * 2^-20 <= cap <= scale * 2^20, and then scale <= 256 (else W4_ERR_VALUE).
+ *   slopes       [heads] device binary32, finite.   first_keys  [T] device int32, any values.
+ *   prefix_lens  [B] device int32, any values (negative: none).   4-B aligned.   reserved  0
+ *                (W4_ERR_UNSUPPORTED).
+ * Other arguments, workspace, limits, precision and what is read and written as w4_paged_attention; no page
+ * is looked up that lies wholly ahead of what the rows of a tile see (up to 256 rows of a request), or behind
+ * it.  Distances are held in binary32 (exact up to 2^24); capped scores are within 2^-19 of the largest
+ * score's size.
+ */
+typedef struct {
+    float cap;
+    int32_t reserved;            /* 0 */
+    const float* slopes;
+    const int32_t* first_keys;
+    const int32_t* prefix_lens;
+} w4_scores;
+w4_status w4_paged_attention_scores(const void* q, int64_t T, int64_t heads, const w4_kv_cache* cache,
+                                    const int32_t* block_table, int64_t max_pages, const int32_t* cu_q,
+                                    const int32_t* lens, int64_t B, float scale, int64_t window,
+                                    const w4_scores* scores, void* o, void* workspace, size_t workspace_bytes,
+                                    uint32_t* d_status, hipStream_t stream);
 
 /*
  * w4_stream_read -- measurement probe, not part of the method: reads `bytes` bytes of

@@ -23,3 +23,6 @@ from .layer_oracle import (  # noqa: F401
     bf16_round, residual_sum_ref, rmsnorm_ref, silu_mul_ref, rope_frequencies_ref, rope_ref,
     block_tables_ref, attention_ref,
 )
+from .block_oracle import (  # noqa: F401
+    BLOCK, write_block_ref, write_rows_ref, block_values, key_range_ref, attention_scores_ref,
+)
