@@ -87,14 +87,15 @@ struct Bias {
     int pos;
 };
 
-// The capped score c tanh(z / c) log2 e of a product z (z / c = z * cap_in).  Up to kCapSmall its odd series,
-// whose next term is below 2^-21 of the score there; beyond, c (1 - 2 / (1 + exp(2 z / c))), off by about 2^-22 c, so
-// 2^-20 of the score: near zero that difference would lose the score.
-constexpr float kCapSmall = 0.25f;
-__device__ __forceinline__ float cap_small(const AttendArgs& a, float z) {
+// The capped score c tanh(z / c) log2 e of a product z (z / c = z * cap_in).  Up to a quarter of c by the odd
+// polynomial of degree 5 that meets tanh(y) / y at three Chebyshev nodes in y^2, within 2^-21 of the score (its last
+// coefficient is positive, so that it takes a masked product, -inf, to -inf); beyond, c (1 - 2 / (1 + exp(2 z / c))), off by
+// about 2^-22 c, so 2^-20 of the score: near zero that difference would lose the score.
+__device__ __forceinline__ float cap_factor(const AttendArgs& a, float z) {
     const float w = z * z;
-    return z * fmaf(w, fmaf(w, fmaf(w, a.cap_c7, a.cap_c5), a.cap_c3), a.scale_log2);
+    return fmaf(w, fmaf(w, a.cap_c5, a.cap_c3), a.cap_c1);
 }
+__device__ __forceinline__ float cap_small(const AttendArgs& a, float z) { return z * cap_factor(a, z); }
 __device__ __forceinline__ float cap_large(const AttendArgs& a, float z) {
     const float e = exp2_fast(z * a.cap_exp);
     return fmaf(-2.0f * a.cap_log2, __builtin_amdgcn_rcpf(e + 1.0f), a.cap_log2);
@@ -123,14 +124,24 @@ __device__ __forceinline__ void shape_scores(const AttendArgs& a, V (&z)[NB], Bi
         }
     }
     if constexpr (MOD & kBias) {
-        const float from = (float)(first - bias.pos);
+        const float from = (float)(first - bias.pos), base = bias.slope * from;
+        if (a.prefix == nullptr) {                           // no row sees a key behind its position
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                const float score = (MOD & kCap) ? z[b][r] : z[b][r] * a.scale_log2;
-                z[b][r] = fmaf(-bias.slope, fabsf(from + (float)at(b, r)), score);
-            }
+                for (int r = 0; r < NR; ++r) {
+                    const float t = fmaf(bias.slope, (float)at(b, r), base);
+                    z[b][r] = (MOD & kCap) ? z[b][r] + t : fmaf(z[b][r], a.scale_log2, t);
+                }
+        } else {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    const float score = (MOD & kCap) ? z[b][r] : z[b][r] * a.scale_log2;
+                    z[b][r] = fmaf(-bias.slope, fabsf(from + (float)at(b, r)), score);
+                }
+        }
     }
 }
 template <int MOD>
@@ -290,15 +301,26 @@ __device__ __forceinline__ float quarter_max(float x) {
 }
 
 // weights: the running maximum and sum, and the bfloat16 weights p (as the right operand of 16 keys
-// each: p[4 c .. 4 c + 3]).  ks, vs: LDS addresses of the scales of the keys' and values' rows, from
-// row 4 half on (codes); first: position of the first key; the row sees the `count` keys from lo; mask:
-// whether the step reaches outside some row's.
+// each: p[4 c .. 4 c + 3]).  E4M3: ks, vs are the LDS addresses of the scales of the keys' and values' rows, from
+// row 4 half on.  INT8: ks is that of the scales of the four blocks of 16 keys, behind them of their values the
+// binary logarithms and their inverses: a block's scale multiplies in the exponent, so that its 16 keys cost
+// nothing of their own, and what it adds to the weights' sum is taken out of the block's sum.  first: position of
+// the first key; the row sees the `count` keys from lo; mask: whether the step reaches outside some row's.
 template <int D, int TYPE, int MOD>
 __device__ __forceinline__ void weights(Rows<D>& s, f32x16_t (&z)[2], uint32_t (&p)[16], uint32_t ks, uint32_t vs,
                                         const AttendArgs& a, int first, int lo, int count, Bias bias, bool mask) {
+    constexpr bool BLOCKS = TYPE == kInt8Rows, CAP_ONLY = (MOD & kCap) && !(MOD & kBias);
     const int half = (threadIdx.x & 63) >> 5;
     const float scale = kShaped<MOD> ? 1.0f : a.scale_log2;
-    if constexpr (kCodes<TYPE>) {
+    f32x4_t kb, lv, iv;
+    if constexpr (BLOCKS) {
+        kb = read_lds_f32x4(ks);
+        lv = read_lds_f32x4(ks + 16);
+        iv = read_lds_f32x4(ks + 32);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) kb[c] *= scale;
+    }
+    if constexpr (TYPE == kFp8Rows) {
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -308,8 +330,29 @@ __device__ __forceinline__ void weights(Rows<D>& s, f32x16_t (&z)[2], uint32_t (
                 for (int j = 0; j < 4; ++j) z[b][4 * i + j] *= f[j];
             }
     }
-    if constexpr (kShaped<MOD>)
+    if constexpr (BLOCKS && kShaped<MOD>) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) z[b][r] *= kb[2 * b + r / 8];
+    }
+    bool large = false;                                      // CAP_ONLY: z holds scores
+    if constexpr (CAP_ONLY) {
+        float most = 0.0f;
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) most = fmaxf(most, fabsf(z[b][r]));
+        large = __any(most > a.cap_small);
+        if (large) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) z[b][r] = cap_large(a, z[b][r]);
+        }
+    } else if constexpr (kShaped<MOD>) {
         shape_scores<MOD, 2, 16>(a, z, bias, first + 4 * half, [](int b, int r) { return 32 * b + 8 * (r >> 2) + (r & 3); });
+    }
     if (mask) {
         const uint32_t from = (uint32_t)(first + 4 * half - lo);
 #pragma unroll
@@ -318,12 +361,26 @@ __device__ __forceinline__ void weights(Rows<D>& s, f32x16_t (&z)[2], uint32_t (
             for (int r = 0; r < 16; ++r)
                 if (from + (32 * b + 8 * (r >> 2) + (r & 3)) >= (uint32_t)count) z[b][r] = kNegInf;
     }
-    float mx = z[0][0];
+    float mx;
+    if constexpr (BLOCKS && !kShaped<MOD>) {
+        mx = kNegInf;
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+        for (int c = 0; c < 4; ++c) {
+            float most = z[c / 2][8 * (c % 2)];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) mx = fmaxf(mx, z[b][r]);
-    mx = half_max(mx) * scale;                               // scale > 0
+            for (int r = 1; r < 8; ++r) most = fmaxf(most, z[c / 2][8 * (c % 2) + r]);
+            mx = fmaxf(mx, most * kb[c]);
+        }
+        mx = half_max(mx);
+    } else {
+        mx = z[0][0];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) mx = fmaxf(mx, z[b][r]);
+        mx = half_max(mx) * scale;                           // scale > 0
+        if (CAP_ONLY && !large) mx = cap_small(a, mx);       // which rises with the product
+    }
     if (__any(mx > s.m + kSlack)) {
         const float m = fmaxf(s.m, mx);
         const float f = m == s.m ? 1.0f : exp2_fast(s.m - m);
@@ -335,26 +392,48 @@ __device__ __forceinline__ void weights(Rows<D>& s, f32x16_t (&z)[2], uint32_t (
             for (int r = 0; r < 16; ++r) s.o[i][r] *= f;
     }
     const float sub = s.m == kNegInf ? 0.0f : s.m;           // nothing seen yet: every weight is 0
-    float sum[2] = {0.0f, 0.0f};
+    float off[4];
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-        f32x4_t f = {1.0f, 1.0f, 1.0f, 1.0f};
+    for (int c = 0; c < 4; ++c) off[c] = BLOCKS ? lv[c] - sub : -sub;
+    auto weigh = [&](auto exponent) {
+        float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float e0 = exp2_fast(fmaf(z[b][2 * i], scale, -sub));
-            const float e1 = exp2_fast(fmaf(z[b][2 * i + 1], scale, -sub));
-            sum[0] += e0;
-            sum[1] += e1;
-            float w0 = e0, w1 = e1;
-            if constexpr (kCodes<TYPE>) {
-                if ((i & 1) == 0) f = read_lds_f32x4(vs + 4 * (32 * b + 4 * i));
-                w0 *= f[2 * (i & 1)];
-                w1 *= f[2 * (i & 1) + 1];
+        for (int b = 0; b < 2; ++b) {
+            f32x4_t f = {1.0f, 1.0f, 1.0f, 1.0f};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int c = 2 * b + i / 4;                 // the block of 16 keys
+                const float e0 = exp2_fast(exponent(z[b][2 * i], c));
+                const float e1 = exp2_fast(exponent(z[b][2 * i + 1], c));
+                sum[0] += e0;
+                sum[1] += e1;
+                float w0 = e0, w1 = e1;
+                if constexpr (TYPE == kFp8Rows) {
+                    if ((i & 1) == 0) f = read_lds_f32x4(vs + 4 * (32 * b + 4 * i));
+                    w0 *= f[2 * (i & 1)];
+                    w1 *= f[2 * (i & 1) + 1];
+                }
+                p[8 * b + i] = bf16_pair(w0, w1);
+                if constexpr (BLOCKS) {
+                    if ((i & 3) == 3) {
+                        s.l = fmaf(sum[0] + sum[1], iv[c], s.l);
+                        sum[0] = sum[1] = 0.0f;
+                    }
+                }
             }
-            p[8 * b + i] = bf16_pair(w0, w1);
         }
+        if constexpr (!BLOCKS) s.l += sum[0] + sum[1];
+    };
+    if constexpr (CAP_ONLY) {
+        if (large)
+            weigh([&](float x, int c) { return x + off[c]; });
+        else
+            weigh([&](float x, int c) { return fmaf(x, cap_factor(a, x), off[c]); });
+    } else if constexpr (kShaped<MOD>) {
+        weigh([&](float x, int c) { return x + off[c]; });
+    } else {
+        weigh([&](float x, int c) { return fmaf(x, BLOCKS ? kb[c] : scale, off[c]); });
     }
-    s.l += sum[0] + sum[1];
 }
 
 // accumulate: O += V p for the staged values vt.
@@ -941,14 +1020,22 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, uint32_t index,
     const uint32_t lane_v = crow16 * kRowBytes + (CODES ? 16 * chunk : v_place<D>(crow, chunk) - crow * 2 * D);
     const uint32_t lds_k = lds_address(&kt[0][0]) + wave * 1024, lds_v = lds_address(&vt[0][0]) + wave * 1024;
     u32x4_t kw, vw;
-    float sc = 1.0f;
+    float sc = 1.0f, sc_v = 1.0f;
+    bool no_v = false;                                       // INT8: the values staged next have a scale of 0
     auto bring = [&](int i, bool values) {
         const uint8_t* from = values ? rows.v : rows.k;
         const uint32_t lane_byte = values ? lane_v : lane_k;
         if constexpr (CODES) {
             static_assert(!CODES || kLoads == 1, "one row a thread");
             (values ? vw : kw) = load16(from, off[0], lane_byte);
-            if (!values) sc = (chunk & 1 ? rows.vs : rows.ks)[(off[0] / kRowBytes + crow16) >> kScaleShift<TYPE>];
+            if (!values) {
+                if constexpr (TYPE == kInt8Rows) {           // the rows of a wave's load lie in one block
+                    sc = rows.ks[off[0] / kRowBytes >> 4];
+                    sc_v = rows.vs[off[0] / kRowBytes >> 4];
+                } else {
+                    sc = (chunk & 1 ? rows.vs : rows.ks)[off[0] / kRowBytes + crow16];
+                }
+            }
         } else {
             const uint32_t lds = (values ? lds_v : lds_k) + (i % kWideStages) * kTileBytes;
             if (left(i) >= kKeyTile) {
@@ -971,10 +1058,25 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, uint32_t index,
         int at = i % kWideStages;
         asm volatile("" : "+s"(at));                         // addresses formed here, not kept for every place
         if (values) {
+            if (TYPE == kInt8Rows && no_v) vw = u32x4_t{0u, 0u, 0u, 0u};
             stage<D, TYPE, true>(vt[at], crow, chunk, vw, left(i));
         } else {
             stage<D, TYPE, false>(kt[at], crow, chunk, kw, left(i));
-            if (chunk < 2) sc_lds[chunk][at][crow] = crow < left(i) ? sc : 1.0f;
+            if constexpr (TYPE == kInt8Rows) {
+                // A scale of 0: any that is not 0 for the keys, whose scores then are 0 as well (2^-100 times a score,
+                // should a cache made elsewhere hold codes under it), 1 for the values, whose codes are staged as zeros.
+                no_v = sc_v == 0.0f;
+                if (crow16 == 0 && chunk == 0) {
+                    const bool in = crow < left(i);
+                    const float lv = in && !no_v ? __builtin_amdgcn_logf(sc_v) : 0.0f;
+                    float* to = &sc_lds[0][at][crow >> 4];
+                    to[0] = !in ? 1.0f : sc == 0.0f ? 0x1p-100f : sc;
+                    to[4] = lv;
+                    to[8] = exp2_fast(-lv);
+                }
+            } else if (chunk < 2) {
+                sc_lds[chunk][at][crow] = crow < left(i) ? sc : 1.0f;
+            }
         }
     };
     // Waits for this wave's LDS accesses and then for the other waves; loads of the cache stay in
@@ -1008,7 +1110,7 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, uint32_t index,
     // written over by those of tile i+4 in phase 2i+5 at the earliest.
     constexpr int kAhead = CODES ? 1 : 2;                    // pairs in flight
     const int behind = wave >> 2;                            // 1 for waves 4-7
-    uint32_t sc_lane = lds_address(&sc_lds[0][0][0]) + 16 * (lane >> 5);
+    uint32_t sc_lane = lds_address(&sc_lds[0][0][0]) + (TYPE == kInt8Rows ? 0 : 16 * (lane >> 5));
     asm volatile("" : "+v"(sc_lane));                        // one register for all places
     f32x16_t z[2];
     uint32_t pw[16];

@@ -5,7 +5,7 @@
 // first row is written, for the block then begins anew) and S = m / 127 in binary64 if that is larger than old,
 // else old:   scale = S, code = round(y / S), and of the block's other rows, where the scale has grown,
 // code = round(code / (S / old)).  All quotients are those of binary64 (a new block's codes are the row
-// quantizer's for its 16 rows as one); w4_codes.h has them from a binary32 reciprocal where no half is near.
+// quantizer's for its 16 rows as one).
 //
 // One wave takes a block of one kv head, K or V: D / 16 lanes a row, so that all 16 rows are in registers, the
 // largest value is found by shuffles and a row is either written from its token or, where the scale grows,
@@ -38,6 +38,43 @@ __device__ __forceinline__ u32x4_t bf16_of8(const float* v) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) a[q] = bf16_pair2(v[2 * q], v[2 * q + 1]);
     return a;
+}
+
+// What codes are divided by: S, and 1 / S correctly rounded to binary64 and binary32.
+struct Step {
+    double s, r;
+    float r32;
+    __device__ explicit Step(double by) : s(by), r(1.0 / by), r32((float)r) {}
+};
+
+// round(v / S) of 8 values as bytes, |v / S| <= 128.  fma(v, r32, 1.5 * 2^23) has the nearest whole number in its
+// low bits and what it leaves tells how near a half is; v * r32 is within 128 * 2^-23 of v / S, so only nearer than
+// 2^-15 the binary64 quotient has to decide.  That quotient in three operations: with r the rounded reciprocal and
+// q = v r, q + (v - q S) r rounds to the correctly rounded v / S (Markstein).
+__device__ __forceinline__ uint2 int8_codes8(const float* v, const Step& by) {
+    uint32_t w[2];
+    float far = 0.0f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t b[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float x = v[4 * h + q], i = fmaf(x, by.r32, 0x1.8p23f);
+            b[q] = __float_as_uint(i);
+            far = fmaxf(far, fabsf(fmaf(x, by.r32, 0x1.8p23f - i)));
+        }
+        w[h] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[3], b[2], 0x0c0c0400u),
+                                     __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u), 0x05040100u);
+    }
+    if (far >= 0.5f - 0x1p-15f) {
+        w[0] = w[1] = 0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const double x = v[q], t = x * by.r;
+            w[q >> 2] |= (uint32_t)(uint8_t)(int8_t)(int)rint(fma(fma(-t, by.s, x), by.r, t)) << (8 * (q & 3));
+        }
+    }
+    return make_uint2(w[0], w[1]);
 }
 
 __device__ __forceinline__ void values_of8(uint2 c, float* v) {
@@ -115,14 +152,13 @@ __device__ __forceinline__ void write_q(const RopeArgs& a, int64_t t, int part, 
     *reinterpret_cast<u32x4_t*>(q + c.c1) = bf16_of8(v + 8);
 }
 
-// The block that begins with token t: heads of K and V, wave by wave.
+// The block that begins with token t, in slot `slot`: heads of K and V, wave by wave.
 template <bool XF32, int D>
-__device__ __forceinline__ void write_block(const RopeArgs& a, int64_t t, int part, int parts, float (*cs)[kMaxPairs],
-                                            float (*sn)[kMaxPairs]) {
+__device__ __forceinline__ void write_block(const RopeArgs& a, int64_t t, int64_t slot, int part, int parts,
+                                            float (*cs)[kMaxPairs], float (*sn)[kMaxPairs]) {
     constexpr int kLanes = D / 16, kGroups = 64 / kLanes, kRows = kBlockRows / kGroups;   // rows of a lane
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t slot = a.slots[t], block = slot >> 4;
-    if (slot < 0 || (t > 0 && a.slots[t - 1] >> 4 == block)) return;
+    const int64_t block = slot >> 4;
     if (slot >= a.pages << a.page_shift) {
         if (part == 0 && threadIdx.x == 0 && a.status) atomicOr(a.status, kStatusPage);
         return;
@@ -145,6 +181,7 @@ __device__ __forceinline__ void write_block(const RopeArgs& a, int64_t t, int pa
             if (r == i * kGroups + group) token[i] = j;
     }
     if (a.rotary > 0) {
+        __syncthreads();                                     // those of the block before are read
         angles(a, t, n, cs, sn);
         __syncthreads();
     }
@@ -187,41 +224,55 @@ __device__ __forceinline__ void write_block(const RopeArgs& a, int64_t t, int pa
         for (int off = 32; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor(most, off));
         const double need = most < kLeastMax ? 0.0 : (double)most / 127.0;
         const bool more = (float)need > old;
-        const double S = more ? need : old > 0.0f ? (double)old : 1.0;
-        const float r = (float)(1.0 / S);
-        const bool in_range = S <= 0x1p100;                  // and at least 2^-100
+        const Step S(more ? need : old > 0.0f ? (double)old : 1.0);
         if (__any(bad) && lane == 0 && a.status) atomicOr(a.status, kStatusNonfinite);
         if (lane == 0) *scale = more ? (float)need : old;
         const bool grown = more && !anew;                    // the same for the wave
-        const double by = grown && old > 0.0f ? S / old : 0x1p60;   // a scale of 0: all codes become 0
-        const float r_by = (float)(1.0 / by);
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
             uint8_t* row = codes + (i * kGroups + group) * D;
             if (token[i] >= 0) {
-                *reinterpret_cast<uint2*>(row + c.c0) = w8_codes8_of<true>(v[i], S, r, in_range);
-                *reinterpret_cast<uint2*>(row + c.c1) = w8_codes8_of<true>(v[i] + 8, S, r, in_range);
+                *reinterpret_cast<uint2*>(row + c.c0) = int8_codes8(v[i], S);
+                *reinterpret_cast<uint2*>(row + c.c1) = int8_codes8(v[i] + 8, S);
             } else if (grown) {
                 const u32x4_t w = *reinterpret_cast<const u32x4_t*>(row + 16 * u);
                 float x[16];
                 values_of8(make_uint2(w[0], w[1]), x);
                 values_of8(make_uint2(w[2], w[3]), x + 8);
-                const uint2 lo = w8_codes8_of<true>(x, by, r_by, by <= 0x1p100);
-                const uint2 hi = w8_codes8_of<true>(x + 8, by, r_by, by <= 0x1p100);
+                const Step by(old > 0.0f ? S.s / old : 0x1p60);   // a scale of 0: all codes become 0
+                const uint2 lo = int8_codes8(x, by), hi = int8_codes8(x + 8, by);
                 *reinterpret_cast<u32x4_t*>(row + 16 * u) = u32x4_t{lo.x, lo.y, hi.x, hi.y};
             }
         }
     }
 }
 
+// Workgroups of blocks first: of the `window` tokens from window * w on, those that begin one, one after the other.
+struct WriteGrid {
+    int window, q_parts, kv_parts;
+    uint32_t blocks, all;   // workgroups of blocks; of all
+};
 template <bool XF32, int D>
-__global__ __launch_bounds__(kThreads) void write_blocks_kernel(RopeArgs a, int q_parts, int kv_parts) {
+__global__ __launch_bounds__(kThreads) void write_blocks_kernel(RopeArgs a, WriteGrid g) {
     __shared__ float cs[kBlockRows][kMaxPairs], sn[kBlockRows][kMaxPairs];
-    const int64_t t = blockIdx.x;
-    if ((int)blockIdx.y < kv_parts)
-        write_block<XF32, D>(a, t, blockIdx.y, kv_parts, cs, sn);
-    else
-        write_q<XF32>(a, t, blockIdx.y - kv_parts, cs, sn);
+    const uint32_t number = blockIdx.y * gridDim.x + blockIdx.x;
+    if (number >= g.all) return;
+    if (number >= g.blocks) {
+        const uint32_t q = number - g.blocks, t = q / (uint32_t)g.q_parts;
+        write_q<XF32>(a, t, (int)(q - t * g.q_parts), cs, sn);
+        return;
+    }
+    const uint32_t w = number / (uint32_t)g.kv_parts;
+    const int part = (int)(number - w * g.kv_parts), lane = threadIdx.x & 63;
+    const int64_t t0 = (int64_t)w * g.window, t = t0 + lane;
+    const int64_t slot = lane < g.window && t < a.T ? a.slots[t] : -1;
+    const int64_t before = slot >= 0 && t > 0 ? a.slots[t - 1] : -1;
+    uint64_t begin = __ballot(slot >= 0 && slot >> 4 != before >> 4);
+    while (begin) {
+        const int i = __builtin_ctzll(begin);
+        begin &= begin - 1;
+        write_block<XF32, D>(a, t0 + i, __shfl(slot, i), part, g.kv_parts, cs, sn);
+    }
 }
 
 // --------------------------------------------------------------------------
@@ -281,19 +332,24 @@ __global__ __launch_bounds__(kThreads) void cache_read_kernel(ReadArgs a) {
 }  // namespace
 
 hipError_t launch_write_blocks(const RopeArgs& a, bool x_f32, hipStream_t s) {
-    const int q_parts = (int)ceil_div((int64_t)a.heads * (a.head_dim / 16), kThreads);
-    const int kv_parts = (int)ceil_div(2 * a.kv_heads, kWaves);
-    const dim3 grid((unsigned)a.T, (unsigned)(q_parts + kv_parts)), block(kThreads);
+    WriteGrid g;
+    g.window = a.T <= 1024 ? 1 : kBlockRows;
+    g.q_parts = (int)ceil_div((int64_t)a.heads * (a.head_dim / 16), kThreads);
+    g.kv_parts = (int)ceil_div(2 * a.kv_heads, kWaves);
+    g.blocks = (uint32_t)(ceil_div(a.T, g.window) * g.kv_parts);
+    g.all = g.blocks + (uint32_t)(a.T * g.q_parts);
+    const int64_t x = imin(g.all, 1 << 20);                  // a dimension of a grid holds less than 2^32 threads
+    const dim3 grid((unsigned)x, (unsigned)ceil_div(g.all, x)), block(kThreads);
     if (a.head_dim == 128) {
         if (x_f32)
-            hipLaunchKernelGGL((write_blocks_kernel<true, 128>), grid, block, 0, s, a, q_parts, kv_parts);
+            hipLaunchKernelGGL((write_blocks_kernel<true, 128>), grid, block, 0, s, a, g);
         else
-            hipLaunchKernelGGL((write_blocks_kernel<false, 128>), grid, block, 0, s, a, q_parts, kv_parts);
+            hipLaunchKernelGGL((write_blocks_kernel<false, 128>), grid, block, 0, s, a, g);
     } else {
         if (x_f32)
-            hipLaunchKernelGGL((write_blocks_kernel<true, 64>), grid, block, 0, s, a, q_parts, kv_parts);
+            hipLaunchKernelGGL((write_blocks_kernel<true, 64>), grid, block, 0, s, a, g);
         else
-            hipLaunchKernelGGL((write_blocks_kernel<false, 64>), grid, block, 0, s, a, q_parts, kv_parts);
+            hipLaunchKernelGGL((write_blocks_kernel<false, 64>), grid, block, 0, s, a, g);
     }
     return hipGetLastError();
 }

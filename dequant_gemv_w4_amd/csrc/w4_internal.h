@@ -209,9 +209,9 @@ struct AttendArgs {
     const int32_t* first;     // [T], or none
     const int32_t* prefix;    // [B], or none
     // a capped score of a product z, times log2 e: up to |z| = cap_small the series
-    // z (scale_log2 + cap_c3 z^2 + cap_c5 z^4 + cap_c7 z^6), beyond cap_log2 (1 - 2 / (1 + 2^(cap_exp z)));
+    // z (cap_c1 + cap_c3 z^2 + cap_c5 z^4), beyond cap_log2 (1 - 2 / (1 + 2^(cap_exp z)));
     // cap_log2 = 0: no cap
-    float cap_log2, cap_exp, cap_small, cap_c3, cap_c5, cap_c7;
+    float cap_log2, cap_exp, cap_small, cap_c1, cap_c3, cap_c5;
 };
 struct AttendPlan;
 size_t attend_workspace(int64_t D, const AttendPlan& p);
