@@ -160,29 +160,26 @@ constexpr bool kCodes = TYPE != kBf16Rows;
 template <int TYPE>
 constexpr int kScaleShift = TYPE == kInt8Rows ? 4 : 0;       // rows that share a scale
 
-// 16 bytes of codes -> 16 bfloat16 values (exact: 4 bits of E4M3, 7 of INT8)
+// 4 codes -> 4 bfloat16 values (exact: 4 bits of E4M3, 7 of INT8)
+template <int TYPE>
+__device__ __forceinline__ uint2 codes4_to_bf16(uint32_t c) {
+    if constexpr (TYPE == kInt8Rows) {
+        const int w = (int)c;
+        return make_uint2(bf16_pair((float)(int8_t)w, (float)(int8_t)(w >> 8)),
+                          bf16_pair((float)(int8_t)(w >> 16), (float)(w >> 24)));
+    } else {
+        const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, false);
+        const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, true);
+        return make_uint2(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b));
+    }
+}
 template <int TYPE>
 __device__ __forceinline__ void codes_to_bf16(const u32x4_t c, u32x4_t& lo, u32x4_t& hi) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if constexpr (TYPE == kInt8Rows) {
-            const int w = (int)c[i];
-            const uint32_t ua = bf16_pair((float)(int8_t)w, (float)(int8_t)(w >> 8));
-            const uint32_t ub = bf16_pair((float)(int8_t)(w >> 16), (float)(w >> 24));
-            (i < 2 ? lo : hi)[2 * (i & 1)] = ua;
-            (i < 2 ? lo : hi)[2 * (i & 1) + 1] = ub;
-            continue;
-        }
-        const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], 1.0f, false);
-        const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], 1.0f, true);
-        const uint32_t ua = __builtin_bit_cast(uint32_t, a), ub = __builtin_bit_cast(uint32_t, b);
-        if (i < 2) {
-            lo[2 * i] = ua;
-            lo[2 * i + 1] = ub;
-        } else {
-            hi[2 * (i - 2)] = ua;
-            hi[2 * (i - 2) + 1] = ub;
-        }
+        const uint2 v = codes4_to_bf16<TYPE>(c[i]);
+        (i < 2 ? lo : hi)[2 * (i & 1)] = v.x;
+        (i < 2 ? lo : hi)[2 * (i & 1) + 1] = v.y;
     }
 }
 
@@ -242,42 +239,59 @@ __device__ __forceinline__ void clear_rows(Rows<D>& s) {
 }
 
 // A step of attend_wide takes 64 keys in three parts.  The products read their left operands from LDS,
-// which answers after about 130 cycles; a product takes 32.  The operands of four products are read
-// while the four before them are in the matrix unit, and held to that order: left alone the compiler
-// reads two to eight ahead, by what registers seem free (a chunk of 2048 + 1889 tokens: 737 us when it
-// read eight ahead, 790 with two).
+// which answers after about 130 cycles and hands the four waves that ask at once 128 bytes a cycle: a group of four
+// products takes 128 cycles, the reads of one as many behind that answer.  So operands are read two groups ahead, those
+// of the scores from within the accumulation, and held to that order: left alone the compiler reads two to eight products
+// ahead, by what registers seem free.  (XXX)
 __device__ __forceinline__ void hold_order() { __builtin_amdgcn_sched_barrier(0); }
 
-// scores: z = K q for the staged keys kt.
+template <int... I, typename F>
+__device__ __forceinline__ void each(std::integer_sequence<int, I...>, F f) {
+    (f(std::integral_constant<int, I>()), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(F f) { each(std::make_integer_sequence<int, N>(), f); }
+
+// What the products are interleaved with: beside(k) behind product k of a part, or nothing.
+struct Alone {};
+template <typename Beside, typename K>
+__device__ __forceinline__ void beside_product(Beside& beside, K k) {
+    if constexpr (!std::is_same<Beside, Alone>::value) {
+        hold_order();
+        beside(k);
+        hold_order();
+    }
+}
+
+// The operands of four products of the scores: group g of the staged keys kt.
 template <int D>
-__device__ __forceinline__ void scores(const Rows<D>& s, const uint8_t* kt, f32x16_t (&z)[2]) {
-    constexpr int kGroups = D / 32;
+__device__ __forceinline__ void read_keys(const uint8_t* kt, int g, u32x4_t (&a)[4]) {
     const int lane = threadIdx.x & 63, half = lane >> 5, l32 = lane & 31;
-    auto operand = [&](int d, int b) {
-        return *reinterpret_cast<const u32x4_t*>(kt + k_place<D>(32 * b + l32, 2 * d + half));
-    };
-    auto multiply = [&](u32x4_t a, int d, int b) {
-        z[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
-                                                       __builtin_bit_cast(bf16x8_t, s.q[d]), z[b], 0, 0, 0);
-    };
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        a[j] = *reinterpret_cast<const u32x4_t*>(kt + k_place<D>(32 * (j % 2) + l32, 2 * (2 * g + j / 2) + half));
+}
+
+// scores: z = K q for the staged keys kt, whose first two groups are in a.
+template <int D, typename Beside>
+__device__ __forceinline__ void scores(const Rows<D>& s, const uint8_t* kt, f32x16_t (&z)[2], u32x4_t (&a)[3][4], Beside beside) {
+    constexpr int kGroups = D / 32;
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int r = 0; r < 16; ++r) z[b][r] = 0.0f;
-    u32x4_t a[2][4];
-#pragma unroll
-    for (int g = 0; g <= kGroups; ++g) {
-        if (g < kGroups) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) a[g & 1][j] = operand(2 * g + j / 2, j % 2);
-        }
+    each<kGroups>([&](auto group) {
+        constexpr int g = decltype(group)::value;
+        if constexpr (g + 2 < kGroups) read_keys<D>(kt, g + 2, a[(g + 2) % 3]);
         hold_order();
-        if (g > 0) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) multiply(a[(g - 1) & 1][j], 2 * (g - 1) + j / 2, j % 2);
-        }
+        each<4>([&](auto product) {
+            constexpr int j = decltype(product)::value, d = 2 * g + j / 2, b = j % 2;
+            z[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a[g % 3][j]),
+                                                           __builtin_bit_cast(bf16x8_t, s.q[d]), z[b], 0, 0, 0);
+            beside_product(beside, std::integral_constant<int, 4 * g + j>());
+        });
         hold_order();
-    }
+    });
 }
 
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
@@ -436,9 +450,9 @@ __device__ __forceinline__ void weights(Rows<D>& s, f32x16_t (&z)[2], uint32_t (
     }
 }
 
-// accumulate: O += V p for the staged values vt.
-template <int D>
-__device__ __forceinline__ void accumulate(Rows<D>& s, const uint8_t* vt, const uint32_t (&p)[16]) {
+// accumulate: O += V p for the staged values vt; ahead(0) and ahead(1) read the first operands of what follows.
+template <int D, typename Beside, typename Ahead>
+__device__ __forceinline__ void accumulate(Rows<D>& s, const uint8_t* vt, const uint32_t (&p)[16], Beside beside, Ahead ahead) {
     constexpr int kBlocks = D / 32, kSteps = 4 / kBlocks;    // blocks of columns; steps of 16 keys in a group
     constexpr int kGroups = 4 / kSteps;
     const int lane = threadIdx.x & 63, half = lane >> 5, i16 = lane & 15, g16 = (lane >> 4) & 1;
@@ -449,25 +463,29 @@ __device__ __forceinline__ void accumulate(Rows<D>& s, const uint8_t* vt, const 
         const uint64_t a1 = read_tr(vt + v_place<D>(r0 + 8, chunk) + off);
         return u32x4_t{(uint32_t)a0, (uint32_t)(a0 >> 32), (uint32_t)a1, (uint32_t)(a1 >> 32)};
     };
-    auto multiply = [&](u32x4_t a, int c, int i) {
-        const u32x4_t pb = {p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]};
-        s.o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
-                                                         __builtin_bit_cast(bf16x8_t, pb), s.o[i], 0, 0, 0);
+    u32x4_t a[3][4];
+    auto read = [&](int g) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a[g % 3][j] = operand(g * kSteps + j / kBlocks, j % kBlocks);
     };
-    u32x4_t a[2][4];
-#pragma unroll
-    for (int g = 0; g <= kGroups; ++g) {
-        if (g < kGroups) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) a[g & 1][j] = operand(g * kSteps + j / kBlocks, j % kBlocks);
-        }
+    read(0);
+    read(1);
+    each<kGroups>([&](auto group) {
+        constexpr int g = decltype(group)::value;
+        if constexpr (g + 2 < kGroups)
+            read(g + 2);
+        else
+            ahead(std::integral_constant<int, g + 2 - kGroups>());
         hold_order();
-        if (g > 0) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) multiply(a[(g - 1) & 1][j], (g - 1) * kSteps + j / kBlocks, j % kBlocks);
-        }
+        each<4>([&](auto product) {
+            constexpr int j = decltype(product)::value, c = g * kSteps + j / kBlocks, i = j % kBlocks;
+            const u32x4_t pb = {p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]};
+            s.o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a[g % 3][j]),
+                                                             __builtin_bit_cast(bf16x8_t, pb), s.o[i], 0, 0, 0);
+            beside_product(beside, std::integral_constant<int, 4 * g + j>());
+        });
         hold_order();
-    }
+    });
 }
 
 // The running state of attend_narrow's 16 N query rows: lane % 16 is the row of each 16, lane / 16 picks a
@@ -1022,20 +1040,39 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, uint32_t index,
     u32x4_t kw, vw;
     float sc = 1.0f, sc_v = 1.0f;
     bool no_v = false;                                       // INT8: the values staged next have a scale of 0
+    auto bring_scales = [&]() {
+        if constexpr (TYPE == kInt8Rows) {                   // the rows of a wave's load lie in one block
+            sc = rows.ks[off[0] / kRowBytes >> 4];
+            sc_v = rows.vs[off[0] / kRowBytes >> 4];
+        } else {
+            sc = (chunk & 1 ? rows.vs : rows.ks)[off[0] / kRowBytes + crow16];
+        }
+    };
+    // of a tile in place `at` whose rows from `end` on are past the part
+    auto put_scales = [&](int at, int end) {
+        if constexpr (TYPE == kInt8Rows) {
+            // A scale of 0: any that is not 0 for the keys, whose scores then are 0 as well (2^-100 times a score,
+            // should a cache made elsewhere hold codes under it), 1 for the values, whose codes are staged as zeros.
+            no_v = sc_v == 0.0f;
+            if (crow16 == 0 && chunk == 0) {
+                const bool in = crow < end;
+                const float lv = in && !no_v ? __builtin_amdgcn_logf(sc_v) : 0.0f;
+                float* to = &sc_lds[0][at][crow >> 4];
+                to[0] = !in ? 1.0f : sc == 0.0f ? 0x1p-100f : sc;
+                to[4] = lv;
+                to[8] = exp2_fast(-lv);
+            }
+        } else if (chunk < 2) {
+            sc_lds[chunk][at][crow] = crow < end ? sc : 1.0f;
+        }
+    };
     auto bring = [&](int i, bool values) {
         const uint8_t* from = values ? rows.v : rows.k;
         const uint32_t lane_byte = values ? lane_v : lane_k;
         if constexpr (CODES) {
             static_assert(!CODES || kLoads == 1, "one row a thread");
             (values ? vw : kw) = load16(from, off[0], lane_byte);
-            if (!values) {
-                if constexpr (TYPE == kInt8Rows) {           // the rows of a wave's load lie in one block
-                    sc = rows.ks[off[0] / kRowBytes >> 4];
-                    sc_v = rows.vs[off[0] / kRowBytes >> 4];
-                } else {
-                    sc = (chunk & 1 ? rows.vs : rows.ks)[off[0] / kRowBytes + crow16];
-                }
-            }
+            if (!values) bring_scales();
         } else {
             const uint32_t lds = (values ? lds_v : lds_k) + (i % kWideStages) * kTileBytes;
             if (left(i) >= kKeyTile) {
@@ -1062,21 +1099,7 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, uint32_t index,
             stage<D, TYPE, true>(vt[at], crow, chunk, vw, left(i));
         } else {
             stage<D, TYPE, false>(kt[at], crow, chunk, kw, left(i));
-            if constexpr (TYPE == kInt8Rows) {
-                // A scale of 0: any that is not 0 for the keys, whose scores then are 0 as well (2^-100 times a score,
-                // should a cache made elsewhere hold codes under it), 1 for the values, whose codes are staged as zeros.
-                no_v = sc_v == 0.0f;
-                if (crow16 == 0 && chunk == 0) {
-                    const bool in = crow < left(i);
-                    const float lv = in && !no_v ? __builtin_amdgcn_logf(sc_v) : 0.0f;
-                    float* to = &sc_lds[0][at][crow >> 4];
-                    to[0] = !in ? 1.0f : sc == 0.0f ? 0x1p-100f : sc;
-                    to[4] = lv;
-                    to[8] = exp2_fast(-lv);
-                }
-            } else if (chunk < 2) {
-                sc_lds[chunk][at][crow] = crow < left(i) ? sc : 1.0f;
-            }
+            put_scales(at, left(i));
         }
     };
     // Waits for this wave's LDS accesses and then for the other waves; loads of the cache stay in
@@ -1102,12 +1125,11 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, uint32_t index,
     //     waves 0-3    A(i)          B(i)          A(i+1)
     //     waves 4-7    B(i-1)        A(i)          B(i)
     // "Pair n", V(n) and K(n+1), is read in phases 2n+1 and 2n+2; LDS has four places for either.
-    // Each wave brings its share of pair n at the end of its A: of a bfloat16 cache at A(n-2) of waves
-    // 0-3 and A(n-3) of waves 4-7, phases 2n-4 and 2n-5, two pairs ahead of the one that has landed
-    // by the end of that phase; its place was pair n-4's, read last in phase 2n-6.  E4M3 rows are one
-    // pair ahead in registers and staged in phases 2n (A(n)) and 2n-1 (A(n-1)).  Row scales come with
-    // the keys of their tile: those of tile i are staged in phase 2i-2 at the latest, read in A(i), and
-    // written over by those of tile i+4 in phase 2i+5 at the earliest.
+    // A B(i) also takes care of its wave's share of the pairs to come: pair i+1 lands or is staged by the end of it, in
+    // phase 2n-1 for waves 0-3 and 2n for waves 4-7; of a bfloat16 cache pair i+3 goes on its way, whose place was
+    // pair i-1's, read last in phase 2(i-1)+2, one phase ahead of the B(i) of waves 0-3.  E4M3 and INT8 rows are one
+    // pair ahead in registers.  Row scales come with the keys of their tile: those of tile i are staged by phase 2i-2,
+    // read in A(i), the last one in phase 2i+1, and written over by those of tile i+4 in phase 2i+5 at the earliest.
     constexpr int kAhead = CODES ? 1 : 2;                    // pairs in flight
     const int behind = wave >> 2;                            // 1 for waves 4-7
     uint32_t sc_lane = lds_address(&sc_lds[0][0][0]) + (TYPE == kInt8Rows ? 0 : 16 * (lane >> 5));
@@ -1136,19 +1158,78 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, uint32_t index,
             }
         }
         if (!CODES && tiles < 2) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        look_up(kAhead + 2);
     }
     meet();
-    if (seen(0)) scores<D>(s, kt[0], z);
+    if (seen(0)) {
+        u32x4_t keys[3][4];
+        read_keys<D>(kt[0], 0, keys[0]);
+        read_keys<D>(kt[0], 1, keys[1]);
+        scores<D>(s, kt[0], z, keys, Alone());
+    }
     if (behind) meet();
+    // What a B does beside its products, in pieces of a few instructions: pair n = i + 1 is staged, the values of
+    // pair n + kAhead and the keys of tile n + kAhead + 1 are brought, the next tile's entries looked up.
+    constexpr int kSlots = D / 4;                            // products of a B
+    constexpr int kPieces = CODES ? 13 : 4 * kLoads + 1;
+    u32x4_t widened;
+    auto piece = [&](auto number, auto place, int i) {
+        constexpr int P = decltype(number)::value, S = decltype(place)::value;
+        const int n = i + 1;
+        if constexpr (!CODES) {
+            constexpr int c = P % kLoads;
+            constexpr int NV = (S + 1 + kAhead) % kWideStages, NK = (S + 2 + kAhead) % kWideStages;
+            if constexpr (P < kLoads) {
+                load_lds16(rows.v + off[c], lane_v, lds_v + NV * kTileBytes + c * (kStepRows * 2 * D));
+            } else if constexpr (P < 2 * kLoads) {
+                off[c] = rows.offset(entry[c], k0 + (n + kAhead + 1) * kKeyTile + granule + c * kStepRows);
+            } else if constexpr (P < 3 * kLoads) {
+                load_lds16(rows.k + off[c], lane_k, lds_k + NK * kTileBytes + c * (kStepRows * 2 * D));
+            } else if constexpr (P < 4 * kLoads) {
+                entry[c] = rows.entry(k0 + (n + kAhead + 2) * kKeyTile + granule + c * kStepRows);
+            } else {                                         // pair n has landed; n + 1 and n + 2 may stay in flight
+                asm volatile("s_waitcnt vmcnt(%0)" ::"n"(4 * kLoads) : "memory");
+            }
+        } else if constexpr (P == 10) {
+            off[0] = rows.offset(entry[0], k0 + (n + 2) * kKeyTile + granule);
+        } else if constexpr (P == 12) {
+            entry[0] = rows.entry(k0 + (n + 3) * kKeyTile + granule);
+        } else if (loads) {
+            if constexpr (P == 4) {
+                vw = load16(rows.v, off[0], lane_v);
+            } else if constexpr (P < 9) {                    // 8 codes in two pieces: of V(n), of K(n + 1)
+                constexpr bool VALUES = P < 4;
+                constexpr int q = VALUES ? P : P - 5, c = q / 2;
+                uint2 v = codes4_to_bf16<TYPE>((VALUES ? vw : kw)[q]);
+                if (VALUES && TYPE == kInt8Rows && no_v) v = make_uint2(0, 0);
+                widened[2 * (q % 2)] = v.x;
+                widened[2 * (q % 2) + 1] = v.y;
+                if constexpr (q % 2 == 1) {
+                    uint8_t* tile = VALUES ? vt[(S + 1) % kWideStages] : kt[(S + 2) % kWideStages];
+                    *reinterpret_cast<u32x4_t*>(tile + (VALUES ? v_place<D>(crow, 2 * chunk + c) : k_place<D>(crow, 2 * chunk + c))) = widened;
+                }
+            } else if constexpr (P == 9) {
+                put_scales((S + 2) % kWideStages, kKeyTile);
+            } else if constexpr (P == 11) {
+                kw = load16(rows.k, off[0], lane_k);
+                bring_scales();
+            }
+        }
+    };
     // One step, tile i in place S = i % kWideStages.
     auto step = [&](auto place, int i) {
         constexpr int S = decltype(place)::value;
-        const int n = i + behind;
-        look_up(n + kAhead + 1);
+        const int n = i + 1;
         if (seen(i))
             weights<D, TYPE, MOD>(s, z, pw, sc_lane + 4 * S * kKeyTile, sc_lane + 4 * (kWideStages + S) * kKeyTile, a,
                                   k0 + i * kKeyTile, p.lo, p.count, bias, i < whole_lo || i > whole_hi);
-        if (n >= 1 && n < tiles) {
+        else
+#pragma unroll
+            for (int c = 0; c < 16; ++c) pw[c] = 0;
+        meet();
+        __builtin_amdgcn_s_setprio(1);
+        const bool both = left(n + kAhead + 1) >= kKeyTile;
+        if (!both && n < tiles) {
             if constexpr (CODES) {
                 put(n, true);
                 if (n + 1 < tiles) put(n + 1, false);
@@ -1162,11 +1243,22 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, uint32_t index,
                 locate(n + kAhead + 1);
                 bring(n + kAhead + 1, false);
             }
+            look_up(n + kAhead + 2);
         }
-        meet();
-        __builtin_amdgcn_s_setprio(1);
-        if (seen(i)) accumulate<D>(s, vt[S], pw);
-        if (seen(i + 1)) scores<D>(s, kt[(S + 1) % kWideStages], z);
+        auto beside = [&](auto first) {
+            return [&](auto slot) {
+                constexpr int at = decltype(first)::value + decltype(slot)::value;
+                constexpr int from = at * kPieces / kSlots, to = (at + 1) * kPieces / kSlots;
+                if constexpr (from < to) {
+                    if (both) piece(std::integral_constant<int, from>(), place, i);
+                }
+            };
+        };
+        static_assert(kPieces <= kSlots, "a piece a product");
+        u32x4_t keys[3][4];
+        auto ahead = [&](auto g) { read_keys<D>(kt[(S + 1) % kWideStages], decltype(g)::value, keys[decltype(g)::value]); };
+        accumulate<D>(s, vt[S], pw, beside(std::integral_constant<int, 0>()), ahead);
+        scores<D>(s, kt[(S + 1) % kWideStages], z, keys, beside(std::integral_constant<int, kSlots / 2>()));
         __builtin_amdgcn_s_setprio(0);
         meet();
     };
