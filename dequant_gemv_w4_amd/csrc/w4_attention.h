@@ -500,11 +500,11 @@ struct Few {
     Bias bias[N];
 };
 
-// A step of attend_narrow: the 32 staged keys from position `first` on.  sc: LDS address of the keys' row
-// scales from row 4 (lane / 16) on, the values' 32 floats on; mask: whether the step reaches outside some
-// row's keys.
-template <int D, int TYPE, int MOD, int N>
-__device__ __forceinline__ void step_narrow(Few<D, N>& s, const uint8_t* kt, const uint8_t* vt, uint32_t sc,
+// A step of attend_narrow: the 32 keys from position `first` on.  key(b, d): the left operand of 16 keys b and of
+// 32 elements d; scored(): what follows the last of them; vt: the staged values.  sc: LDS address of the keys' row
+// scales from row 4 (lane / 16) on, the values' 32 floats on; mask: whether the step reaches outside some row's.
+template <int D, int TYPE, int MOD, int N, typename Key, typename Scored>
+__device__ __forceinline__ void step_narrow(Few<D, N>& s, Key key, Scored scored, const uint8_t* vt, uint32_t sc,
                                             const AttendArgs& a, int first, bool mask) {
     const int lane = threadIdx.x & 63, i16 = lane & 15, quarter = lane >> 4;
     const float scale = kShaped<MOD> ? 1.0f : a.scale_log2;
@@ -517,12 +517,13 @@ __device__ __forceinline__ void step_narrow(Few<D, N>& s, const uint8_t* kt, con
     for (int d = 0; d < D / 32; ++d)
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            const u32x4_t k = *reinterpret_cast<const u32x4_t*>(kt + k_place<D>(16 * b + i16, 4 * d + quarter));
+            const u32x4_t k = key(b, d);
 #pragma unroll
             for (int n = 0; n < N; ++n)
                 z[n][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, k),
                                                                   __builtin_bit_cast(bf16x8_t, s.q[n][d]), z[n][b], 0, 0, 0);
         }
+    scored();
     if constexpr (kCodes<TYPE>) {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
@@ -1318,6 +1319,10 @@ __device__ __forceinline__ void attend_narrow(const AttendArgs& a, uint32_t inde
     constexpr int kStepRows = 64 / kChunks;                  // rows that one load of the wave covers
     constexpr int kLoads = kKeys / kStepRows;
     constexpr int kTileBytes = kKeys * 2 * D;
+    // INT8 keys go from memory into the registers that the products read them from: lane % 16 is the key, and which
+    // elements stand at which place of the inner dimension is free, so that lane / 16 takes 16 neighbours of each 64.
+    // Through LDS the step would be bound by its instructions and their waits (XXX).
+    constexpr bool DIRECT = TYPE == kInt8Rows;
     static_assert(kNarrowWaves * kTileBytes <= sizeof(lds.k) && kTileBytes >= 16 * D * 4 && N <= 2,
                   "a tile a wave, and at the end its O in the place of the keys and, of rows past 16, the values");
     auto& scales = lds.rest.narrow.scales;
@@ -1333,7 +1338,13 @@ __device__ __forceinline__ void attend_narrow(const AttendArgs& a, uint32_t inde
 #pragma unroll
     for (int n = 0; n < N; ++n) {
         const Place p = row_place<MOD>(a, t, kv, t.row0 + 16 * n + i16);
-        load_q(a.q + (int64_t)p.row * D + 8 * quarter, s.q[n], 32);
+        if constexpr (DIRECT) {
+#pragma unroll
+            for (int d = 0; d < D / 32; ++d)
+                s.q[n][d] = *reinterpret_cast<const u32x4_t*>(a.q + (int64_t)p.row * D + 64 * (d / 2) + 16 * quarter + 8 * (d % 2));
+        } else {
+            load_q(a.q + (int64_t)p.row * D + 8 * quarter, s.q[n], 32);
+        }
         s.lo[n] = p.lo;
         s.count[n] = p.count;
         s.bias[n] = row_bias<MOD>(a, t, kv, t.row0 + 16 * n + i16);
@@ -1359,6 +1370,7 @@ __device__ __forceinline__ void attend_narrow(const AttendArgs& a, uint32_t inde
     Rows16<kRowBytes, kScaleShift<TYPE>> rows(a, __builtin_amdgcn_readfirstlane(t.b), __builtin_amdgcn_readfirstlane(kv), k1);
     int entry[2];                                            // table entries of the next tile
     u32x4_t kw[kLoads], vw[kLoads];
+    uint64_t k_off[2];
     float sc = 1.0f;
     auto look_up = [&](int i, int* e) {                      // read here, used a tile later
 #pragma unroll
@@ -1371,19 +1383,29 @@ __device__ __forceinline__ void attend_narrow(const AttendArgs& a, uint32_t inde
 #pragma unroll
         for (int c = 0; c < kLoads; ++c) {
             const uint64_t from = off[(c * kStepRows) >> 4] + (c * kStepRows & 15) * kRowBytes;
-            kw[c] = load16(rows.k, from, lane_byte);
+            if constexpr (!DIRECT) kw[c] = load16(rows.k, from, lane_byte);
             vw[c] = load16(rows.v, from, lane_byte);
         }
         if constexpr (CODES) {
             const uint64_t at = ((lane & 16 ? off[1] : off[0]) / kRowBytes + (lane & 15)) >> kScaleShift<TYPE>;
             sc = (lane < 32 ? rows.ks : rows.vs)[at];
         }
+        if constexpr (DIRECT) {
+            k_off[0] = off[0];
+            k_off[1] = off[1];
+        }
+    };
+    auto fetch_keys = [&]() {                                // DIRECT: of the tile that fetch was last called for
+#pragma unroll
+        for (int c = 0; c < kLoads; ++c)
+            kw[c] = load16(rows.k, k_off[c / (kLoads / 2)], i16 * kRowBytes + 64 * (c % (kLoads / 2)) + 16 * quarter);
     };
     const uint32_t sc_lane = lds_address(scales[wave]) + 16 * quarter;
     const int tiles = (k1 - k0 + kKeys - 1) / kKeys;
     if (wave < tiles) {
         look_up(wave, entry);
         fetch(wave);
+        if constexpr (DIRECT) fetch_keys();
         look_up(wave + kNarrowWaves, entry);
     }
 #pragma unroll
@@ -1401,17 +1423,32 @@ __device__ __forceinline__ void attend_narrow(const AttendArgs& a, uint32_t inde
 #pragma unroll
         for (int c = 0; c < kLoads; ++c) {
             const int row = c * kStepRows + crow;
-            stage<D, TYPE, false>(kt, row, chunk, kw[c], k1 - first);
+            if constexpr (!DIRECT) stage<D, TYPE, false>(kt, row, chunk, kw[c], k1 - first);
             stage<D, TYPE, true>(vt, row, chunk, vw[c], k1 - first);
         }
         if constexpr (CODES) scales[wave][lane] = first + (lane & 31) < k1 ? sc : 1.0f;
-        if (i + kNarrowWaves < tiles) {
+        const bool more = i + kNarrowWaves < tiles;
+        if (more) {
             fetch(i + kNarrowWaves);
             entry[0] = later[0];
             entry[1] = later[1];
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // rows staged by other lanes
-        step_narrow<D, TYPE, MOD, N>(s, kt, vt, sc_lane, a, first, first < all_lo || first + kKeys - 1 > all_hi);
+        auto key = [&](int b, int d) {
+            if constexpr (DIRECT) {
+                const u32x4_t w = kw[b * (kLoads / 2) + d / 2];
+                const uint2 lo = codes4_to_bf16<TYPE>(w[2 * (d % 2)]), hi = codes4_to_bf16<TYPE>(w[2 * (d % 2) + 1]);
+                return u32x4_t{lo.x, lo.y, hi.x, hi.y};
+            } else {
+                return *reinterpret_cast<const u32x4_t*>(kt + k_place<D>(16 * b + i16, 4 * d + quarter));
+            }
+        };
+        auto scored = [&]() {
+            if constexpr (DIRECT) {
+                if (more) fetch_keys();
+            }
+        };
+        step_narrow<D, TYPE, MOD, N>(s, key, scored, vt, sc_lane, a, first, first < all_lo || first + kKeys - 1 > all_hi);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // read before the next rows land
     }
 
