@@ -279,53 +279,80 @@ __global__ __launch_bounds__(kThreads) void write_blocks_kernel(RopeArgs a, Writ
 // Rows read back
 // --------------------------------------------------------------------------
 //
-// Bound by memory: a lane reads 8 elements and writes 8, four of them in flight.
+// Bound by memory, if the address of an element costs few instructions: a thread keeps to one place of a token's row, 16
+// bytes of it in the output, and goes through tokens, four of them on their way.  Where a wave's 64 places are of one
+// token (WHOLE) what depends on the slot is formed once for all in scalar registers.  65,536 tokens of 8 INT8 heads of
+// 128 take 77 us as bfloat16 rows (403 MB, 5.2 TB/s); with a place found again for each 8 elements 101.  The stores are
+// non-temporal: 87 us otherwise.
 
-template <int TYPE, bool F32>
-__global__ __launch_bounds__(kThreads) void cache_read_kernel(ReadArgs a) {
-    const int chunks = 2 * a.kv_heads * (a.head_dim >> 3);   // of a token
-    const int64_t total = a.n * chunks;
-    const int64_t end = a.pages << a.page_shift;
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
-        const int64_t t = i / chunks;
-        const int c = (int)(i - t * chunks);
-        const int64_t slot = a.slots[t];
-        if (slot < 0) continue;                              // padding
-        if (slot >= end) {
-            if (c == 0 && a.status) atomicOr(a.status, kStatusPage);
+constexpr int kReadTokens = 4;
+
+template <int TYPE, bool F32, bool WHOLE>
+__global__ __launch_bounds__(kThreads) void cache_read_kernel(ReadArgs a, int places_shift) {
+    constexpr int E = F32 ? 4 : 8;                           // elements of a place
+    typedef uint32_t raw_t __attribute__((ext_vector_type(TYPE == 0 ? E / 2 : E / 4 < 2 ? 2 : E / 4)));
+    const int places = 2 * a.kv_heads * a.head_dim / E;      // of a token, here at most 1 << places_shift of them
+    const int place = ((int)blockIdx.y << places_shift) + ((int)threadIdx.x & ((1 << places_shift) - 1));
+    const int beside = kThreads >> places_shift;             // tokens at once
+    const int head_shift = (a.head_dim == 128 ? 7 : 6) - (F32 ? 2 : 3);   // places of a head
+    const bool is_v = (place >> head_shift) >= a.kv_heads, real = place < places;
+    const int kvh = (place >> head_shift) - (is_v ? a.kv_heads : 0), at = E * (place & ((1 << head_shift) - 1));
+    const int64_t head_row = (int64_t)kvh << a.page_shift;
+    const uint8_t* from = static_cast<const uint8_t*>(is_v ? a.v : a.k) + (head_row * a.head_dim + at) * (TYPE == 0 ? 2 : 1);
+    const float* scales = (is_v ? a.v_scales : a.k_scales) + (TYPE == 2 ? head_row >> 4 : head_row);
+    const uint32_t page_rows = (uint32_t)a.kv_heads << a.page_shift;   // at most 2^22
+    const int64_t t0 = (int64_t)blockIdx.x * (beside * kReadTokens), end = a.pages << a.page_shift;
+    raw_t w[kReadTokens];
+    float s[kReadTokens];
+    int64_t slot[kReadTokens], t[kReadTokens];
+#pragma unroll
+    for (int q = 0; q < kReadTokens; ++q) {
+        const int first = (int)(threadIdx.x >> places_shift) + q * beside;
+        t[q] = t0 + (WHOLE ? __builtin_amdgcn_readfirstlane(first) : first);
+        const int64_t known = t[q] < a.n ? t[q] : a.n - 1;
+        if constexpr (WHOLE)                                 // through the scalar cache
+            slot[q] = ((__attribute__((address_space(4))) const int64_t*)(uintptr_t)a.slots)[known];
+        else
+            slot[q] = a.slots[known];
+        if (t[q] >= a.n) slot[q] = -1;
+    }
+#pragma unroll
+    for (int q = 0; q < kReadTokens; ++q) {
+        // rows that are left out (negative, or past the cache) read the cache's first one
+        const int64_t here = slot[q] >= 0 && slot[q] < end ? slot[q] : 0;
+        const uint64_t row = (uint64_t)(uint32_t)(here >> a.page_shift) * page_rows + (uint32_t)(here & ((1 << a.page_shift) - 1));
+        if (!real) continue;
+        const uint8_t* p = from + row * (a.head_dim * (TYPE == 0 ? 2 : 1));
+        if constexpr (TYPE != 0 && F32)
+            w[q][0] = *reinterpret_cast<const uint32_t*>(p);
+        else
+            w[q] = *reinterpret_cast<const raw_t*>(p);
+        if constexpr (TYPE != 0) s[q] = scales[TYPE == 2 ? row >> 4 : row];
+    }
+#pragma unroll
+    for (int q = 0; q < kReadTokens; ++q) {
+        if (slot[q] >= end && place == 0 && a.status) atomicOr(a.status, kStatusPage);
+        if (slot[q] < 0 || slot[q] >= end || !real) continue;
+        u32x4_t* to = static_cast<u32x4_t*>(a.out) + (t[q] * places + place);
+        if constexpr (TYPE == 0 && !F32) {
+            __builtin_nontemporal_store(w[q], to);
             continue;
         }
-        const int head = c / (a.head_dim >> 3), at = 8 * (c - head * (a.head_dim >> 3));
-        const bool is_v = head >= a.kv_heads;
-        const int64_t row = (((slot >> a.page_shift) * a.kv_heads + head - (is_v ? a.kv_heads : 0)) << a.page_shift) +
-                            (slot & ((1 << a.page_shift) - 1));
-        const void* from = is_v ? a.v : a.k;
-        const float* scales = is_v ? a.v_scales : a.k_scales;
-        float v[8];
+        float v[E];
         if constexpr (TYPE == 0) {
-            load8<true>(from, row * a.head_dim + at, v);
-        } else {
-            const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(from) + row * a.head_dim + at);
-            const float s = scales[TYPE == 2 ? row >> 4 : row];
-            if constexpr (TYPE == 2) {
-                values_of8(w, v);
-            } else {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    v[q] = __builtin_amdgcn_cvt_f32_fp8(w.x >> (8 * q), 0);
-                    v[4 + q] = __builtin_amdgcn_cvt_f32_fp8(w.y >> (8 * q), 0);
-                }
+            for (int e = 0; e < E; ++e) v[e] = __uint_as_float(e % 2 ? w[q][e / 2] & 0xFFFF0000u : w[q][e / 2] << 16);
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const uint32_t c = w[q][e / 4] >> (8 * (e % 4));
+                v[e] = s[q] * (TYPE == 2 ? (float)(int8_t)c : __builtin_amdgcn_cvt_f32_fp8(c, 0));
             }
-#pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] *= s;
         }
-        if constexpr (F32) {
-            float* to = static_cast<float*>(a.out) + i * 8;
-            *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<float4*>(to + 4) = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
-            *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(a.out) + i * 8) = bf16_of8(v);
-        }
+        if constexpr (F32)
+            __builtin_nontemporal_store(u32x4_t{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])}, to);
+        else
+            __builtin_nontemporal_store(bf16_of8(v), to);
     }
 }
 
@@ -354,20 +381,24 @@ hipError_t launch_write_blocks(const RopeArgs& a, bool x_f32, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <int TYPE>
-static hipError_t launch_read_type(const ReadArgs& a, bool out_f32, hipStream_t s) {
-    const int64_t chunks = a.n * 2 * a.kv_heads * (a.head_dim / 8);
-    const dim3 grid((unsigned)imin(ceil_div(chunks, kThreads), 1 << 20)), block(kThreads);
-    if (out_f32)
-        hipLaunchKernelGGL((cache_read_kernel<TYPE, true>), grid, block, 0, s, a);
+template <int TYPE, bool F32>
+static hipError_t launch_read_type(const ReadArgs& a, hipStream_t s) {
+    const int places = 2 * a.kv_heads * a.head_dim / (F32 ? 4 : 8);   // 16 at least
+    int shift = 4;
+    while ((1 << shift) < places && (1 << shift) < kThreads) ++shift;
+    const int64_t tokens = (kThreads >> shift) * kReadTokens;
+    const dim3 grid((unsigned)ceil_div(a.n, tokens), (unsigned)ceil_div(places, 1 << shift)), block(kThreads);
+    if (shift >= 6)
+        hipLaunchKernelGGL((cache_read_kernel<TYPE, F32, true>), grid, block, 0, s, a, shift);
     else
-        hipLaunchKernelGGL((cache_read_kernel<TYPE, false>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((cache_read_kernel<TYPE, F32, false>), grid, block, 0, s, a, shift);
     return hipGetLastError();
 }
 
 hipError_t launch_cache_read(const ReadArgs& a, int type, bool out_f32, hipStream_t s) {
-    if (type == 0) return launch_read_type<0>(a, out_f32, s);
-    return type == 1 ? launch_read_type<1>(a, out_f32, s) : launch_read_type<2>(a, out_f32, s);
+    if (type == 0) return out_f32 ? launch_read_type<0, true>(a, s) : launch_read_type<0, false>(a, s);
+    if (type == 1) return out_f32 ? launch_read_type<1, true>(a, s) : launch_read_type<1, false>(a, s);
+    return out_f32 ? launch_read_type<2, true>(a, s) : launch_read_type<2, false>(a, s);
 }
 
 }  // namespace w4
