@@ -136,12 +136,14 @@ class DecoderStep:
     grows by n and ``lens[b]`` becomes 0; the next request may then use its place.
     A step of another size over the same requests (a captured one for single tokens beside one for
     prompts) is made with ``state``, the step whose caches, lengths, pages, table and status it shares.
+    ``rope`` None leaves positions to ``scores``: a W4Scores for all layers, or one (or None) for each, with its
+    ``first_keys`` [tokens] and ``prefix_lens`` [seqs], which the caller writes between steps like ``new_lens``.
     ``tokens`` = ``seqs`` suits single tokens; a step that takes prompts should have another number of
     tokens, since the attention takes T = B for one token a request and is slower where it is not.
     """
 
     def __init__(self, layers, caches, heads, rope, final_norm, tokens, seqs, max_pages, eps=1e-5, free_pages=None,
-                 state=None):
+                 state=None, scores=None):
         import torch
         if not layers or len(layers) != len(caches):
             raise ValueError("one cache per layer")
@@ -149,6 +151,13 @@ class DecoderStep:
         if any((x.pages, x.page_size, x.kv_heads, x.head_dim) != (c.pages, c.page_size, c.kv_heads, c.head_dim) for x in caches):
             raise ValueError("the caches of all layers have one geometry")
         self.layers, self.caches, self.heads, self.rope, self.eps = layers, caches, heads, rope, eps
+        self.scores = list(scores) if isinstance(scores, (list, tuple)) else [scores] * len(layers)
+        if len(self.scores) != len(layers):
+            raise ValueError("one record of scores per layer")
+        for r in self.scores:
+            for t, n in (() if r is None else ((r.slopes, heads), (r.first_keys, tokens), (r.prefix_lens, seqs))):
+                if t is not None and tuple(t.shape) != (n,):
+                    raise ValueError("scores of other heads, tokens or requests")
         self.final_norm, self.tokens, self.page_size = final_norm, tokens, c.page_size
         dev, hidden = c.device, layers[0].qkv.k
         self._device = dev
@@ -160,7 +169,7 @@ class DecoderStep:
                 raise ValueError("inconsistent layer shapes")
         i32, bf16 = dict(dtype=torch.int32, device=dev), dict(dtype=torch.bfloat16, device=dev)
         self.scale = c.head_dim ** -0.5
-        self.freqs, _ = w4_rope_frequencies(rope, dev)
+        self.freqs = None if rope is None else w4_rope_frequencies(rope, dev)[0]
         self.residual, self.hidden = torch.zeros(tokens, hidden, **bf16), torch.zeros(tokens, hidden, **bf16)
         self.new_lens = torch.zeros(seqs, **i32)
         if state is not None:
@@ -190,7 +199,7 @@ class DecoderStep:
         gemm = max([w4_gemm_workspace_bytes(tokens, p.n, p.k) for p in products if p.kind == "w4" and tokens > 16], default=0)
         self._gemm_workspace = torch.zeros(max(gemm, 16), dtype=torch.uint8, device=dev)
         from . import w4_paged_attention_workspace_bytes
-        need = w4_paged_attention_workspace_bytes(tokens, heads, c, seqs, max_pages)
+        need = max(w4_paged_attention_workspace_bytes(tokens, heads, x, seqs, max_pages) for x in caches)
         self._attend_workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=dev)
         self._graph = None
 
@@ -237,22 +246,29 @@ class DecoderStep:
 
     def _step(self) -> None:
         import torch
-        from . import w4_block_tables, w4_paged_attention, w4_rmsnorm, w4_rope_cache
+        from . import w4_block_tables, w4_cache_write, w4_paged_attention, w4_paged_attention_scores, w4_rmsnorm, w4_rope_cache
         w4_block_tables(self.new_lens, self.lens, self.free_pages, self.free_count, self.block_table, self.page_size,
                         cu_q=self.cu_q, positions=self.positions, slots=self.slots, status=self.status)
         # Rows without a slot: the cache write and the attention leave them out, the products and norms do not.
         torch.lt(self.slots.view(-1, 1), 0, out=self._idle)
         self.residual.masked_fill_(self._idle, 0)
         self._qo.masked_fill_(self._idle.view(-1, 1, 1), 0)
-        for i, (a, cache) in enumerate(zip(self.layers, self.caches)):
+        for i, (a, cache, scores) in enumerate(zip(self.layers, self.caches, self.scores)):
             if i == 0:
                 x = self._norm(a.qkv, self.residual, a.attn_norm, None)
             else:
                 x = self._norm(a.qkv, self._y, a.attn_norm, self.residual)
             self._product(a.qkv, x, self._qkv)
-            w4_rope_cache(self._qkv, cache, self.positions, self.slots, self.rope, self.freqs, q=self._q, status=self.status)
-            w4_paged_attention(self._q, cache, self.block_table, self.cu_q, self.lens, self.scale, o=self._o,
-                               workspace=self._attend_workspace, status=self.status)
+            if self.rope is None:
+                w4_cache_write(self._qkv, cache, self.slots, q=self._q, status=self.status)
+            else:
+                w4_rope_cache(self._qkv, cache, self.positions, self.slots, self.rope, self.freqs, q=self._q, status=self.status)
+            attend = (self._q, cache, self.block_table, self.cu_q, self.lens, self.scale)
+            out = dict(o=self._o, workspace=self._attend_workspace, status=self.status)
+            if scores is None:
+                w4_paged_attention(*attend, **out)
+            else:
+                w4_paged_attention_scores(*attend, scores, **out)
             self._product(a.o, self._rows(a.o, self._o.view(self.tokens, -1)), self._y)
             x = self._norm(a.gate_up, self._y, a.mlp_norm, self.residual)
             self._product(a.gate_up, x, self._gate_up[a.down.k])
@@ -265,6 +281,8 @@ class DecoderStep:
         import torch
         with torch.cuda.device(self._device):
             kept = [t.clone() for t in self._state()]
+            if any(c.k.dtype == torch.int8 for c in self.caches):
+                self.new_lens.zero_()         # tokens written twice could make a block's step coarser than once
             self.run_eager()                  # warm caches and the device check outside capture
             torch.cuda.synchronize()
             g = torch.cuda.CUDAGraph()
@@ -277,7 +295,7 @@ class DecoderStep:
         self._graph = g
 
     def _state(self):
-        return self.lens, self.free_count, self.block_table, self.status, self.residual
+        return self.lens, self.free_count, self.block_table, self.status, self.residual, self.new_lens
 
     def run(self) -> None:
         if self._graph is not None:
