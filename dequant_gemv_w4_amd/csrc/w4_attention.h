@@ -1,7 +1,9 @@
 // Attention of new tokens over the paged cache:
 //     o = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale * q.k_j - max),
-// over the keys that a query sees, in one pass with the running maximum and sum of the softmax.
-// The index arithmetic (tiles, parts, pages) is in w4_paging.h.
+// over the keys that a query sees, in one pass with the running maximum and sum of the softmax; the scores as they are,
+// capped by a tanh or with a bias by distance (MOD, below).
+// The index arithmetic (tiles, parts, pages, the keys of a row) is in w4_paging.h.  The sources that include this one
+// instantiate the kernels for a type of cache and the kinds of scores each.
 //
 // Both kernels multiply on the matrix cores with the keys as rows and the query rows as columns
 // (32x32x16 in attend_wide, 16x16x32 in attend_narrow): S^T = K Q^T leaves each lane one query row and
@@ -17,17 +19,21 @@
 // the bfloat16 output, and averaged over the keys: outputs are 1.4 times as far from 64 bits as an
 // unrounded P would leave them).  attend_narrow, which waits for memory, multiplies V by what that
 // rounding leaves as well (P = p + rest, both bfloat16, together within 2^-16): a decode step of 32
-// requests takes 153.0 us instead of 152.3.  E4M3 codes enter as exact bfloat16 values; the scale of a
-// key's row multiplies its scores, that of a value's row its P, both in binary32.
+// requests takes 153.0 us instead of 152.3.  E4M3 and INT8 codes enter as exact bfloat16 values; the scale of a
+// key's row or block multiplies its scores, that of a value's its P, in binary32.
 //
 // attend_wide: 256 rows a workgroup, 8 waves of 32 rows; tiles of 64 keys pass through LDS for
 // all of them, the next tiles' loads in flight, and the two waves of a SIMD take turns on the matrix
 // unit.  Bound by the matrix unit and LDS together: two chunks of up to 2048 tokens over up to 6144
-// cached (64 heads, 8 kv heads, 0.79 Tflop) take 722 to 763 us on different cards, 1.03 to 1.09 PFLOP/s
-// where a large bfloat16 product of the vendor's library reaches 1.37; the matrix unit is busy for 51 % of
-// the cycles, and the products without their LDS reads take 0.55 of the time.  64 rows a wave would halve
-// those reads, with 512 registers and one wave a SIMD, which then has none to take turns with; half of
+// cached (64 heads, 8 kv heads, 0.79 Tflop) take 721 to 772 us on different cards, 1.02 to 1.09 PFLOP/s
+// where a large bfloat16 product of the vendor's library reaches 1.37 to 1.59; the matrix unit is busy for 50 % of
+// the cycles.  The products alone take 547 us, with the loads beside them 600, and the softmax alone 415 (one
+// thing or the other left out, the rest as it is).  64 rows a wave would halve
+// the LDS reads, with 512 registers and one wave a SIMD, which then has none to take turns with; half of
 // those registers are out of the vector unit's reach, and the compiler moves 256 values a step for that.
+// Over an E4M3 cache the same chunks take 800 to 850 us, over INT8 790 to 834, capped 843 to 895, with a bias 789 to 840:
+// what is more is vector work, 48 conversions a wave and step for INT8 codes (745 us without them), and two to five
+// operations for each of 2048 scores.
 // attend_narrow: 16 rows or 32, for single tokens: the waves take 32-key tiles in turn, each with its own
 // piece of LDS, and join their sums at the end.  (Products of 32 rows for 8 rows, twice the registers and
 // matrix work: 157.0 us instead of 152.9 for single tokens of 32 requests over up to 8192 cached, 86.2
@@ -36,7 +42,9 @@
 // bound by latency: one request over 1000 keys (16 MB) takes 11.2 us, 8.3 of them one chain of lengths,
 // table entries, rows, products and the waves' join, and 3 the launch that joins the parts.  Code that
 // the chain runs once is paid at the rate at which instructions arrive (600 more cost 1.5 us: two tiles
-// of loads in flight instead of one, in a loop unrolled by two, were dropped for that).
+// of loads in flight instead of one, in a loop unrolled by two, were dropped for that).  8-bit rows are half the
+// bytes and as many instructions, and neither two tiles in flight nor two workgroups on a compute unit nor more
+// parts make them faster: the same 32 requests' 427 MB of INT8 take 85 to 87 us (5.0 TB/s).
 // Either may split the keys of a tile over several workgroups, which then leave (m, l, O / l) in
 // the workspace for combine_kernel.
 //
@@ -242,7 +250,8 @@ __device__ __forceinline__ void clear_rows(Rows<D>& s) {
 // which answers after about 130 cycles and hands the four waves that ask at once 128 bytes a cycle: a group of four
 // products takes 128 cycles, the reads of one as many behind that answer.  So operands are read two groups ahead, those
 // of the scores from within the accumulation, and held to that order: left alone the compiler reads two to eight products
-// ahead, by what registers seem free.  (XXX)
+// ahead, by what registers seem free.  (One group ahead: chunks of 2048 tokens over 6144 768 us instead of 741, over an
+// INT8 cache 857 instead of 805.)
 __device__ __forceinline__ void hold_order() { __builtin_amdgcn_sched_barrier(0); }
 
 template <int... I, typename F>
@@ -1032,7 +1041,7 @@ __device__ __forceinline__ void attend_wide(const AttendArgs& a, uint32_t index,
     // meet a weight of zero.
     auto left = [&](int i) { return k1 - k0 - i * kKeyTile; };
 
-    // A bfloat16 tile goes straight into LDS: a lane loads the chunk whose place it is.  An E4M3 tile
+    // A bfloat16 tile goes straight into LDS: a lane loads the chunk whose place it is.  A tile of codes
     // passes through registers (kw, vw), where its codes are widened.
     const int crow16 = crow & 15;
     const uint32_t lane_k = crow16 * kRowBytes + (CODES ? 16 * chunk : k_place<D>(crow, chunk) - crow * 2 * D);
@@ -1321,7 +1330,8 @@ __device__ __forceinline__ void attend_narrow(const AttendArgs& a, uint32_t inde
     constexpr int kTileBytes = kKeys * 2 * D;
     // INT8 keys go from memory into the registers that the products read them from: lane % 16 is the key, and which
     // elements stand at which place of the inner dimension is free, so that lane / 16 takes 16 neighbours of each 64.
-    // Through LDS the step would be bound by its instructions and their waits (XXX).
+    // Through LDS, 32
+    // requests over up to 8192 keys take 93 us instead of 85.
     constexpr bool DIRECT = TYPE == kInt8Rows;
     static_assert(kNarrowWaves * kTileBytes <= sizeof(lds.k) && kTileBytes >= 16 * D * 4 && N <= 2,
                   "a tile a wave, and at the end its O in the place of the keys and, of rows past 16, the values");

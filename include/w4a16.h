@@ -541,7 +541,7 @@ w4_status w4_block_tables(const int32_t* new_lens, const int32_t* lens_in, int64
  * reach the row, NaN and infinities included.
  * Scores, softmax sums and outputs are formed in binary32 and o is rounded once.  V is multiplied by
  * weights held in two bfloat16 parts (2^-16) for every request where T = B or all rows together
- * (T times heads / kv_heads) are at most 32, else for requests of at most 32 rows, 64 with an E4M3
+ * (T times heads / kv_heads) are at most 32, else for requests of at most 32 rows, 64 with an 8-bit
  * cache or where 2 * B * kv_heads <= 256; for the others by weights rounded to bfloat16 (2^-8).  A
  * request's last bits may so depend on the batch that it is in.
  * T = B is taken for one token a request: any lengths give right results, but a long prompt there
