@@ -378,6 +378,11 @@ class W4Scores:
         self._c = _ScoresStruct(cap, 0, _opt(slopes), _opt(first_keys), _opt(prefix_lens))
         self._ref = ctypes.byref(self._c)
 
+    def __setattr__(self, name, value):
+        if "_ref" in self.__dict__:                           # its record would still name the old ones
+            raise AttributeError("a W4Scores keeps what it was made with: write into its tensors or make another")
+        super().__setattr__(name, value)
+
 
 def w4_paged_attention_scores(q, cache: W4KVCache, block_table, cu_q, lens, scale, scores: W4Scores, window=0, o=None,
                               workspace=None, status=None):

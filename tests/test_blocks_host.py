@@ -118,6 +118,15 @@ def test_python_layer_rejects_cpu_tensors():
         w4.W4Scores(first_keys=[0, 1])
 
 
+def test_scores_keep_what_they_were_made_with():
+    pytest.importorskip("torch")
+    r = w4.W4Scores(cap=30.0)
+    for name, value in (("cap", 50.0), ("slopes", None), ("first_keys", None), ("prefix_lens", None)):
+        with pytest.raises(AttributeError):
+            setattr(r, name, value)
+    assert r.cap == 30.0 and r._c.cap == 30.0
+
+
 PROGRAM = r"""
 #include <cstdio>
 #include <climits>
