@@ -44,7 +44,8 @@
 // the chain runs once is paid at the rate at which instructions arrive (600 more cost 1.5 us: two tiles
 // of loads in flight instead of one, in a loop unrolled by two, were dropped for that).  8-bit rows are half the
 // bytes and as many instructions, and neither two tiles in flight nor two workgroups on a compute unit nor more
-// parts make them faster: the same 32 requests' 427 MB of INT8 take 85 to 87 us (5.0 TB/s).
+// parts make them faster: the same 32 requests' 427 MB of INT8 take 83 to 88 us (5.0 TB/s), 79 where all are as long:
+// 256 tiles are not split, so the longest request ends last.
 // Either may split the keys of a tile over several workgroups, which then leave (m, l, O / l) in
 // the workspace for combine_kernel.
 //
