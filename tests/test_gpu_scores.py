@@ -108,6 +108,25 @@ def test_caps_over_the_range(cap):
             b.check(b.run(scores=w4.W4Scores(cap=cap)), 0, f"cap {cap} {qscale}", cap=cap)
 
 
+@pytest.mark.parametrize("cap", [30.0, 88.0, 89.0])
+@pytest.mark.parametrize("kind,d", [("bf16", 128), ("bf16", 64), ("int8", 128)])
+def test_capped_scores_far_below_zero(cap, kind, d):
+    # every key against the query, at not quite a quarter of the cap, and one along it that only the last token sees
+    for new, cached in (([300], [200]), ([300], [2500]), ([1], [900])):
+        b = Batch(new, cached, 4, 1, d, 16, kind, seed=8)
+        x = float(oracle.bf16_round(np.array([0.24 * cap / (d * b.scale)], np.float32))[0])
+        b.q[:] = -x
+        b.d_q = dev(b.q, BF)
+        last, one = b.ctx[0] - 1, 1.0 if kind == "bf16" else 127.0
+        b.cache.k.fill_(int(one) if kind == "int8" else one)
+        b.cache.k[int(b.table[0, last // 16]), :, last % 16] = -int(one) if kind == "int8" else -one
+        if kind == "int8":
+            b.cache.k_scales.fill_(1.0 / 128)
+        b.keys[0][:] = one if kind == "bf16" else one / 128
+        b.keys[0][:, last] *= -1
+        b.check(b.run(scores=w4.W4Scores(cap=cap)), 0, f"{cap} {kind} {new} {cached}", cap=cap)
+
+
 def test_slopes_negative_large_and_far():
     # a bias that grows with the distance, one that leaves the row's own key alone, and distances past 2^16
     for new, cached in (([1], [70000]), ([40], [300])):
