@@ -96,8 +96,8 @@ struct Bias {
     int pos;
 };
 
-// The capped score c tanh(z / c) log2 e of a product z (z / c = z * cap_in).  Up to a quarter of c by the odd
-// polynomial of degree 5 that meets tanh(y) / y at three Chebyshev nodes in y^2, within 2^-21 of the score (its last
+// The capped score c tanh(z / c) log2 e of a product z (z / c = z * cap_in).  Up to 0.28 c by the odd
+// polynomial of degree 5 that meets tanh(y) / y at three Chebyshev nodes in y^2, within 2^-20 of the score (its last
 // coefficient is positive, so that it takes a masked product, -inf, to -inf); beyond, c (1 - 2 / (1 + exp(2 z / c))), off by
 // about 2^-22 c, so 2^-20 of the score: near zero that difference would lose the score.
 __device__ __forceinline__ float cap_factor(const AttendArgs& a, float z) {
@@ -397,8 +397,8 @@ __device__ __forceinline__ void weights(Rows<D>& s, f32x16_t (&z)[2], uint32_t (
         }
         mx = half_max(mx);
     } else {
-        // Capped scores below a quarter of a cap of at most 88 are within 32 of 0 in powers of two, so that the largest
-        // magnitude, which is there, does for the maximum: the largest weight is then at least 2^-64.  Chunks of the
+        // Capped scores below 0.28 of a cap of at most 88 are within 36 of 0 in powers of two, so that the largest
+        // magnitude, which is there, does for the maximum: the largest weight is then at least 2^-72.  Chunks of the
         // bfloat16 cache above 857 -> 841 us; not with a head dimension of 64 (699 -> 703), E4M3 rows (prompts of 333
         // tokens 23.7 -> 24.9) or INT8 blocks, whose scale is in the weight.
         if (CAP_ONLY && TYPE == kBf16Rows && D == 128 && !large && a.cap_log2 <= 128.0f) {
