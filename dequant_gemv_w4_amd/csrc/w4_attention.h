@@ -31,7 +31,7 @@
 // thing or the other left out, the rest as it is).  64 rows a wave would halve
 // the LDS reads, with 512 registers and one wave a SIMD, which then has none to take turns with; half of
 // those registers are out of the vector unit's reach, and the compiler moves 256 values a step for that.
-// Over an E4M3 cache the same chunks take 800 to 850 us, over INT8 790 to 834, capped 843 to 895, with a bias 789 to 840:
+// Over an E4M3 cache the same chunks take 800 to 850 us, over INT8 790 to 834, capped 813 to 820, with a bias 789 to 840:
 // what is more is vector work, 48 conversions a wave and step for INT8 codes (745 us without them), and two to five
 // operations for each of 2048 scores.
 // attend_narrow: 16 rows or 32, for single tokens: the waves take 32-key tiles in turn, each with its own
