@@ -397,11 +397,13 @@ __device__ __forceinline__ void weights(Rows<D>& s, f32x16_t (&z)[2], uint32_t (
         }
         mx = half_max(mx);
     } else {
-        // Capped scores below 0.28 of a cap of at most 88 are within 36 of 0 in powers of two, so that the largest
-        // magnitude, which is there, does for the maximum: the largest weight is then at least 2^-72.  Chunks of the
+        // Capped scores below 0.28 of a cap of at most 88 are within 36 of 0 in powers of two, so that where every row
+        // sees all keys of the step the largest magnitude, which is there, does for the maximum: the row's largest weight
+        // is then at least 2^-72.  (Not where a mask is: a row that sees nothing of the step would begin with a maximum that
+        // none of its own scores need be near.)  Chunks of the
         // bfloat16 cache above 857 -> 841 us; not with a head dimension of 64 (699 -> 703), E4M3 rows (prompts of 333
         // tokens 23.7 -> 24.9) or INT8 blocks, whose scale is in the weight.
-        if (CAP_ONLY && TYPE == kBf16Rows && D == 128 && !large && a.cap_log2 <= 128.0f) {
+        if (CAP_ONLY && TYPE == kBf16Rows && D == 128 && !large && !mask && a.cap_log2 <= 128.0f) {
             mx = most;
         } else {
             mx = z[0][0];
