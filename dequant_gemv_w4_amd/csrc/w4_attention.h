@@ -96,10 +96,10 @@ struct Bias {
     int pos;
 };
 
-// The capped score c tanh(z / c) log2 e of a product z (z / c = z * cap_in).  Up to 0.28 c by the odd
+// The capped score c tanh(z / c) log2 e of a product z.  Up to |z| = 0.28 c (cap_small, in units of z) by the odd
 // polynomial of degree 5 that meets tanh(y) / y at three Chebyshev nodes in y^2, within 2^-20 of the score (its last
 // coefficient is positive, so that it takes a masked product, -inf, to -inf); beyond, c (1 - 2 / (1 + exp(2 z / c))), off by
-// about 2^-22 c, so 2^-20 of the score: near zero that difference would lose the score.
+// 2^-21 c at most, so 2^-19 of the score: near zero that difference would lose the score.
 __device__ __forceinline__ float cap_factor(const AttendArgs& a, float z) {
     const float w = z * z;
     return fmaf(w, fmaf(w, a.cap_c5, a.cap_c3), a.cap_c1);
@@ -110,9 +110,34 @@ __device__ __forceinline__ float cap_large(const AttendArgs& a, float z) {
     return fmaf(-2.0f * a.cap_log2, __builtin_amdgcn_rcpf(e + 1.0f), a.cap_log2);
 }
 
-// Products z of one query row with NB * NR keys, key first + at(b, r), to scores times log2 e.  Which form of
-// the cap is taken goes by the largest product of the wave's step.
-template <int MOD, int NB, int NR, typename V, typename At>
+__device__ __forceinline__ float cap_score(const AttendArgs& a, float z) {
+    const float few = cap_small(a, z), many = cap_large(a, z);   // both: a branch would cost more
+    return fabsf(z) > a.cap_small ? many : few;
+}
+
+// The scores of a step that holds products past cap_small.  WIDE, where weights are rounded to 2^-8: under a cap of up
+// to 1024 all by the form for those, which is off by 2^-11 then at most (two chunks of up to 2048 over up to 6144, products of
+// deviation 12 under a cap of 50: 957 us, 1209 with both forms).  Else each by its own, whatever others of the step need: under a
+// cap of 60,000 the small scores beside large ones were off by 0.01.  Single tokens wait for memory in either case.
+constexpr float kNearCap = 1024 * kLog2e;
+template <bool WIDE, int NB, int NR, typename V>
+__device__ __forceinline__ void cap_scores(const AttendArgs& a, V (&z)[NB]) {
+    if (WIDE && a.cap_log2 <= kNearCap) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int r = 0; r < NR; ++r) z[b][r] = cap_large(a, z[b][r]);
+    } else {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int r = 0; r < NR; ++r) z[b][r] = cap_score(a, z[b][r]);
+    }
+}
+
+// Products z of one query row with NB * NR keys, key first + at(b, r), to scores times log2 e.  Which forms of
+// the cap are taken goes by the largest product of the wave's step.
+template <int MOD, bool WIDE, int NB, int NR, typename V, typename At>
 __device__ __forceinline__ void shape_scores(const AttendArgs& a, V (&z)[NB], Bias bias, int first, At at) {
     if constexpr (MOD & kCap) {
         float most = 0.0f;
@@ -121,10 +146,7 @@ __device__ __forceinline__ void shape_scores(const AttendArgs& a, V (&z)[NB], Bi
 #pragma unroll
             for (int r = 0; r < NR; ++r) most = fmaxf(most, fabsf(z[b][r]));
         if (__any(most > a.cap_small)) {
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int r = 0; r < NR; ++r) z[b][r] = cap_large(a, z[b][r]);
+            cap_scores<WIDE, NB, NR>(a, z);
         } else {
 #pragma unroll
             for (int b = 0; b < NB; ++b)
@@ -156,7 +178,7 @@ __device__ __forceinline__ void shape_scores(const AttendArgs& a, V (&z)[NB], Bi
 template <int MOD>
 __device__ __forceinline__ float shape_score(const AttendArgs& a, float z, Bias bias, int key) {
     float s = z * a.scale_log2;
-    if constexpr (MOD & kCap) s = fabsf(z) > a.cap_small ? cap_large(a, z) : cap_small(a, z);
+    if constexpr (MOD & kCap) s = cap_score(a, z);
     if constexpr (MOD & kBias) s = fmaf(-bias.slope, fabsf((float)(key - bias.pos)), s);
     return s;
 }
@@ -368,14 +390,9 @@ __device__ __forceinline__ void weights(Rows<D>& s, f32x16_t (&z)[2], uint32_t (
 #pragma unroll
             for (int r = 0; r < 16; ++r) most = fmaxf(most, fabsf(z[b][r]));
         large = __any(most > a.cap_small);
-        if (large) {
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) z[b][r] = cap_large(a, z[b][r]);
-        }
+        if (large) cap_scores<true, 2, 16>(a, z);
     } else if constexpr (kShaped<MOD>) {
-        shape_scores<MOD, 2, 16>(a, z, bias, first + 4 * half, [](int b, int r) { return 32 * b + 8 * (r >> 2) + (r & 3); });
+        shape_scores<MOD, true, 2, 16>(a, z, bias, first + 4 * half, [](int b, int r) { return 32 * b + 8 * (r >> 2) + (r & 3); });
     }
     if (mask) {
         const uint32_t from = (uint32_t)(first + 4 * half - lo);
@@ -557,7 +574,7 @@ __device__ __forceinline__ void step_narrow(Few<D, N>& s, Key key, Scored scored
     if constexpr (kShaped<MOD>) {
 #pragma unroll
         for (int n = 0; n < N; ++n)
-            shape_scores<MOD, 2, 4>(a, z[n], s.bias[n], first + 4 * quarter, [](int b, int r) { return 16 * b + r; });
+            shape_scores<MOD, false, 2, 4>(a, z[n], s.bias[n], first + 4 * quarter, [](int b, int r) { return 16 * b + r; });
     }
     if (mask) {
 #pragma unroll

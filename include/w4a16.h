@@ -576,8 +576,8 @@ w4_status w4_paged_attention(const void* q, int64_t T, int64_t heads, const w4_k
  *                (W4_ERR_UNSUPPORTED).
  * Other arguments, workspace, limits, precision and what is read and written as w4_paged_attention; no page
  * is looked up that lies wholly ahead of what the rows of a tile see (up to 256 rows of a request), or behind
- * it.  Distances are held in binary32 (exact up to 2^24); capped scores are within 2^-19 of the largest
- * score's size.
+ * it.  Distances are held in binary32 (exact up to 2^24).  A capped score is within 2^-19 of its own size, or, with
+ * a cap of up to 1024 and where weights are rounded to bfloat16, within 2^-21 of the cap.
  */
 typedef struct {
     float cap;

@@ -7,7 +7,8 @@ import pytest
 
 import dequant_gemv_w4_amd as w4
 import oracle
-from _batch import BF, Batch, dev
+from _batch import BF, U32, UB, Batch, dev
+from _util import to_np32
 
 pytestmark = pytest.mark.gpu
 
@@ -64,3 +65,51 @@ def test_scores_at_the_end_of_the_polynomial(cap, sign):
         for new, cached in (([300], [200]), ([70], [2500]), ([1], [900])):
             b = _flat(cap, new, cached, 128, lambda j: np.where(j % 7 == 3, -sign * of, sign * of))
             b.check(b.run(scores=_scores(cap)), 0, f"{cap} {sign} {of} {new}", cap=cap)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("heads", [4, 12])
+@pytest.mark.parametrize("slopes", [False, True])
+def test_small_scores_beside_large_ones(slopes, heads, kind):
+    # One head's scores reach a cap of 60000 and more, the others' are of size 1 in the same tile.  Tolerance as in
+    # _batch.Batch.check, with the size of each row's own products and weights in two bfloat16 parts (2^-16): single tokens.
+    cap = 60000.0
+    d, s = 128, (2.0 ** -np.arange(3, 3 + heads)).astype(np.float32) if slopes else None
+    b = Batch([1] * 4, [5, 30, 40, 90], heads, 1, d, 16, kind, seed=6, qscale=1.0)
+    b.q[:, 1] *= 2.0 ** 17
+    b.d_q = dev(b.q, BF)
+    got = to_np32(b.run(scores=_scores(cap, s))).astype(np.float64)
+    for i, ctx in enumerate(b.ctx):
+        ref, w = oracle.attention_scores_ref(b.q[i: i + 1], b.keys[i], b.values[i], ctx, b.scale, cap=cap, slopes=s)
+        size = b.scale * np.abs(b.q[i]).sum(-1) * np.abs(b.keys[i]).max()       # [heads]
+        bias = 0.0 if s is None else s * ctx
+        score = (d + 4) * U32 * size + 2.0 ** -19 * size + 4 * U32 * (size + bias)
+        tol = (2.0 ** -16 + 2 * (score[:, None] + (4 + ctx / 8) * U32)) * w[0] + UB * np.abs(ref[0])
+        off = np.abs(got[i] - ref[0])
+        worst = float(np.delete(off - tol, 1, 0).max())
+        assert worst <= 0, (i, worst)
+        assert np.all(np.isfinite(got[i, 1]))
+
+
+@pytest.mark.parametrize("slopes", [False, True])
+def test_small_scores_beside_large_ones_in_chunks(slopes):
+    # Documents of two tokens with values of 1 and -1, so that the difference of their weights is what comes out: a weight
+    # is off by 2^-8 and by its score's error, the sum of both by the scores'.
+    cap, d, n = 90000.0, 128, 300
+    s = np.array([0.125, 0.25, 0.5, 1.0], np.float32) if slopes else None
+    b = Batch([n], [0], 4, 1, d, 16, "bf16", seed=7, qscale=0.1)
+    b.q[:, 1] *= 2.0 ** 22
+    b.d_q = dev(b.q, BF)
+    j = np.arange(n)
+    b.values[0][:] = np.where(j % 2, -1.0, 1.0)[None, :, None]
+    b.cache.v[dev(b.table[0, j // 16].astype(np.int64)), :, dev((j % 16).astype(np.int64))] = dev(b.values[0][0].astype(np.float32), BF)[:, None]
+    first = np.maximum(j - 1, 0).astype(np.int32)
+    got = to_np32(b.run(scores=_scores(cap, s, first=first))).astype(np.float64)
+    ref, w = oracle.attention_scores_ref(b.q, b.keys[0], b.values[0], n, b.scale, cap=cap, slopes=s, first=first)
+    size = b.scale * np.abs(b.q).sum(-1) * np.abs(b.keys[0]).max()
+    bias = 0.0 if s is None else s
+    score = (d + 4) * U32 * size + 2.0 ** -19 * size + 4 * U32 * (size + bias)
+    tol = (UB + 2 * (score[..., None] + 8 * U32)) * w + UB * np.abs(ref)
+    worst = np.delete(np.abs(got - ref) - tol, 1, 1).max()
+    assert worst <= 0, worst
+    assert np.all(np.isfinite(got))
