@@ -97,9 +97,9 @@ struct Bias {
 };
 
 // The capped score c tanh(z / c) log2 e of a product z.  Up to |z| = 0.28 c (cap_small, in units of z) by the odd
-// polynomial of degree 5 that meets tanh(y) / y at three Chebyshev nodes in y^2, within 2^-20 of the score (its last
-// coefficient is positive, so that it takes a masked product, -inf, to -inf); beyond, c (1 - 2 / (1 + exp(2 z / c))), off by
-// 2^-21 c at most, so 2^-19 of the score: near zero that difference would lose the score.
+// polynomial of degree 5 that meets tanh(y) / y at three Chebyshev nodes in y^2, within 2^-20 of the score;
+// beyond, c (1 - 2 / (1 + exp(2 z / c))), off by 2^-21 c at most, so 2^-19 of the score: near zero that difference
+// would lose the score.
 __device__ __forceinline__ float cap_factor(const AttendArgs& a, float z) {
     const float w = z * z;
     return fmaf(w, fmaf(w, a.cap_c5, a.cap_c3), a.cap_c1);
@@ -136,16 +136,17 @@ __device__ __forceinline__ void cap_scores(const AttendArgs& a, V (&z)[NB]) {
 }
 
 // Products z of one query row with NB * NR keys, key first + at(b, r), to scores times log2 e.  Which forms of
-// the cap are taken goes by the largest product of the wave's step.
+// the cap are taken goes by the largest product of the wave's step, or, where it has keys that some row does not see
+// (mask), by nothing: keys that no row sees, old ones behind the last among them, change no bit.
 template <int MOD, bool WIDE, int NB, int NR, typename V, typename At>
-__device__ __forceinline__ void shape_scores(const AttendArgs& a, V (&z)[NB], Bias bias, int first, At at) {
+__device__ __forceinline__ void shape_scores(const AttendArgs& a, V (&z)[NB], Bias bias, int first, bool mask, At at) {
     if constexpr (MOD & kCap) {
         float most = 0.0f;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int r = 0; r < NR; ++r) most = fmaxf(most, fabsf(z[b][r]));
-        if (__any(most > a.cap_small)) {
+        if (mask || __any(most > a.cap_small)) {
             cap_scores<WIDE, NB, NR>(a, z);
         } else {
 #pragma unroll
@@ -382,17 +383,17 @@ __device__ __forceinline__ void weights(Rows<D>& s, f32x16_t (&z)[2], uint32_t (
 #pragma unroll
             for (int r = 0; r < 16; ++r) z[b][r] *= kb[2 * b + r / 8];
     }
-    bool large = false;                                      // CAP_ONLY: z holds scores
+    bool large = false;                                      // CAP_ONLY: z holds scores; else nothing is masked
     float most = 0.0f;
     if constexpr (CAP_ONLY) {
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) most = fmaxf(most, fabsf(z[b][r]));
-        large = __any(most > a.cap_small);
+        large = mask || __any(most > a.cap_small);
         if (large) cap_scores<true, 2, 16>(a, z);
     } else if constexpr (kShaped<MOD>) {
-        shape_scores<MOD, true, 2, 16>(a, z, bias, first + 4 * half, [](int b, int r) { return 32 * b + 8 * (r >> 2) + (r & 3); });
+        shape_scores<MOD, true, 2, 16>(a, z, bias, first + 4 * half, mask, [](int b, int r) { return 32 * b + 8 * (r >> 2) + (r & 3); });
     }
     if (mask) {
         const uint32_t from = (uint32_t)(first + 4 * half - lo);
@@ -415,12 +416,12 @@ __device__ __forceinline__ void weights(Rows<D>& s, f32x16_t (&z)[2], uint32_t (
         mx = half_max(mx);
     } else {
         // Capped scores below 0.28 of a cap of at most 88 are within 36 of 0 in powers of two, so that where every row
-        // sees all keys of the step the largest magnitude, which is there, does for the maximum: the row's largest weight
-        // is then at least 2^-72.  (Not where a mask is: a row that sees nothing of the step would begin with a maximum that
-        // none of its own scores need be near.)  Chunks of the
+        // sees all keys of the step (else it is a large one) the largest magnitude, which is there, does for the maximum: the
+        // row's largest weight is then at least 2^-72.  (A row that sees nothing of the step would begin with a maximum
+        // that none of its own scores need be near.)  Chunks of the
         // bfloat16 cache above 857 -> 841 us; not with a head dimension of 64 (699 -> 703), E4M3 rows (prompts of 333
         // tokens 23.7 -> 24.9) or INT8 blocks, whose scale is in the weight.
-        if (CAP_ONLY && TYPE == kBf16Rows && D == 128 && !large && !mask && a.cap_log2 <= 128.0f) {
+        if (CAP_ONLY && TYPE == kBf16Rows && D == 128 && !large && a.cap_log2 <= 128.0f) {
             mx = most;
         } else {
             mx = z[0][0];
@@ -574,7 +575,7 @@ __device__ __forceinline__ void step_narrow(Few<D, N>& s, Key key, Scored scored
     if constexpr (kShaped<MOD>) {
 #pragma unroll
         for (int n = 0; n < N; ++n)
-            shape_scores<MOD, false, 2, 4>(a, z[n], s.bias[n], first + 4 * quarter, [](int b, int r) { return 16 * b + r; });
+            shape_scores<MOD, false, 2, 4>(a, z[n], s.bias[n], first + 4 * quarter, mask, [](int b, int r) { return 16 * b + r; });
     }
     if (mask) {
 #pragma unroll

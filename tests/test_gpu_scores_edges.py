@@ -4,6 +4,7 @@ binary64 oracle (tolerances: _batch.Batch.check, where no other stands at the te
 
 import numpy as np
 import pytest
+import torch
 
 import dequant_gemv_w4_amd as w4
 import oracle
@@ -113,3 +114,34 @@ def test_small_scores_beside_large_ones_in_chunks(slopes):
     worst = np.delete(np.abs(got - ref) - tol, 1, 1).max()
     assert worst <= 0, worst
     assert np.all(np.isfinite(got))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("new,cached", [([1], [70]), ([1, 1, 1], [70, 600, 3]), ([3, 1], [37, 2]), ([7], [100]), ([40, 150], [37, 100]), ([300], [83])])
+@pytest.mark.parametrize("slopes", [False, True])
+def test_keys_that_no_row_sees_change_no_bit(slopes, new, cached, kind):
+    # ahead of every row's document and behind the last key: zeros there, or products far above 0.28 of the cap
+    given = dict(cap=200.0, slopes=(2.0 ** -np.arange(1, 9)).astype(np.float32) if slopes else None)
+    outs = []
+    for code in (0.0, 112.0):                                 # 112: in bfloat16, INT8; as E4M3 code 0x70, which is 2^7
+        b = Batch(new, cached, 8, 2, 128, 16, kind, seed=4, qscale=2.0)
+        if kind == "int8":
+            b.cache.k_scales.clamp_(min=0.05)
+        first = np.zeros(b.q.shape[0], np.int32)
+        for i, (n, c) in enumerate(zip(new, b.ctx)):
+            at = min(c - n, 37)                               # the first key that the request's rows see
+            first[int(b.cu[i]): int(b.cu[i]) + n] = at
+            held = 16 * (-(-c // 16))                         # of its last page
+            hidden = np.concatenate([np.arange(at), np.arange(c, held)])
+            pg, row = b.table[i, hidden // 16].astype(np.int64), (hidden % 16).astype(np.int64)
+            for x in (b.cache.k, b.cache.v):                  # a code of zero or of the sign of q's elements, key by key
+                x[dev(pg), :, dev(row)] = 0
+            if len(hidden) and code:
+                q = b.q[int(b.cu[i])].reshape(2, 4, 128)[:, 0]                  # along a row's query: scores of 100 at least
+                k = dev(np.sign(q) * code).to(b.cache.k.dtype) if kind != "fp8" else dev(np.where(q < 0, 0xF0, 0x70).astype(np.uint8))
+                b.cache.k[dev(pg), :, dev(row)] = k[None]
+            if kind == "fp8":
+                for s in (b.cache.k_scales, b.cache.v_scales):
+                    s[dev(pg), :, dev(row)] = 1.0
+        outs.append(b.run(scores=_scores(first=first, **given)))
+    assert torch.equal(outs[0], outs[1]), int((outs[0] != outs[1]).sum())
