@@ -90,7 +90,9 @@ template <int MOD>
 constexpr bool kShaped = (MOD & (kBias | kCap)) != 0;
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// Of a query row: its head's slope times log2 e, its position.
+// Of a query row: its head's slope times log2 e, its position.  Slopes past 2^96, where a distance of one leaves no
+// weight to anything else already, count as that: times any distance (below 2^30) they stay numbers.
+constexpr float kMostSlope = 0x1p96f;
 struct Bias {
     float slope;
     int pos;
@@ -855,7 +857,7 @@ __device__ __forceinline__ Bias row_bias(const AttendArgs& a, const Tile& t, int
     Bias b = {0.0f, 0};
     if constexpr (MOD & kBias) {
         const int token = r < t.rows ? quotient(r, a.group) : 0, head = kv * a.group + (r < t.rows ? r - token * a.group : 0);
-        b.slope = a.slopes[head] * kLog2e;
+        b.slope = fminf(fmaxf(a.slopes[head] * kLog2e, -kMostSlope), kMostSlope);
         b.pos = t.seq.ctx - t.seq.n + token;
     }
     return b;

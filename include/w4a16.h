@@ -571,9 +571,9 @@ w4_status w4_paged_attention(const void* q, int64_t T, int64_t heads, const w4_k
  * A row for which hi < lo gets zeros.  Each of the four may be left out (0 or NULL); a record of zeros asks
  * for w4_paged_attention.
  *   cap          0, or scale * 2^-20 <= cap <= scale * 2^20, and then scale <= 256 (else W4_ERR_VALUE).
- *   slopes       [heads] device binary32, finite.   first_keys  [T] device int32, any values.
- *   prefix_lens  [B] device int32, any values (negative: none).   4-B aligned.   reserved  0
- *                (W4_ERR_UNSUPPORTED).
+ *   slopes       [heads] device binary32, finite; one beyond 2^95, of either sign, may count as 2^95.
+ *   first_keys  [T] device int32, any values.   prefix_lens  [B] device int32, any values (negative: none).
+ *   4-B aligned.   reserved  0 (W4_ERR_UNSUPPORTED).
  * Other arguments, workspace, limits, precision and what is read and written as w4_paged_attention; no page
  * is looked up that lies wholly ahead of what the rows of a tile see (up to 256 rows of a request), or behind
  * it.  Distances are held in binary32 (exact up to 2^24).  A capped score is within 2^-19 of its own size, or, with

@@ -145,3 +145,23 @@ def test_keys_that_no_row_sees_change_no_bit(slopes, new, cached, kind):
                     s[dev(pg), :, dev(row)] = 1.0
         outs.append(b.run(scores=_scores(first=first, **given)))
     assert torch.equal(outs[0], outs[1]), int((outs[0] != outs[1]).sum())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8"])
+@pytest.mark.parametrize("slope", [2.0 ** 95, 2.0 ** 100, 1e38, 3.4e38])
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+def test_slopes_at_the_end_of_binary32(cap, slope, kind):
+    # a weight of 1 for the row's own key, or with the sign turned for the farthest
+    for new, cached in (([1], [0]), ([1, 1], [100, 2000]), ([90, 1], [500, 3]), ([70], [2500])):
+        for prefix in (False, True):
+            b = Batch(new, cached, 4, 1, 64, 16, kind, seed=2)
+            s = np.array([slope, -slope, 0.0, slope], np.float32)
+            lens = np.zeros(len(new), np.int32) if prefix else None
+            got = to_np32(b.run(scores=_scores(cap, s, prefix=lens))).astype(np.float64)
+            for i, (n, c) in enumerate(zip(new, b.ctx)):
+                for t in range(n):
+                    row = got[int(b.cu[i]) + t]
+                    for h, j in ((0, c - n + t), (1, 0), (3, c - n + t)):
+                        v = b.values[i][0, j]
+                        assert np.all(np.abs(row[h] - v) <= 2 * UB * np.abs(v) + 2.0 ** -100), (new, prefix, i, t, h, row[h][:4], v[:4])
+                    assert np.all(np.isfinite(row))
