@@ -25,7 +25,7 @@ constexpr int kBlockRows = 16;
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kMaxPairs = 64;   // head_dim 128
 constexpr float kLeastMax = 0x1p-93f;                        // a block below it counts as zeros
-constexpr float kLeastScale = 0x1p-100f;                     // below kLeastMax / 127
+constexpr float kLeastScale = (float)(0x1p-93 / 127.0);      // of those that a write leaves; values below kLeastMax pass 127 of a smaller one
 
 __device__ __forceinline__ uint32_t bf16_pair2(float a, float b) {
     typedef float f2_t __attribute__((ext_vector_type(2)));

@@ -393,7 +393,8 @@ w4_status w4_silu_mul_int8(const void* gate_up, w4_dtype gt, int64_t rows, int64
  * (rows 16 i .. 16 i + 15 of a page) forms, with m the largest magnitude of the values that it writes
  * there (0 below 2^-93),
  *   old = 0 where the block's first row is among those written (the block begins anew, whatever it
- *         held), else the block's scale (0 where that is no finite number of at least 2^-100);
+ *         held), else the block's scale (0 where that is no finite number of at least 2^-93 / 127,
+ *         as binary32);
  *   S = m / 127 in binary64 where that, rounded to binary32, is larger than old, else old;
  *   scale = S in binary32;   code = y / S in binary64, to the nearest whole number, halves to even;
  * where the scale has grown and the block goes on, the codes c of its other rows become c / (S / old),

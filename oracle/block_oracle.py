@@ -7,6 +7,7 @@ from __future__ import annotations
 import numpy as np
 
 BLOCK = 16
+LEAST_SCALE = float(np.float32(2.0 ** -93 / 127))   # of those that a write leaves
 
 
 def write_block_ref(codes, scale, rows):
@@ -23,7 +24,7 @@ def write_block_ref(codes, scale, rows):
     if most < 2.0 ** -93:
         most = 0.0
     old = float(np.float32(scale))
-    if 0 in rows or not np.isfinite(old) or old < 2.0 ** -100:
+    if 0 in rows or not np.isfinite(old) or old < LEAST_SCALE:
         old = 0.0
     step = most / 127
     if float(np.float32(step)) > old:
