@@ -420,10 +420,10 @@ __device__ __forceinline__ void weights(Rows<D>& s, f32x16_t (&z)[2], uint32_t (
         // Capped scores below 0.28 of a cap of at most 88 are within 36 of 0 in powers of two, so that where every row
         // sees all keys of the step (else it is a large one) the largest magnitude, which is there, does for the maximum: the
         // row's largest weight is then at least 2^-72.  (A row that sees nothing of the step would begin with a maximum
-        // that none of its own scores need be near.)  Chunks of the
-        // bfloat16 cache above 857 -> 841 us; not with a head dimension of 64 (699 -> 703), E4M3 rows (prompts of 333
-        // tokens 23.7 -> 24.9) or INT8 blocks, whose scale is in the weight.
-        if (CAP_ONLY && TYPE == kBf16Rows && D == 128 && !large && a.cap_log2 <= 128.0f) {
+        // that none of its own scores need be near.)  Two chunks of up to 2048 over up to 6144, bfloat16 and E4M3: 875 ->
+        // 857 us, 1034 -> 999, with a head dimension of 64 641 -> 630, 938 -> 904; prompts of 333 tokens as before.  Not over
+        // INT8 blocks, whose scale is in the weight.
+        if (CAP_ONLY && TYPE != kInt8Rows && !large && a.cap_log2 <= 128.0f) {
             mx = most;
         } else {
             mx = z[0][0];

@@ -26,46 +26,60 @@ def _set_keys(b, i, j, codes):
     b.cache.k[pg, :, dev((j % b.page).astype(np.int64))] = dev(np.asarray(codes))[:, None, None].to(b.cache.k.dtype)
 
 
-def _flat(cap, new, cached, d, keys, seed=8):
-    """A batch whose products are small = 0.27 cap (rounded) times the values `keys` of the keys."""
-    b = Batch(new, cached, 4, 1, d, 16, "bf16", seed=seed)
+def _flat(cap, new, cached, d, keys, seed=8, kind="bf16"):
+    """A batch whose products are 0.27 cap (rounded) times the values `keys` of the keys (E4M3: of 1, -1 and -16)."""
+    b = Batch(new, cached, 4, 1, d, 16, kind, seed=seed)
     b.q[:] = oracle.bf16_round(np.array([0.27 * cap / (d * b.scale)], np.float32))[0]
     b.d_q = dev(b.q, BF)
     values = keys(np.arange(b.ctx[0]))
-    _set_keys(b, 0, np.arange(b.ctx[0]), values.astype(np.float32))
+    codes = values.astype(np.float32)
+    if kind == "fp8":
+        codes = np.select([values == 1, values == -1, values == -16], [0x38, 0xB8, 0xD8]).astype(np.uint8)
+        b.cache.k_scales.fill_(1.0)
+    _set_keys(b, 0, np.arange(b.ctx[0]), codes)
     b.keys[0][:] = values[None, :, None]
     return b
 
 
 @pytest.mark.parametrize("cap", [50.0, 70.0, 80.0, 88.0])
-@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kind,d", [("bf16", 64), ("bf16", 128), ("fp8", 64), ("fp8", 128)])
 @pytest.mark.parametrize("form", ["causal", "documents", "split", "window"])
-def test_small_products_that_a_row_does_not_see(form, d, cap):
+def test_small_products_that_a_row_does_not_see(form, kind, d, cap):
     # What a row sees scores at minus the cap; beside it in the wave others see keys that score 0.27 of it, in a step that
     # is all masked for the row: 2^(-(1 + 0.26) cap log2 e) between the two is no number for caps above about 69.
     first, window = None, 0
     if form == "causal":                                      # 124 .. 127 see the keys up to 127, 128 .. 131 those behind
-        b = _flat(cap, [300], [100], d, lambda j: np.where(j < 128, -16.0, 1.0))
+        b = _flat(cap, [300], [100], d, lambda j: np.where(j < 128, -16.0, 1.0), kind=kind)
     elif form == "documents":                                 # small keys ahead of every other row's document
-        b = _flat(cap, [300], [100], d, lambda j: np.where(j < 128, 1.0, -16.0))
+        b = _flat(cap, [300], [100], d, lambda j: np.where(j < 128, 1.0, -16.0), kind=kind)
         first = np.where((np.arange(300) % 2 == 1) & (np.arange(300) >= 28), 128, 0).astype(np.int32)
     elif form == "split":                                     # whole parts of them
-        b = _flat(cap, [70], [4000], d, lambda j: np.where(j < 3968, 1.0, -16.0))
+        b = _flat(cap, [70], [4000], d, lambda j: np.where(j < 3968, 1.0, -16.0), kind=kind)
         first = np.where(np.arange(70) % 2 == 1, 3968, 0).astype(np.int32)
     else:                                                     # the same edge where tiles of keys begin at 96
-        b = _flat(cap, [300], [100], d, lambda j: np.where(j < 224, -16.0, 1.0))
+        b = _flat(cap, [300], [100], d, lambda j: np.where(j < 224, -16.0, 1.0), kind=kind)
         window = 64
     b.check(b.run(window, _scores(cap, first=first)), window, f"{form} {cap}", cap=cap, first=first)
 
 
 @pytest.mark.parametrize("cap", [30.0, 88.0, 89.0])
 @pytest.mark.parametrize("sign", [1.0, -1.0])
-def test_scores_at_the_end_of_the_polynomial(cap, sign):
+@pytest.mark.parametrize("kind,d", [("bf16", 128), ("bf16", 64), ("fp8", 128), ("fp8", 64)])
+def test_scores_at_the_end_of_the_polynomial(kind, d, sign, cap):
     # all products of one size, 0.27 of the cap, or beyond it
     for of in (1.0, 1.04, 1.3):
         for new, cached in (([300], [200]), ([70], [2500]), ([1], [900])):
-            b = _flat(cap, new, cached, 128, lambda j: np.where(j % 7 == 3, -sign * of, sign * of))
-            b.check(b.run(scores=_scores(cap)), 0, f"{cap} {sign} {of} {new}", cap=cap)
+            b = _flat(cap * of, new, cached, d, lambda j: np.where(j % 7 == 3, -sign, sign), kind=kind)
+            b.check(b.run(scores=_scores(cap)), 0, f"{kind} {d} {cap} {sign} {of} {new}", cap=cap)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_all_at_minus_the_polynomials_end(d, kind):
+    # the maximum is taken for 36 powers of two above what every key scores
+    for new, cached in (([300], [212]), ([300], [2500]), ([260], [252])):
+        b = _flat(88.0, new, cached, d, lambda j: np.where(j >= 0, -1.0, 1.0), kind=kind)
+        b.check(b.run(scores=_scores(88.0)), 0, f"{kind} {d} {new}", cap=88.0)
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "int8"])
