@@ -31,9 +31,9 @@
 // thing or the other left out, the rest as it is).  64 rows a wave would halve
 // the LDS reads, with 512 registers and one wave a SIMD, which then has none to take turns with; half of
 // those registers are out of the vector unit's reach, and the compiler moves 256 values a step for that.
-// Over an E4M3 cache the same chunks take 800 to 850 us, over INT8 790 to 834, capped 813 to 820, with a bias 789 to 840:
-// what is more is vector work, 48 conversions a wave and step for INT8 codes (745 us without them), and two to five
-// operations for each of 2048 scores.
+// Over an E4M3 cache the same chunks take 800 to 850 us, over INT8 790 to 850, capped 803 to 868 (985 to 1040 where most
+// scores are past 0.28 of the cap), with a bias 785 to 847, with both 988 to 1033: what is more is vector work, 48
+// conversions a wave and step for INT8 codes (745 us without them), and two to five operations for each of 2048 scores.
 // attend_narrow: 16 rows or 32, for single tokens: the waves take 32-key tiles in turn, each with its own
 // piece of LDS, and join their sums at the end.  (Products of 32 rows for 8 rows, twice the registers and
 // matrix work: 157.0 us instead of 152.9 for single tokens of 32 requests over up to 8192 cached, 86.2
@@ -98,7 +98,7 @@ struct Bias {
     int pos;
 };
 
-// The capped score c tanh(z / c) log2 e of a product z.  Up to |z| = 0.28 c (cap_small, in units of z) by the odd
+// The capped score c tanh(z / c) log2 e of a product z (times the scale).  Up to |z| = 0.28 c by the odd
 // polynomial of degree 5 that meets tanh(y) / y at three Chebyshev nodes in y^2, within 2^-20 of the score;
 // beyond, c (1 - 2 / (1 + exp(2 z / c))), off by 2^-21 c at most, so 2^-19 of the score: near zero that difference
 // would lose the score.
@@ -113,8 +113,8 @@ __device__ __forceinline__ float cap_large(const AttendArgs& a, float z) {
 }
 
 __device__ __forceinline__ float cap_score(const AttendArgs& a, float z) {
-    const float few = cap_small(a, z), many = cap_large(a, z);   // both: a branch would cost more
-    return fabsf(z) > a.cap_small ? many : few;
+    const float low = cap_small(a, z), high = cap_large(a, z);   // both: as a branch it costs more
+    return fabsf(z) > a.cap_small ? high : low;
 }
 
 // The scores of a step that holds products past cap_small.  WIDE, where weights are rounded to 2^-8: under a cap of up

@@ -402,8 +402,8 @@ w4_status w4_silu_mul_int8(const void* gate_up, w4_dtype gt, int64_t rows, int64
  * codes that w4_int8_quantize_rows gives the 16 of them as one row, and a value is within half a step
  * (scale / 2) of y; one that its block outgrows g times is within (g + 1) / 2 of the last step.  Values that
  * are not finite get the code 0 and set W4_STATUS_NONFINITE.  The rows of a block that one call writes
- * have to stand next to each other in the batch (as w4_block_tables places them; in any order): apart, or
- * written by two calls at once, they leave the block's codes and scale undefined.
+ * have to stand next to each other in the batch (as w4_block_tables places them; in any order): apart, a slot
+ * named twice, or written by two calls at once, they leave the block's codes and scale undefined.
  */
 #define W4_CACHE_BLOCK 16
 typedef enum { W4_CACHE_BF16 = 0, W4_CACHE_FP8 = 1, W4_CACHE_INT8 = 3 } w4_cache_type;   /* 2: none */
